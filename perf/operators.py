@@ -238,7 +238,7 @@ def _norm_rope_bwd_plain(x, w, g, s):
 
 def _pow2_scale(amax):
     """The smallest power of two s with amax <= 448 s (1/2^60 at least)."""
-    m, e = torch.frexp(amax / E4M3_MAX)
+    m, e = torch.frexp((amax / E4M3_MAX).clamp(min=2.0 ** -60))
     e = torch.where(m == 0.5, e - 1, e).clamp(-60, 60)
     return torch.ldexp(torch.ones_like(amax), e)
 
