@@ -1,6 +1,7 @@
 /*
  * sdpa.h -- C ABI of the GB300 (sm_103a) scaled dot-product attention
- * forward pass.
+ * forward pass, its gradient, and what stands beside it in a language model:
+ * norm and rotation of queries and keys, a paged 8-bit cache.
  *
  * Operation.  Codelab "Attention on GPU (cuDNN and TransformerEngine)",
  * section 1 ("How attention works"):
@@ -50,7 +51,8 @@ extern "C" {
 typedef enum {
     SDPA_DTYPE_BF16 = 0,   /* bfloat16 Q, K, V and O */
     SDPA_DTYPE_FP16 = 1,   /* IEEE binary16 Q, K, V and O */
-    SDPA_DTYPE_E4M3 = 2    /* FP8 E4M3 Q, K, V; bfloat16 O (sdpa_fwd_fp8 only) */
+    SDPA_DTYPE_E4M3 = 2,   /* FP8 E4M3 Q, K, V; bfloat16 O (sdpa_fwd_fp8 only) */
+    SDPA_DTYPE_F32 = 3     /* float32 (weights of sdpa_qk_norm_rope only) */
 } sdpa_dtype_t;
 
 typedef enum {
@@ -280,6 +282,163 @@ size_t sdpa_bwd_fp8_workspace_bytes(int B, int Hq, int Sq, int D);
  */
 size_t sdpa_decode_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Skv, int D);
 
+/*
+ * Rotation of queries and keys by their positions.  `table` is device memory,
+ * fp32 [n_pos][rot_dim / 2][2]: the cosine and sine of the angle of pair i at
+ * each position, 16-byte aligned.  The first rot_dim channels of a head are
+ * rotated (a multiple of 8, at most D), the others stay as they are; a pair
+ * (x, y) becomes (x cos - y sin, x sin + y cos).
+ *   interleaved   0: pair i is channels (i, i + rot_dim / 2);
+ *                 nonzero: channels (2 i, 2 i + 1).
+ * A NULL sdpa_rope_t or a NULL table means no rotation.
+ */
+typedef struct {
+    const float *table;
+    int n_pos;
+    int rot_dim;
+    int interleaved;
+} sdpa_rope_t;
+
+/*
+ * Norm of queries and keys for each head and their rotation, in one pass, in
+ * front of the attention: for every row x of D channels (one head of one
+ * token)
+ *     y = R(position) (x * w / sqrt(mean(x^2) + eps)),
+ * computed in fp32 and rounded once.
+ *   Q, K      device, read only, [B][S][Hq][D] and [B][S][Hkv][D], type
+ *             `dtype` (bf16 or fp16), D 32, 64 or 128.  K is optional: NULL
+ *             with Hkv = 0.
+ *   Q_out, K_out   device, written, shaped and typed like Q and K.  A tensor
+ *             may be written over itself (the same pointer and strides);
+ *             otherwise what is written shares no element with anything else.
+ *             Tensors that lie side by side in the rows of one buffer (a
+ *             fused projection) count as apart.
+ *   *_layout  strides, NULL for contiguous, as for sdpa_fwd_ex.
+ *   norm      0: rotation only (weights and eps are not read).
+ *   q_weight, k_weight   device, [D], type weight_dtype (SDPA_DTYPE_F32 or
+ *             dtype), or NULL for ones.
+ *   rope      host pointer, see sdpa_rope_t.
+ *   positions device, int32 [B][S] contiguous, or NULL: token s stands at
+ *             position s.  A row whose position is outside the table is not
+ *             written, and the device error word becomes 0x701.
+ */
+sdpa_status_t sdpa_qk_norm_rope(const void *Q, const void *K, void *Q_out, void *K_out,
+                                int B, int S, int Hq, int Hkv, int D,
+                                const sdpa_layout_t *q_layout, const sdpa_layout_t *k_layout,
+                                const sdpa_layout_t *q_out_layout, const sdpa_layout_t *k_out_layout,
+                                int norm, const void *q_weight, const void *k_weight,
+                                sdpa_dtype_t weight_dtype, float eps,
+                                const sdpa_rope_t *rope, const int *positions,
+                                sdpa_dtype_t dtype, void *stream);
+
+/*
+ * Gradients of sum(dQ_out * Q_out) + sum(dK_out * K_out) for the outputs of
+ * sdpa_qk_norm_rope(Q, K) with the same arguments: with h = R^T g, x^ the
+ * normalised row and r its factor, dw = sum over rows of h * x^ and
+ * dx = r (h w - x^ mean(h w x^)).
+ *   dQ_out, dK_out  device, read only, upstream gradients, like Q and K.
+ *   dQ, dK    device, written, like Q and K; they share no element with any
+ *             input.
+ *   dq_weight, dk_weight   device, fp32 [D], written, or NULL.  The order of
+ *             the additions depends on the sizes alone.  Not written with
+ *             norm = 0.
+ *   workspace device scratch of sdpa_qk_norm_rope_bwd_workspace_bytes(B, S,
+ *             Hq, Hkv, D) bytes, 16-byte aligned, needing no initialisation,
+ *             not used by a concurrent call; may be NULL with norm = 0.
+ * Rows whose position is outside the table are left out of everything.
+ */
+sdpa_status_t sdpa_qk_norm_rope_bwd(const void *Q, const void *K, const void *dQ_out, const void *dK_out,
+                                    void *dQ, void *dK, float *dq_weight, float *dk_weight,
+                                    int B, int S, int Hq, int Hkv, int D,
+                                    const sdpa_layout_t *q_layout, const sdpa_layout_t *k_layout,
+                                    const sdpa_layout_t *dq_out_layout, const sdpa_layout_t *dk_out_layout,
+                                    const sdpa_layout_t *dq_layout, const sdpa_layout_t *dk_layout,
+                                    int norm, const void *q_weight, const void *k_weight,
+                                    sdpa_dtype_t weight_dtype, float eps,
+                                    const sdpa_rope_t *rope, const int *positions,
+                                    sdpa_dtype_t dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes sdpa_qk_norm_rope_bwd needs (0 for invalid sizes). */
+size_t sdpa_qk_norm_rope_bwd_workspace_bytes(int B, int S, int Hq, int Hkv, int D);
+
+/*
+ * A paged key / value cache in 8 bits: a pool of pages of page_size tokens,
+ * E4M3 codes and one fp32 scale for each page and KV head (value = code *
+ * scale).  All pointers are device memory, owned by the caller.
+ *   k, v      [n_pages][page_size][Hkv][D] codes, 16-byte aligned.
+ *   k_scale, v_scale   [n_pages][Hkv] contiguous, in [2^-60, 2^60] for every
+ *             page that is read.
+ *   page_size 16, 32, 64 or 128.
+ *   k_layout, v_layout   host pointers to strides (batch: page to page, seq:
+ *             slot to slot), NULL for contiguous.  {Hkv * page_size * D, D,
+ *             page_size * D} keeps each head's part of a page together.
+ * A block table (device, int32 [B][max_pages], contiguous) gives, for each
+ * sequence, the pages of its positions 0 .. page_size - 1, page_size .. and
+ * so on; entries behind a sequence's last position are not read.
+ */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int n_pages;
+    int page_size;
+    const sdpa_layout_t *k_layout, *v_layout;
+} sdpa_cache_t;
+
+/*
+ * Appends keys and values to a paged cache, the keys rotated on the way.
+ *   K, V      device, read only, [B][S][Hkv][D], bf16 or fp16, D 64 or 128.
+ *   start     device, int32 [B]: tokens that the sequence has in the cache.
+ *   count     device, int32 [B]: tokens that are appended (the first
+ *             count[b] of the S, taken into 0 .. S), or NULL: S each.
+ *             Token i goes to position start[b] + i, which is also the
+ *             position that rotates its key.
+ *   rope      see sdpa_rope_t.
+ * The scale of a page is the smallest power of two s with max|x| <= 448 s over
+ * its tokens (of finite values; 2^-60 at least, 2^60 at most), where a call
+ * that begins inside a page keeps at least the page's scale, and rounds the
+ * page's earlier tokens to a scale that grows.  Larger values and infinities
+ * saturate at 448 s, NaN stays NaN.  Pages that a call writes belong to one
+ * sequence each.  Slots behind the last token are not written.
+ * A page index outside the pool, a position outside the block table and a
+ * position outside the rotation table are not followed: what would go there
+ * is not written and the device error word becomes 0x601, 0x602 or 0x701.
+ */
+sdpa_status_t sdpa_cache_append(const void *K, const void *V, const sdpa_cache_t *cache,
+                                const int *block_table, const int *start, const int *count,
+                                int B, int S, int Hkv, int D, int max_pages,
+                                const sdpa_layout_t *k_layout, const sdpa_layout_t *v_layout,
+                                const sdpa_rope_t *rope, sdpa_dtype_t dtype, void *stream);
+
+/*
+ * Attention over a paged 8-bit cache: O = softmax(Q K^T * scale) V for the
+ * tokens that the last sdpa_cache_append (same start and count) has put
+ * there, or any others.
+ *   Q         device, read only, [B][Sq][Hq][D], bf16 or fp16, D 64 or 128;
+ *             Hq % Hkv == 0.
+ *   start, count   as for the append: query i < count[b] of sequence b stands
+ *             at position start[b] + i.
+ *   causal    nonzero: it sees positions 0 .. start[b] + i; 0: all of
+ *             0 .. start[b] + count[b] - 1.  (The alignment is that of the
+ *             sequence's end, unlike sdpa_fwd's.)
+ *   O         device, written, [B][Sq][Hq][D], type `dtype`; rows i >=
+ *             count[b] are not written.  A row that sees no key is 0.
+ *   LSE       device, fp32 [B][Hq][Sq], or NULL; -infinity for such a row.
+ *   workspace device scratch of sdpa_paged_workspace_bytes(...) bytes,
+ *             16-byte aligned, needing no initialisation, not used by a
+ *             concurrent call.
+ * Keys in pages outside the pool or positions outside the block table are
+ * left out, and the device error word becomes 0x601 or 0x602.
+ */
+sdpa_status_t sdpa_fwd_paged(const void *Q, const sdpa_cache_t *cache,
+                             const int *block_table, const int *start, const int *count,
+                             void *O, float *LSE, int B, int Hq, int Hkv, int Sq, int D, int max_pages,
+                             const sdpa_layout_t *q_layout, const sdpa_layout_t *o_layout,
+                             float scale, int causal, sdpa_dtype_t dtype,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes sdpa_fwd_paged needs (0 for invalid sizes). */
+size_t sdpa_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D);
+
 /* Static, human-readable name of a status code. */
 const char *sdpa_status_string(sdpa_status_t status);
 
@@ -290,13 +449,16 @@ int sdpa_last_cuda_error(void);
  * Reads and clears the device error word of the current device (0 = none;
  * 0x1xx / 0x2xx / 0x3xx = a bounded wait of the producer / MMA issuer /
  * softmax gave up; 0x4xx / 0x5xx = a bounded wait of the 16-bit / FP8
- * backward pass gave up).  Synchronises the device.  Returns SDPA_OK or
+ * backward pass gave up; 0x601 / 0x602 / 0x701 = an index that a call was
+ * given in device memory is out of range, see sdpa_cache_append; 0x8xx = a
+ * bounded wait of the attention over a paged cache gave up).  Synchronises
+ * the device.  Returns SDPA_OK or
  * SDPA_ERR_CUDA; `code` (host pointer) receives the word.
  */
 sdpa_status_t sdpa_device_error(unsigned int *code);
 
 /* Version of this ABI (bumped on any change; 2 added the *_ex entry points, 3 the decode pass,
- * 4 the backward pass, 5 the FP8 backward pass). */
+ * 4 the backward pass, 5 the FP8 backward pass, 6 the norm and rotation, the paged cache and its attention). */
 int sdpa_abi_version(void);
 
 #ifdef __cplusplus

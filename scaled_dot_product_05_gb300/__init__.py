@@ -1,4 +1,5 @@
-"""GB300 (sm_103a) scaled dot-product attention forward pass.
+"""GB300 (sm_103a) scaled dot-product attention: forward, backward, decode, and
+the norm, rotation and paged 8-bit cache around it.
 
 Python binding of the C ABI in include/sdpa.h.  Every step of the computation
 runs in the CUDA library; these functions only marshal PyTorch CUDA tensors
@@ -16,7 +17,9 @@ from ._abi import SdpaError, check, lib, status_string
 
 __all__ = ["sdpa_fwd", "sdpa_fwd_fp8", "sdpa_fwd_ex", "sdpa_fwd_fp8_ex", "sdpa_fwd_decode", "sdpa_fwd_decode_noalloc",
            "sdpa_bwd", "bwd_workspace_bytes", "sdpa_bwd_fp8", "bwd_fp8_workspace_bytes",
-           "decode_workspace_bytes", "sdpa_status_string", "sdpa_device_error", "SdpaError", "lib"]
+           "decode_workspace_bytes", "sdpa_status_string", "sdpa_device_error", "SdpaError", "lib",
+           "rope_table", "sdpa_qk_norm_rope", "sdpa_qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_bytes",
+           "PagedCache", "sdpa_cache_append", "sdpa_fwd_paged", "paged_workspace_bytes"]
 
 _DTYPE = {torch.bfloat16: _abi.SDPA_DTYPE_BF16, torch.float16: _abi.SDPA_DTYPE_FP16}
 
@@ -319,3 +322,7 @@ def sdpa_device_error() -> int:
     code = ctypes.c_uint(0)
     check(lib().sdpa_device_error(ctypes.byref(code)))
     return int(code.value)
+
+
+from .cache import (PagedCache, paged_workspace_bytes, qk_norm_rope_bwd_workspace_bytes, rope_table,  # noqa: E402
+                    sdpa_cache_append, sdpa_fwd_paged, sdpa_qk_norm_rope, sdpa_qk_norm_rope_bwd)

@@ -1,0 +1,211 @@
+// cache_append.cuh -- new keys and values into a paged 8-bit cache, the keys
+// rotated on the way.
+//
+// The cache holds E4M3 codes and one fp32 scale for each page and KV head;
+// a value is code * scale.  The scale is a power of two, the smallest with
+// max|x| <= 448 scale over the page's tokens: E4M3 is a floating type, so a
+// scale finer than that would not make its rounding (at most 2^-4 relative)
+// smaller, while a power of two makes the division exact and lets the scale of
+// a page that is filled over several calls grow without a second rounding of
+// what it holds already (but for values that become subnormal).  A call that
+// goes on in a page keeps at least the page's scale; a call that begins a page
+// ignores what its scale was.
+//
+// One unit is a (sequence, page, KV head, K or V).  Two instances: eight warps
+// a unit for prompts, one warp a unit (eight units a block) for the few tokens
+// of a decoding step.  The rows wait in registers between the maximum and the
+// rounding, so each is read once: bound by HBM for prompts (2 D bytes read, D
+// written a row), by latency for single tokens.
+#pragma once
+
+#include "rope.cuh"
+
+namespace sdpa {
+namespace cache {
+
+enum : unsigned int {
+    kErrPage = 0x601,            // a page index outside the pool
+    kErrTable = 0x602,           // a position outside the page table
+};
+
+// A paged cache: page p, slot t, KV head h at p * sp + t * ss + h * sh (elements = bytes).
+struct Pool {
+    uint8_t* codes;
+    float* scale;                // [n_pages][Hkv]
+    long long sp, ss, sh;
+};
+
+struct AppendParams {
+    const void* x[2];            // keys, values: [B][S][Hkv][D]
+    long long x_sb[2], x_ss[2], x_sh[2];
+    Pool pool[2];
+    const int* table;            // [B][max_pages]
+    const int* start;            // [B]
+    const int* count;            // [B], or null: S
+    const float* rope;           // [n_pos][rot / 2][2]
+    int B, S, Hkv, page, n_pages, max_pages;
+    int n_pos, rot;
+    int n_ord;                   // pages that S tokens can touch
+};
+
+constexpr int kAppendThreads = 256;
+
+// Smallest e in [-60, 60] with amax <= 448 * 2^e (448 = 1.75 * 2^8), as 2^e.
+__device__ __forceinline__ float pow2_scale(float amax)
+{
+    const uint32_t bits = __float_as_uint(amax);
+    int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    e = max(-60, min(60, e));
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// kWarps warps a unit (1 or 8), kPasses rows at most for each lane group.
+template <int D, bool kBF16, bool kInter, int kWarps, int kPasses>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p)
+{
+    constexpr int kLanes = D / 8;
+    constexpr int kUnitThreads = 32 * kWarps;
+    constexpr int kRows = kUnitThreads / kLanes;       // rows of a pass
+    __shared__ float warp_max[kAppendThreads / 32];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int tid = threadIdx.x % kUnitThreads;
+    const long long unit = (long long)blockIdx.x * (kAppendThreads / kUnitThreads) + threadIdx.x / kUnitThreads;
+    const int lane = tid % kLanes;
+    const int group = tid / kLanes;
+    // unit -> (KV head fastest, K or V, page of the sequence's new tokens, sequence)
+    long long rest = unit;
+    const int h = (int)(rest % p.Hkv);
+    rest /= p.Hkv;
+    const int kv = (int)(rest & 1);
+    rest >>= 1;
+    const int ord = (int)(rest % p.n_ord);
+    const long long bl = rest / p.n_ord;
+    if (bl >= p.B)
+        return;                                        // whole units: their warps leave together
+    const int b = (int)bl;
+    const long long start = p.start[b];
+    const int count = p.count ? max(0, min(p.S, p.count[b])) : p.S;
+    if (start < 0) {
+        if (tid == 0 && count > 0)
+            atomicCAS(&g_sdpa_error, 0u, (unsigned)kErrTable);
+        return;
+    }
+    const long long ord_page = start / p.page + ord;   // ordinal of the page in its sequence
+    const long long p0 = ord_page * p.page;            // position of its first slot
+    const int lo = (int)(start > p0 ? start - p0 : 0);
+    const long long end = start + count - p0;
+    const int hi = (int)(end < p.page ? end : p.page);
+    if (hi <= lo)
+        return;
+    if (ord_page >= p.max_pages) {
+        if (tid == 0)
+            atomicCAS(&g_sdpa_error, 0u, (unsigned)kErrTable);
+        return;
+    }
+    const int id = p.table[(long long)b * p.max_pages + ord_page];
+    if ((unsigned)id >= (unsigned)p.n_pages) {
+        if (tid == 0)
+            atomicCAS(&g_sdpa_error, 0u, (unsigned)kErrPage);
+        return;
+    }
+    const int rot = kv ? 0 : p.rot;                    // only the keys are rotated
+    int a, c;
+    rope::lane_channels<kInter>(lane, rot, a, c);
+    const int i0 = (int)(p0 + lo - start);             // first new token of the page
+    const uint16_t* x = reinterpret_cast<const uint16_t*>(p.x[kv]) + b * p.x_sb[kv] + h * p.x_sh[kv];
+    float v[kPasses][8];
+    uint2 ra[kPasses], rb[kPasses];
+    uint32_t ok = 0;                                   // rows that are written
+#pragma unroll
+    for (int n = 0; n < kPasses; ++n) {
+        const int r = n * kRows + group;               // row among the page's new ones
+        ra[n] = rb[n] = make_uint2(0, 0);
+        if (r < hi - lo) {
+            const uint16_t* row = x + (i0 + r) * p.x_ss[kv];
+            ra[n] = *reinterpret_cast<const uint2*>(row + a);
+            rb[n] = *reinterpret_cast<const uint2*>(row + c);
+            ok |= 1u << n;
+        }
+    }
+    float amax = 0.f;
+#pragma unroll
+    for (int n = 0; n < kPasses; ++n) {
+        if (!(ok >> n & 1))
+            continue;
+        rope::unpack4<kBF16>(ra[n], v[n]);
+        rope::unpack4<kBF16>(rb[n], v[n] + 4);
+        if (rot) {
+            const long long pos = p0 + lo + n * kRows + group;
+            if (pos >= p.n_pos) {
+                atomicCAS(&g_sdpa_error, 0u, (unsigned)rope::kErrPosition);
+                ok &= ~(1u << n);
+                continue;
+            }
+            float cs[4], sn[4];
+            rope::lane_angles(p.rope, (int)pos, rot, lane, cs, sn);
+            rope::rotate<kInter>(v[n], cs, sn);
+        }
+        // infinities (they saturate) and NaN stay out of the scale
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float t = fabsf(v[n][i]);
+            amax = t < INFINITY ? fmaxf(amax, t) : amax;
+        }
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+    const Pool pool = p.pool[kv];
+    float* scale_at = pool.scale + (long long)id * p.Hkv + h;
+    const float old = *scale_at;                       // before the barrier: written after it
+    if constexpr (kWarps > 1) {
+        if ((threadIdx.x & 31) == 0)
+            warp_max[threadIdx.x >> 5] = amax;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i)
+            amax = fmaxf(amax, warp_max[i]);
+    } else {
+        __syncwarp();
+    }
+    float scale = pow2_scale(amax);
+    uint8_t* page = pool.codes + (long long)id * pool.sp + h * pool.sh;
+    bool exact = true;                                 // the scale is a power of two
+    if (lo > 0) {
+        if (old >= scale) {
+            scale = old;
+            exact = (__float_as_uint(old) & 0x7fffffu) == 0 && old < 1e37f;
+        } else {
+            // the page's earlier tokens, rounded to the scale that it has now
+            const float f = old / scale;
+            for (int i = tid; i < lo * (D / 4); i += kUnitThreads) {
+                uint32_t* at = reinterpret_cast<uint32_t*>(page + (long long)(i / (D / 4)) * pool.ss + 4 * (i % (D / 4)));
+                const uint32_t w = *at;
+                const float2 s = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)w));
+                const float2 t = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(w >> 16)));
+                *at = (uint32_t)f32x2_to_e4m3x2(s.x * f, s.y * f) | ((uint32_t)f32x2_to_e4m3x2(t.x * f, t.y * f) << 16);
+            }
+        }
+    }
+    if (tid == 0)
+        *scale_at = scale;
+    const float inv = 1.f / scale;
+#pragma unroll
+    for (int n = 0; n < kPasses; ++n) {
+        if (!(ok >> n & 1))
+            continue;
+        uint8_t* row = page + (long long)(lo + n * kRows + group) * pool.ss;
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            q[i] = exact ? v[n][i] * inv : v[n][i] / scale;
+        *reinterpret_cast<uint32_t*>(row + a) =
+            (uint32_t)f32x2_to_e4m3x2(q[0], q[1]) | ((uint32_t)f32x2_to_e4m3x2(q[2], q[3]) << 16);
+        *reinterpret_cast<uint32_t*>(row + c) =
+            (uint32_t)f32x2_to_e4m3x2(q[4], q[5]) | ((uint32_t)f32x2_to_e4m3x2(q[6], q[7]) << 16);
+    }
+}
+
+}  // namespace cache
+}  // namespace sdpa

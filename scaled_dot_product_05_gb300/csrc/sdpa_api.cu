@@ -938,6 +938,8 @@ Args make_args(const void* Q, const void* K, const void* V, void* O, float* lse,
 
 }  // namespace
 
+#include "cache_api.cuh"
+
 extern "C" {
 
 sdpa_status_t sdpa_fwd(const void* Q, const void* K, const void* V, void* O, int B, int Hq, int Hkv, int Sq,
@@ -1102,7 +1104,7 @@ sdpa_status_t sdpa_device_error(unsigned int* code)
 
 int sdpa_abi_version(void)
 {
-    return 5;
+    return 6;
 }
 
 #ifdef SDPA_WAIT_TEST
