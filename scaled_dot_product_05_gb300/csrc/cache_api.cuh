@@ -296,7 +296,7 @@ sdpa_status_t check_cache(const sdpa_cache_t* c, const int* table, const int* st
         return SDPA_ERR_BAD_SHAPE;
     if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
         return SDPA_ERR_BAD_SHAPE;
-    if (static_cast<long long>(max_pages) * c->page_size > INT32_MAX)
+    if (static_cast<long long>(max_pages) * c->page_size > 1ll << 30)
         return SDPA_ERR_BAD_SHAPE;
     if (D != 64 && D != 128)
         return SDPA_ERR_HEAD_DIM;
@@ -333,9 +333,53 @@ cudaError_t launch_append_d(const sdpa::cache::AppendParams& p, bool bf16, bool 
     return inter ? launch_append<D, false, true>(p, s) : launch_append<D, false, false>(p, s);
 }
 
-size_t paged_workspace(int, int, int, int, int)
+// Attention over a paged cache: rows of a tile (16 for up to 16 rows of a KV
+// head, 32 for up to 32, else 64), and the CTAs that share the key tiles: two
+// on each of 152 SMs.
+constexpr int kPagedCtas = 304;
+
+int paged_tile_rows(int Sq, int group)
 {
-    return 16;
+    const long long rows = static_cast<long long>(Sq) * group;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+size_t paged_workspace(int Hq, int Hkv, int Sq, int D)
+{
+    return static_cast<size_t>(kPagedCtas) * 2 * paged_tile_rows(Sq, Hq / Hkv) * (D + 1) * sizeof(float);
+}
+
+template <int D, bool kBF16, int NR>
+cudaError_t launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const sdpa::paged::Params& p, int dev,
+                         cudaStream_t stream)
+{
+    using namespace sdpa::paged;
+    constexpr int QP = kBF16 ? 2 : 3;
+    using L = PagedLayout<D, NR, QP>;
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t attr[kMaxDevices];
+    std::call_once(once[dev], [&] {
+        attr[dev] = cudaFuncSetAttribute(paged_attn_kernel<D, kBF16, NR, QP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         L::kSmemBytes);
+    });
+    if (attr[dev] != cudaSuccess)
+        return attr[dev];
+    cudaError_t e = launch_pdl(true, paged_attn_kernel<D, kBF16, NR, QP>, dim3(p.ctas), dim3(L::kThreads), L::kSmemBytes,
+                               stream, tk, tv, p);
+    const long long rows = static_cast<long long>(p.Sq) * p.group;
+    if (e == cudaSuccess && p.ctas > 1)
+        e = launch_pdl(true, paged_join_kernel<D, kBF16, NR>, dim3(p.ctas - 1, static_cast<unsigned>(rows < NR ? rows : NR)),
+                       dim3(kJoinThreads), 0, stream, p);
+    return e;
+}
+
+template <int D, bool kBF16>
+cudaError_t launch_paged_rows(int nr, const CUtensorMap& tk, const CUtensorMap& tv, const sdpa::paged::Params& p, int dev,
+                              cudaStream_t s)
+{
+    return nr == 16   ? launch_paged<D, kBF16, 16>(tk, tv, p, dev, s)
+           : nr == 32 ? launch_paged<D, kBF16, 32>(tk, tv, p, dev, s)
+                      : launch_paged<D, kBF16, 64>(tk, tv, p, dev, s);
 }
 
 }  // namespace
@@ -479,7 +523,7 @@ sdpa_status_t sdpa_fwd_paged(const void* Q, const sdpa_cache_t* cache, const int
     const View q{Q, resolve(q_layout, Sq, Hq, D), B, Sq, Hq, D, 2}, o{O, resolve(o_layout, Sq, Hq, D), B, Sq, Hq, D, 2};
     if (!view_ok(q) || !view_ok(o) || !injective(o.st, B, Sq, Hq, D))
         return SDPA_ERR_LAYOUT;
-    const size_t need = paged_workspace(B, Hq, Hkv, Sq, D);
+    const size_t need = paged_workspace(Hq, Hkv, Sq, D);
     if (!aligned16(workspace) || workspace_bytes < need)
         return SDPA_ERR_WORKSPACE;
     // O, LSE and the workspace lie apart from one another and from every input
@@ -520,14 +564,25 @@ sdpa_status_t sdpa_fwd_paged(const void* Q, const sdpa_cache_t* cache, const int
     p.max_pages = max_pages;
     p.causal = causal ? 1 : 0;
     p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
-    const long long rows = static_cast<long long>(B) * Sq * Hq;
-    const dim3 grid(static_cast<unsigned>((rows + 3) / 4));
+    const int nr = paged_tile_rows(Sq, p.group);
+    p.row_tiles = static_cast<int>((static_cast<long long>(Sq) * p.group + nr - 1) / nr);
+    // no more CTAs than there can be tiles
+    const __int128 most = static_cast<__int128>(B) * Hkv * p.row_tiles *
+                          ((static_cast<long long>(max_pages) * p.page + sdpa::paged::kTileKeys - 1) / sdpa::paged::kTileKeys);
+    p.ctas = 2 * sm_count < kPagedCtas ? 2 * sm_count : kPagedCtas;
+    p.ctas = most < p.ctas ? static_cast<int>(most) : p.ctas;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_lse = p.part_o + static_cast<long long>(p.ctas) * 2 * nr * D;
+    CUtensorMap tk, tv;
+    if (!make_map(&tk, cache->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, Hkv, p.page, p.n_pages, ck.st, 1, p.page) ||
+        !make_map(&tv, cache->v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, Hkv, p.page, p.n_pages, cv.st, 1, p.page))
+        return cuda_fail(cudaErrorInvalidValue);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == SDPA_DTYPE_BF16;
-    const cudaError_t e = D == 64 ? (bf16 ? launch_pdl(true, sdpa::paged::paged_rows_kernel<64, true>, grid, dim3(128), 0, cs, p)
-                                          : launch_pdl(true, sdpa::paged::paged_rows_kernel<64, false>, grid, dim3(128), 0, cs, p))
-                                  : (bf16 ? launch_pdl(true, sdpa::paged::paged_rows_kernel<128, true>, grid, dim3(128), 0, cs, p)
-                                          : launch_pdl(true, sdpa::paged::paged_rows_kernel<128, false>, grid, dim3(128), 0, cs, p));
+    const cudaError_t e = D == 64 ? (bf16 ? launch_paged_rows<64, true>(nr, tk, tv, p, dev, cs)
+                                          : launch_paged_rows<64, false>(nr, tk, tv, p, dev, cs))
+                                  : (bf16 ? launch_paged_rows<128, true>(nr, tk, tv, p, dev, cs)
+                                          : launch_paged_rows<128, false>(nr, tk, tv, p, dev, cs));
     return e == cudaSuccess ? SDPA_OK : cuda_fail(e);
 }
 
@@ -535,7 +590,7 @@ size_t sdpa_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D)
 {
     if (B < 1 || Hq < 1 || Hkv < 1 || Sq < 1 || Hq % Hkv != 0 || (D != 64 && D != 128))
         return 0;
-    return paged_workspace(B, Hq, Hkv, Sq, D);
+    return paged_workspace(Hq, Hkv, Sq, D);
 }
 
 }  // extern "C"
