@@ -334,19 +334,20 @@ cudaError_t launch_append_d(const sdpa::cache::AppendParams& p, bool bf16, bool 
 }
 
 // Attention over a paged cache: rows of a tile (16 for up to 16 rows of a KV
-// head, 32 for up to 32, else 64), and the CTAs that share the key tiles: two
-// on each of 152 SMs.
+// head; else 32, or 64 for bf16 and more than 32 rows), and the CTAs that
+// share the key tiles: two on each of 152 SMs.
 constexpr int kPagedCtas = 304;
 
-int paged_tile_rows(int Sq, int group)
+int paged_tile_rows(int Sq, int group, bool bf16)
 {
     const long long rows = static_cast<long long>(Sq) * group;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    return rows <= 16 ? 16 : rows <= 32 || !bf16 ? 32 : 64;
 }
 
+// The pieces' results, their LSE, and what is to join.
 size_t paged_workspace(int Hq, int Hkv, int Sq, int D)
 {
-    return static_cast<size_t>(kPagedCtas) * 2 * paged_tile_rows(Sq, Hq / Hkv) * (D + 1) * sizeof(float);
+    return static_cast<size_t>(kPagedCtas) * (2 * paged_tile_rows(Sq, Hq / Hkv, true) * (D + 1) * sizeof(float) + sizeof(int4));
 }
 
 template <int D, bool kBF16, int NR>
@@ -354,22 +355,21 @@ cudaError_t launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const sdp
                          cudaStream_t stream)
 {
     using namespace sdpa::paged;
-    constexpr int QP = kBF16 ? 2 : 3;
-    using L = PagedLayout<D, NR, QP>;
+    using L = PagedLayout<D, kBF16, NR>;
     static std::once_flag once[kMaxDevices];
     static cudaError_t attr[kMaxDevices];
     std::call_once(once[dev], [&] {
-        attr[dev] = cudaFuncSetAttribute(paged_attn_kernel<D, kBF16, NR, QP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        attr[dev] = cudaFuncSetAttribute(paged_attn_kernel<D, kBF16, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          L::kSmemBytes);
     });
     if (attr[dev] != cudaSuccess)
         return attr[dev];
-    cudaError_t e = launch_pdl(true, paged_attn_kernel<D, kBF16, NR, QP>, dim3(p.ctas), dim3(L::kThreads), L::kSmemBytes,
+    cudaError_t e = launch_pdl(true, paged_attn_kernel<D, kBF16, NR>, dim3(p.ctas), dim3(L::kThreads), L::kSmemBytes,
                                stream, tk, tv, p);
     const long long rows = static_cast<long long>(p.Sq) * p.group;
+    const unsigned blocks = static_cast<unsigned>(NR == 16 ? rows : (rows < NR ? rows + 7 : NR) / 8);
     if (e == cudaSuccess && p.ctas > 1)
-        e = launch_pdl(true, paged_join_kernel<D, kBF16, NR>, dim3(p.ctas - 1, static_cast<unsigned>(rows < NR ? rows : NR)),
-                       dim3(kJoinThreads), 0, stream, p);
+        e = launch_pdl(true, paged_join_kernel<D, kBF16, NR>, dim3(p.ctas - 1, blocks), dim3(kJoinThreads), 0, stream, p);
     return e;
 }
 
@@ -377,9 +377,13 @@ template <int D, bool kBF16>
 cudaError_t launch_paged_rows(int nr, const CUtensorMap& tk, const CUtensorMap& tv, const sdpa::paged::Params& p, int dev,
                               cudaStream_t s)
 {
-    return nr == 16   ? launch_paged<D, kBF16, 16>(tk, tv, p, dev, s)
-           : nr == 32 ? launch_paged<D, kBF16, 32>(tk, tv, p, dev, s)
-                      : launch_paged<D, kBF16, 64>(tk, tv, p, dev, s);
+    if (nr == 16)
+        return launch_paged<D, kBF16, 16>(tk, tv, p, dev, s);
+    if constexpr (kBF16) {
+        if (nr == 64)
+            return launch_paged<D, kBF16, 64>(tk, tv, p, dev, s);
+    }
+    return launch_paged<D, kBF16, 32>(tk, tv, p, dev, s);
 }
 
 }  // namespace
@@ -564,7 +568,8 @@ sdpa_status_t sdpa_fwd_paged(const void* Q, const sdpa_cache_t* cache, const int
     p.max_pages = max_pages;
     p.causal = causal ? 1 : 0;
     p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
-    const int nr = paged_tile_rows(Sq, p.group);
+    p.page_shift = p.page == 16 ? 4 : p.page == 32 ? 5 : p.page == 64 ? 6 : 7;
+    const int nr = paged_tile_rows(Sq, p.group, dtype == SDPA_DTYPE_BF16);
     p.row_tiles = static_cast<int>((static_cast<long long>(Sq) * p.group + nr - 1) / nr);
     // no more CTAs than there can be tiles
     const __int128 most = static_cast<__int128>(B) * Hkv * p.row_tiles *
@@ -573,6 +578,7 @@ sdpa_status_t sdpa_fwd_paged(const void* Q, const sdpa_cache_t* cache, const int
     p.ctas = most < p.ctas ? static_cast<int>(most) : p.ctas;
     p.part_o = static_cast<float*>(workspace);
     p.part_lse = p.part_o + static_cast<long long>(p.ctas) * 2 * nr * D;
+    p.joins = reinterpret_cast<int4*>(p.part_lse + static_cast<long long>(p.ctas) * 2 * nr);
     CUtensorMap tk, tv;
     if (!make_map(&tk, cache->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, Hkv, p.page, p.n_pages, ck.st, 1, p.page) ||
         !make_map(&tv, cache->v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, Hkv, p.page, p.n_pages, cv.st, 1, p.page))

@@ -12,12 +12,12 @@
 // word; no address is formed from such an index.
 //
 // The codes go to the FP8 tensor cores as they lie in the cache, and the
-// 16-bit operands are split instead: q, scaled by a power of two, into E4M3
-// parts that add up to it (two hold the 8 bits of bf16, three the 11 of fp16),
-// and the weight w_j = exp(s_j - m) v_scale_j into two, the second 16 times as
-// large as it counts so that small weights keep their bits (error 2^-8 of a
-// weight at most, as rounding it to bf16 would give).  Products of E4M3 values are
-// exact in the fp32 accumulator.  Nothing is dequantised, and K and V are
+// 16-bit operands are split instead: q, scaled by a power of two, and the
+// weights w_j = exp(s_j - m) v_scale_j, into E4M3 parts that add up to them:
+// two hold the 8 bits of bf16, three the 11 of fp16.  A weight's second part is
+// held 16 times as large as it counts, its third 256 times, each in columns of
+// its own, so that small weights keep their bits.  Products of E4M3 values
+// are exact in the fp32 accumulator.  Nothing is dequantised, and K and V are
 // read once as bytes.
 //
 // The rows (token, query head) of one KV head are the N side of the products,
@@ -25,7 +25,9 @@
 //     S^T[128 keys][rows] = K8 Q^T,   O^T[D][rows] += V8^T W^T,
 // so a decoding step's few rows cost few columns and every thread of the
 // softmax warpgroup has one key of the tile: its scales, its mask and its
-// weights for all rows.
+// weights for all rows.  Two warpgroups take turns, each with maxima, sums and
+// an accumulator of its own, joined when the item is done: one alone leaves
+// the schedulers waiting on its latencies.
 #pragma once
 
 #include "cache_append.cuh"
@@ -46,10 +48,12 @@ struct Params {
     int page, n_pages, max_pages;
     int causal;
     float scale_log2;                // scale * log2(e)
+    int page_shift;                  // log2(page)
     int row_tiles;                   // tiles of NR rows that Sq * group rows need
     int ctas;                        // CTAs that share the key tiles
     float* part_o;                   // [ctas][2][NR][D]: normalised results of pieces
     float* part_lse;                 // [ctas][2][NR]: their LSE in log2 units
+    int4* joins;                     // [ctas]: x (low, high half), KV head and pieces of an item to join, see Join
 };
 
 enum : unsigned int { kErrPagedLoad = 0x801, kErrPagedMma = 0x811, kErrPagedSoftmax = 0x821 };
@@ -61,41 +65,46 @@ constexpr int kTileKeys = 128;
 constexpr float kLag = 2.0f;
 constexpr float kLog2W = 6.807354922057604f;   // log2(112)
 
-// Shared memory and TMEM of one CTA: NR rows, QP parts of q.
-template <int D, int NR, int QP>
+// Shared memory and TMEM of one CTA: NR rows, in kParts E4M3 parts.
+template <int D, bool kBF16, int NR>
 struct PagedLayout {
     static_assert(D == 64 || D == 128, "head dimension");
-    static_assert(NR == 16 || NR == 32 || NR == 64, "rows of a tile");
-    static constexpr int kThreads = 192;   // 4 softmax warps, TMA producer, MMA issuer
+    static_assert(NR == 16 || NR == 32 || (NR == 64 && kBF16), "rows of a tile");
+    static constexpr int kParts = kBF16 ? 2 : 3;
+    static constexpr int kGroups = NR == 64 ? 1 : 2;            // softmax warpgroups
+    static constexpr int kSoftmax = 128 * kGroups;              // warps 0 ..
+    static constexpr int kThreads = kSoftmax + 64;              // then TMA producer, MMA issuer
     static constexpr int kTileBytes = kTileKeys * D;            // a K or V tile
-    // depth of the rings and of the weights' buffers: what two CTAs fit into an SM
+    // depth of the rings: what two CTAs fit into an SM
     static constexpr int kStagesK = D == 64 ? 4 : NR == 16 ? 3 : 2;
-    static constexpr int kStagesV = D == 64 ? 4 : NR == 64 ? 2 : 3;
-    static constexpr int kBufsW = NR == 64 ? 1 : 2;
+    static constexpr int kStagesV = D == 64 ? 4 : NR < 64 && kBF16 ? 3 : 2;
     static constexpr int kQPartBytes = NR * D;
-    static constexpr int kWRow = 2 * NR;                        // bytes of a key's weights: two parts
+    static constexpr int kWRow = (kBF16 ? 2 : 4) * NR;          // bytes of a key's weights (a power of two)
     static constexpr int kWBytes = kTileKeys * kWRow;
     static constexpr int kOffK = 0;
     static constexpr int kOffV = kOffK + kStagesK * kTileBytes;
     static constexpr int kOffW = kOffV + kStagesV * kTileBytes;  // at D = 64 also what the unused half of the last
-    static constexpr int kOffQ = kOffW + kBufsW * kWBytes;       // V tile's operand reads
-    static constexpr int kOffRows = kOffQ + QP * kQPartBytes;    // per-row numbers, see Rows
-    static constexpr int kRowsBytes = 4 * (4 * NR + 4 * NR + D); // scale, max, last key, factor; 4 x exchange; NaN
+    static constexpr int kOffQ = kOffW + kGroups * kWBytes;      // V tile's operand reads
+    static constexpr int kOffRows = kOffQ + kParts * kQPartBytes;
+    // per row: q's scale, last key; per warpgroup: negative maximum, shift, factor, 4 x exchange; per channel: NaN
+    static constexpr int kRowsBytes = 4 * (2 * NR + 7 * NR * kGroups + D);
     static constexpr int kOffBar = (kOffRows + kRowsBytes + 15) / 16 * 16;
-    static constexpr int kSmemBytes = kOffBar + 512 + 1024;      // barriers, alignment
+    static constexpr int kBarBytes = 384;
+    static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;                // + alignment
     static_assert(kOffQ % 1024 == 0 && kOffW % 1024 == 0, "swizzle atoms");
-    static_assert(D == 128 || kBufsW * kWBytes + QP * kQPartBytes >= kTileBytes, "operand of the unused half");
+    static_assert(D == 128 || kGroups * kWBytes + kParts * kQPartBytes >= kTileBytes, "operand of the unused half");
     static_assert(2 * (kSmemBytes + 1024) <= 233472, "two CTAs per SM");
-    static constexpr uint32_t kTmemCols = 4 * NR;                // S twice, O (two parts)
-    __host__ __device__ static constexpr uint32_t tmem_s(int i) { return i * NR; }
-    static constexpr uint32_t kTmemO = 2 * NR;
+    // a warpgroup's columns: S^T, then the parts of O^T
+    static constexpr int kGroupCols = (1 + kParts) * NR;
+    static constexpr uint32_t kTmemCols = kGroups * kGroupCols <= 64 ? 64 : kGroups * kGroupCols <= 128 ? 128 : 256;
+    static_assert(kGroups * kGroupCols <= 256, "two CTAs per SM");
 };
 
-template <int NK, int NV>
+template <int NK, int NV, int kGroups>
 struct PagedBarriers {
     uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV];
-    uint64_t s_full[2], s_free[2];         // S^T computed / read out
-    uint64_t w_full[2], pv_done[2];        // weights written / multiplied
+    // of each warpgroup: S^T computed / read out, weights written / multiplied
+    uint64_t s_full[kGroups], s_free[kGroups], w_full[kGroups], pv_done[kGroups];
     uint64_t q_full;                       // q's parts written
     uint64_t o_free;                       // O^T read out
     uint64_t drain;
@@ -103,7 +112,7 @@ struct PagedBarriers {
     int abort;
     // where the CTA's share of the tiles begins
     long long total, x, x_first;
-    long long warp_sums[16];
+    long long warp_sums[12];
 };
 
 // Number of key tiles of entry x = (sequence, row tile): 0 without rows, else
@@ -249,18 +258,38 @@ __device__ __forceinline__ Item item_of(const Params& p, const Piece& w)
     return t;
 }
 
-template <int D, bool kBF16, int NR, int QP>
-__global__ void __launch_bounds__(192, 2)
+// An item whose pieces several CTAs have is joined by the block of the second
+// of them, c: joins[c].w is the number of pieces (0: nothing to join there).
+__device__ __forceinline__ int4 join_of(const Params& p, long long total, const Piece& w)
+{
+    const int c = blockIdx.x;
+    const long long first = share_begin(total, c, p.ctas) - w.begin;          // the item's first tile
+    if (w.begin == 0 || first < share_begin(total, c - 1, p.ctas))
+        return make_int4(0, 0, 0, 0);
+    int last = c, hi = p.ctas - 1;                     // the CTA that has the item's last tile: bisection
+    while (last < hi) {
+        const int mid = (last + hi + 1) >> 1;
+        if (share_begin(total, mid, p.ctas) <= first + w.n - 1)
+            last = mid;
+        else
+            hi = mid - 1;
+    }
+    return make_int4((int)(unsigned)w.x, (int)(w.x >> 32), w.h, last - c + 2);
+}
+
+template <int D, bool kBF16, int NR>
+__global__ void __launch_bounds__(PagedLayout<D, kBF16, NR>::kThreads, 2)
 paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p)
 {
-    using L = PagedLayout<D, NR, QP>;
-    constexpr int NK = L::kStagesK, NV = L::kStagesV, NW = L::kBufsW;
-    constexpr int kSoftmax = 128;
-    constexpr uint32_t kBarSoftmax = 1;
+    using L = PagedLayout<D, kBF16, NR>;
+    constexpr int NK = L::kStagesK, NV = L::kStagesV, G = L::kGroups, QP = L::kParts;
+    constexpr int kProducer = L::kSoftmax / 32, kIssuer = kProducer + 1;      // warps
+    constexpr uint32_t kBarAll = 1;                    // named barriers: all softmax threads, 2 + g one warpgroup
+    using Bars = PagedBarriers<NK, NV, G>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    auto* bars = reinterpret_cast<PagedBarriers<NK, NV>*>(smem + L::kOffBar);
-    static_assert(sizeof(PagedBarriers<NK, NV>) <= 512, "barrier block");
+    auto* bars = reinterpret_cast<Bars*>(smem + L::kOffBar);
+    static_assert(sizeof(Bars) <= L::kBarBytes, "barrier block");
     volatile int* abort = &bars->abort;
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -276,23 +305,23 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             mbar_init(smem_u32(&bars->v_full[i]), 1);
             mbar_init(smem_u32(&bars->v_empty[i]), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < G; ++i) {
             mbar_init(smem_u32(&bars->s_full[i]), 1);
-            mbar_init(smem_u32(&bars->s_free[i]), kSoftmax);
-            mbar_init(smem_u32(&bars->w_full[i]), kSoftmax);
+            mbar_init(smem_u32(&bars->s_free[i]), 128);
+            mbar_init(smem_u32(&bars->w_full[i]), 128);
             mbar_init(smem_u32(&bars->pv_done[i]), 1);
         }
-        mbar_init(smem_u32(&bars->q_full), kSoftmax);
-        mbar_init(smem_u32(&bars->o_free), kSoftmax);
+        mbar_init(smem_u32(&bars->q_full), L::kSoftmax);
+        mbar_init(smem_u32(&bars->o_free), L::kSoftmax);
         mbar_init(smem_u32(&bars->drain), 1);
         bars->abort = 0;
         fence_mbar_init();
     }
-    if (warp == 4 && lane == 0) {
+    if (warp == kProducer && lane == 0) {
         tma_prefetch_map(&tm_k);
         tma_prefetch_map(&tm_v);
     }
-    if (warp == 5) {
+    if (warp == kIssuer) {
         tmem_alloc(smem_u32(&bars->tmem_base), L::kTmemCols);
         tmem_relinquish();
     }
@@ -306,18 +335,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 
     Piece w;
     bool more = first_piece<NR>(p, bars, w);
-    if (warp == 4) {
+    if (warp == kProducer) {
         // =========================== TMA producer ===========================
         // lane i brings page i of a tile; pages that no row sees, or whose
         // index is outside the pool, are not loaded (their keys are masked)
-        const int ppt = kTileKeys / p.page;
+        if (lane == 0 && blockIdx.x > 0)
+            p.joins[blockIdx.x] = more ? join_of(p, bars->total, w) : make_int4(0, 0, 0, 0);
+        const int ppt = kTileKeys >> p.page_shift;
         uint32_t n = 0;                                    // tiles issued (ring position)
         bool ok = true;
         for (; ok && more; more = next_piece<NR>(p, w)) {
             const Item it = item_of<NR>(p, w);
             auto page_of = [&](int tile) -> int {
                 const int ord = tile * ppt + lane;
-                if (lane >= ppt || ord >= p.max_pages || (long long)ord * p.page >= it.keys)
+                if (lane >= ppt || ord >= p.max_pages || ord << p.page_shift >= it.keys)
                     return -1;
                 const int id = p.table[(long long)it.b * p.max_pages + ord];
                 return (unsigned)id < (unsigned)p.n_pages ? id : -1;
@@ -351,8 +382,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     tma_load_4d(sV + vs * L::kTileBytes + lane * p.page * D, &tm_v, smem_u32(&bars->v_full[vs]), 0, w.h, 0, id);
             }
         }
-        // never leave with copies in flight (after an abort the last V tile
-        // may not have been issued: its wait then runs out)
+        // never leave with copies in flight (after an abort the last K tile
+        // may or may not have been issued: at worst its wait runs out)
         if (lane == 0) {
             for (uint32_t i = n > NK ? n - NK : 0; i < n; ++i)
                 drain_wait(smem_u32(&bars->k_full[i % NK]), (i / NK) & 1);
@@ -362,27 +393,28 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 drain_wait(smem_u32(&bars->v_full[i % NV]), (i / NV) & 1);
         }
         __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp == kIssuer) {
         // ============================ MMA issuer ============================
         if (lane == 0) {
             constexpr int kSwz = D;                        // bytes of a K / V row = swizzle span
             constexpr uint32_t kSwzCode = D == 128 ? 2u : 4u;
-            constexpr uint32_t kWCode = NR == 16 ? 6u : NR == 32 ? 4u : 2u;
+            constexpr uint32_t kWCode = L::kWRow == 32 ? 6u : L::kWRow == 64 ? 4u : 2u;
             constexpr uint32_t idesc_s = idesc_make(0u, kTileKeys, NR, false);
             // V^T: 128 rows of which D are the tile's; at D = 64 the others are
             // whatever lies behind the tile, and their results are not read
-            constexpr uint32_t idesc_o = idesc_make_amn(0u, 128, 2 * NR, true);
+            constexpr uint32_t idesc_o = idesc_make_amn(0u, 128, QP * NR, true);
             const uint32_t hi = (uint32_t)(smem_desc(0, 16, 8 * kSwz, kSwzCode) >> 32);
             const uint32_t hi_w = (uint32_t)(smem_desc(0, 16, 8 * L::kWRow, kWCode) >> 32);
             const uint32_t lbo_v = (uint32_t)(L::kTileBytes >> 4) << 16;
-            uint32_t ns = 0, nv = 0, pieces = 0;           // S^T and O^T products issued, pieces begun
+            uint32_t ks_n = 0, vs_n = 0, pieces = 0;       // S^T and O^T products issued, pieces begun
+            uint32_t ns[2] = {0, 0}, nv[2] = {0, 0};       // the same, of each warpgroup
             bool ok = true;
             for (; ok && more; more = next_piece<NR>(p, w), ++pieces) {
                 const int n = w.end - w.begin;
-                auto issue_s = [&]() -> bool {
-                    const uint32_t ks = ns % NK, buf = ns & 1;
-                    if (!wait_bar(smem_u32(&bars->k_full[ks]), (ns / NK) & 1, abort, kErrPagedMma) ||
-                        (ns >= 2 && !wait_bar(smem_u32(&bars->s_free[buf]), (ns / 2 - 1) & 1, abort, kErrPagedMma + 1)))
+                auto issue_s = [&](int g) -> bool {
+                    const uint32_t ks = ks_n % NK, done = ns[g];
+                    if (!wait_bar(smem_u32(&bars->k_full[ks]), (ks_n / NK) & 1, abort, kErrPagedMma) ||
+                        (done > 0 && !wait_bar(smem_u32(&bars->s_free[g]), (done - 1) & 1, abort, kErrPagedMma + 1)))
                         return false;
                     tc_fence_after_sync();
                     const uint32_t k_lo = ((sK + ks * L::kTileBytes) >> 4) | (1u << 16);
@@ -391,34 +423,39 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         const uint32_t q_lo = ((sQ + q * L::kQPartBytes) >> 4) | (1u << 16);
 #pragma unroll
                         for (int kk = 0; kk < D / 32; ++kk)
-                            mma_f8_ss(tmem + L::tmem_s(buf), desc_join(hi, k_lo + 2 * kk), desc_join(hi, q_lo + 2 * kk),
+                            mma_f8_ss(tmem + g * L::kGroupCols, desc_join(hi, k_lo + 2 * kk), desc_join(hi, q_lo + 2 * kk),
                                       idesc_s, q > 0 || kk > 0);
                     }
-                    mma_commit(smem_u32(&bars->s_full[buf]));
+                    mma_commit(smem_u32(&bars->s_full[g]));
                     mma_commit(smem_u32(&bars->k_empty[ks]));
-                    ++ns;
+                    ++ns[g];
+                    ++ks_n;
                     return true;
                 };
-                ok = wait_bar(smem_u32(&bars->q_full), pieces & 1, abort, kErrPagedMma + 2) && issue_s();
-                for (int j = 0; ok && j < n; ++j, ++nv) {
-                    if (j + 1 < n && !(ok = issue_s()))
+                ok = wait_bar(smem_u32(&bars->q_full), pieces & 1, abort, kErrPagedMma + 2) && issue_s(0);
+                if (G > 1 && n > 1)
+                    ok = ok && issue_s(1);
+                for (int j = 0; ok && j < n; ++j, ++vs_n) {
+                    const int g = G > 1 ? j & 1 : 0;
+                    if (j + G < n && !(ok = issue_s(g)))
                         break;
-                    const uint32_t vs = nv % NV, buf = nv % NW;
-                    ok = wait_bar(smem_u32(&bars->v_full[vs]), (nv / NV) & 1, abort, kErrPagedMma + 3) &&
-                         wait_bar(smem_u32(&bars->w_full[buf]), (nv / NW) & 1, abort, kErrPagedMma + 4) &&
+                    const uint32_t vs = vs_n % NV;
+                    ok = wait_bar(smem_u32(&bars->v_full[vs]), (vs_n / NV) & 1, abort, kErrPagedMma + 3) &&
+                         wait_bar(smem_u32(&bars->w_full[g]), nv[g] & 1, abort, kErrPagedMma + 4) &&
                          (j > 0 || pieces == 0 ||
                           wait_bar(smem_u32(&bars->o_free), (pieces - 1) & 1, abort, kErrPagedMma + 5));
                     if (!ok)
                         break;
                     tc_fence_after_sync();
                     const uint32_t v_lo = ((sV + vs * L::kTileBytes) >> 4) | lbo_v;
-                    const uint32_t w_lo = ((sW + buf * L::kWBytes) >> 4) | (1u << 16);
+                    const uint32_t w_lo = ((sW + g * L::kWBytes) >> 4) | (1u << 16);
 #pragma unroll
                     for (int kk = 0; kk < kTileKeys / 32; ++kk)
-                        mma_f8_ss(tmem + L::kTmemO, desc_join(hi, v_lo + (uint32_t)((kk * 32 * kSwz) >> 4)),
-                                  desc_join(hi_w, w_lo + (uint32_t)((kk * 32 * L::kWRow) >> 4)), idesc_o, j > 0 || kk > 0);
-                    mma_commit(smem_u32(&bars->pv_done[buf]));
+                        mma_f8_ss(tmem + g * L::kGroupCols + NR, desc_join(hi, v_lo + (uint32_t)((kk * 32 * kSwz) >> 4)),
+                                  desc_join(hi_w, w_lo + (uint32_t)((kk * 32 * L::kWRow) >> 4)), idesc_o, j >= G || kk > 0);
+                    mma_commit(smem_u32(&bars->pv_done[g]));
                     mma_commit(smem_u32(&bars->v_empty[vs]));
+                    ++nv[g];
                 }
             }
             mma_commit(smem_u32(&bars->drain));
@@ -426,22 +463,28 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         __syncwarp();
     } else {
-        // ========================= softmax warpgroup ========================
+        // ======================== softmax warpgroups ========================
+        const int g = G > 1 ? warp >> 2 : 0;
+        const uint32_t bar_group = 2 + g;
+        const int tid = threadIdx.x & 127;                                  // key of the tile; TMEM lane
         float* row_scale = reinterpret_cast<float*>(smem + L::kOffRows);    // q's power of two * scale * log2 e
-        float* row_max = row_scale + NR;
-        int* row_last = reinterpret_cast<int*>(row_max + NR);               // last key that a row sees
-        float* row_factor = row_max + 2 * NR;                               // rescale, or 1 / l
-        float* exch = row_max + 3 * NR;                                     // [4][NR]
-        int* nan_at = reinterpret_cast<int*>(exch + 4 * NR);                // [D]: first masked key with a NaN there
-        const int key = threadIdx.x;                                        // of the tile; TMEM lane
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-        uint32_t ns = 0;                                                    // tiles so far
+        int* row_last = reinterpret_cast<int*>(row_scale + NR);             // last key that a row sees
+        float* group_rows = row_scale + 2 * NR;                             // 7 NR numbers of each warpgroup
+        float* row_nmax = group_rows + 7 * NR * g;                          // log2(112) - maximum
+        float* row_shift = row_nmax + NR;                                   // by how much the maximum grows
+        float* row_factor = row_nmax + 2 * NR;                              // rescale; in the end the weight of O^T
+        float* exch = row_nmax + 3 * NR;                                    // [4][NR]
+        int* nan_at = reinterpret_cast<int*>(group_rows + 7 * NR * G);      // [D]: first masked key with a NaN there
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t t_s = tmem + lanes + g * L::kGroupCols, t_o = t_s + NR;
+        uint32_t ns = 0;                                                    // tiles of this warpgroup so far
+        uint32_t nv = 0;                                                    // tiles of the CTA before this piece
         bool ok = true;
-        for (; more; more = next_piece<NR>(p, w)) {
+        for (; more; nv += w.end - w.begin, more = next_piece<NR>(p, w)) {
             const Item it = item_of<NR>(p, w);
             // ---- q into E4M3 parts, and each row's numbers
             {
-                constexpr int kPer = kSoftmax / NR;                         // threads of a row
+                constexpr int kPer = L::kSoftmax / NR;                      // threads of a row
                 constexpr int kSegs = (D / 16 + kPer - 1) / kPer;           // 16-element runs of a thread
                 const int r = threadIdx.x / kPer, sub = threadIdx.x % kPer;
                 const bool live = r < it.rows;
@@ -507,31 +550,33 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (sub == 0) {
                     const long long last = p.causal ? it.start + i : it.start + it.count - 1;
                     row_scale[r] = finite ? qs * p.scale_log2 : NAN;
-                    row_max[r] = live ? 0.f : INFINITY;                     // rows that are none get no weight
                     row_last[r] = !live || last < 0 ? -1 : (int)(last < it.keys ? last : it.keys - 1);
+#pragma unroll
+                    for (int k = 0; k < G; ++k)                             // rows that are none get no weight
+                        group_rows[7 * NR * k + r] = live ? kLog2W : -INFINITY;
                 }
-                for (int d = threadIdx.x; d < D; d += kSoftmax)
-                    nan_at[d] = INT_MAX;
+                if (threadIdx.x < D)
+                    nan_at[threadIdx.x] = INT_MAX;
                 if (threadIdx.x == 0 && it.start + it.count > (long long)p.max_pages * p.page)
                     atomicCAS(&g_sdpa_error, 0u, (unsigned)cache::kErrTable);
                 fence_proxy_async_smem();
-                named_bar_sync(kBarSoftmax, kSoftmax);
+                named_bar_sync(kBarAll, L::kSoftmax);
                 mbar_arrive(smem_u32(&bars->q_full));
             }
             // every row of the item sees keys 0 .. full - 1
             const int full = row_last[0] + 1;
-            float l[NR];
+            uint64_t l[NR / 2];                                             // pairs of rows
 #pragma unroll
-            for (int r = 0; r < NR; ++r)
-                l[r] = 0.f;
-            bool seen = false;                                              // row threadIdx.x has a maximum
+            for (int r = 0; r < NR / 2; ++r)
+                l[r] = 0;
+            bool seen = false;                                              // row tid has a maximum
             bool force = true;                                              // some row has none yet
             // this thread's page, one and two tiles ahead, and its scales
             auto page_of = [&](int tile) -> int {
-                const int pos = tile * kTileKeys + key;
-                if (pos >= it.keys)
+                const int pos = tile * kTileKeys + tid;
+                if (tile >= w.end || pos >= it.keys)
                     return -1;
-                const int id = p.table[(long long)it.b * p.max_pages + pos / p.page];
+                const int id = p.table[(long long)it.b * p.max_pages + (pos >> p.page_shift)];
                 if ((unsigned)id < (unsigned)p.n_pages)
                     return id;
                 atomicCAS(&g_sdpa_error, 0u, (unsigned)cache::kErrPage);
@@ -544,99 +589,135 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     b = p.v.scale[(long long)id * p.Hkv + w.h];
                 }
             };
-            int id = page_of(w.begin);
-            int id_next = w.begin + 1 < w.end ? page_of(w.begin + 1) : -1;
+            int id = page_of(w.begin + g);
+            int id_next = page_of(w.begin + g + G);
             float k_scale, v_scale;
             scales_of(id, k_scale, v_scale);
-            for (int j = w.begin; j < w.end; ++j, ++ns) {
+            const int first = w.begin + g;                                  // this warpgroup's first tile
+            for (int j = first; j < w.end; j += G, ++ns) {
                 const bool valid = id >= 0;
                 const float ks = k_scale;
                 const float vs = fminf(fmaxf(v_scale, 8.673617379884035e-19f), 1.152921504606847e18f);   // 2^-60 .. 2^60
-                const float lvs = log2f(vs) , rvs = 1.f / vs;
+                const float lvs = __log2f(vs), rvs = __fdividef(1.f, vs);
                 id = id_next;
                 scales_of(id, k_scale, v_scale);
-                id_next = j + 2 < w.end ? page_of(j + 2) : -1;
-                const uint32_t sbuf = ns & 1, wbuf = ns % NW;
-                const int pos = j * kTileKeys + key;
-                const bool edge = (j + 1) * kTileKeys > full;
-                ok = ok && wait_bar(smem_u32(&bars->s_full[sbuf]), (ns / 2) & 1, abort, kErrPagedSoftmax);
+                id_next = page_of(j + 2 * G);
+                const uint32_t vn = nv + (uint32_t)(j - w.begin);           // V ring position
+                const int pos = j * kTileKeys + tid;
+                // tiles in which some row does not see some key, by the item's rows or by a page that is none
+                const bool edge = (j + 1) * kTileKeys > full || __any_sync(0xffffffffu, !valid);
+                ok = ok && wait_bar(smem_u32(&bars->s_full[g]), ns & 1, abort, kErrPagedSoftmax);
                 tc_fence_after_sync();
-                // t = s + log2(v_scale): the logarithm of a weight but for the maximum; x = t - max
-                float x[NR];
-                bool high = false;
-#pragma unroll
-                for (int c = 0; c < NR; c += 16) {
+                // s + log2(v_scale): the logarithm of a weight but for the maximum, which comes off with log2(112) on top
+                const uint64_t ks2 = f32x2(ks, ks), lvs2 = f32x2(lvs, lvs);
+                auto logits = [&](int c, uint64_t (&x)[8]) -> float {
                     uint32_t s[16];
                     __syncwarp();
-                    tmem_ld16_wait(tmem + lanes + L::tmem_s(sbuf) + c, s);
+                    tmem_ld16_wait(t_s + c, s);
 #pragma unroll
                     for (int r = 0; r < 16; r += 4) {
-                        const float4 sc = *reinterpret_cast<const float4*>(row_scale + c + r);
-                        const float4 mx = *reinterpret_cast<const float4*>(row_max + c + r);
-                        const float scv[4] = {sc.x, sc.y, sc.z, sc.w}, mxv[4] = {mx.x, mx.y, mx.z, mx.w};
-                        int last[4] = {INT_MAX, INT_MAX, INT_MAX, INT_MAX};
-                        if (edge) {
-                            const int4 la = *reinterpret_cast<const int4*>(row_last + c + r);
-                            last[0] = la.x, last[1] = la.y, last[2] = la.z, last[3] = la.w;
-                        }
+                        const ulonglong2 sc = *reinterpret_cast<const ulonglong2*>(row_scale + c + r);
+                        const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(row_nmax + c + r);
+                        x[r / 2] = fma_f32x2(f32x2(__uint_as_float(s[r]), __uint_as_float(s[r + 1])), mul_f32x2(sc.x, ks2),
+                                             add_f32x2(nm.x, lvs2));
+                        x[r / 2 + 1] = fma_f32x2(f32x2(__uint_as_float(s[r + 2]), __uint_as_float(s[r + 3])),
+                                                 mul_f32x2(sc.y, ks2), add_f32x2(nm.y, lvs2));
+                    }
+                    if (edge) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float t = fmaf(__uint_as_float(s[r + e]) * scv[e], ks, lvs);
-                            x[c + r + e] = valid && pos <= last[e] ? t - mxv[e] : -INFINITY;
-                            high = high || x[c + r + e] > kLag;
+                        for (int r = 0; r < 16; r += 2) {
+                            float a, b;
+                            f32x2_split(x[r / 2], a, b);
+                            x[r / 2] = f32x2(valid && pos <= row_last[c + r] ? a : -INFINITY,
+                                             valid && pos <= row_last[c + r + 1] ? b : -INFINITY);
                         }
                     }
+                    float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+                    for (int r = 0; r < 8; r += 2) {
+                        float a, b;
+                        f32x2_split(x[r], a, b);
+                        m0 = fmax3(m0, a, b);
+                        f32x2_split(x[r + 1], a, b);
+                        m1 = fmax3(m1, a, b);
+                    }
+                    return fmaxf(m0, m1);
+                };
+                // up to 32 rows stay in registers between the vote and the weights; 64 are read again
+                constexpr bool kKeep = NR <= 32;
+                uint64_t x[kKeep ? NR / 16 : 1][8];
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < NR / 16; ++c)
+                    top = fmaxf(top, logits(16 * c, x[kKeep ? c : 0]));
+                if (kKeep) {
+                    tc_fence_before_sync();
+                    mbar_arrive(smem_u32(&bars->s_free[g]));
                 }
-                tc_fence_before_sync();
-                mbar_arrive(smem_u32(&bars->s_free[sbuf]));
-                if (named_bar_any(kBarSoftmax, kSoftmax, high || force || !ok)) {
-                    // ---- a weight above 2^kLag: everything to the rows' new maxima
-                    if (ok && j > w.begin)
-                        ok = wait_bar(smem_u32(&bars->pv_done[(ns - 1) % NW]), ((ns - 1) / NW) & 1, abort, kErrPagedSoftmax + 1);
+                if (named_bar_any(bar_group, 128, top > kLag + kLog2W || force || !ok)) {
+                    // ---- a weight above 2^kLag, or a row's first key: everything to the rows' new maxima
+                    if (ok && j > first)
+                        ok = wait_bar(smem_u32(&bars->pv_done[g]), (ns - 1) & 1, abort, kErrPagedSoftmax + 1);
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) {
-                        float m = x[r];
+                    for (int c = 0; c < NR / 16; ++c) {
+                        uint64_t y[8];
+                        if (kKeep) {
 #pragma unroll
-                        for (int o = 16; o > 0; o >>= 1)
-                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                        if (lane == (r & 31))
-                            exch[warp * NR + r] = m;
+                            for (int r = 0; r < 8; ++r)
+                                y[r] = x[kKeep ? c : 0][r];
+                        } else {
+                            logits(16 * c, y);
+                        }
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) {
+                            float a, b;
+                            f32x2_split(y[r / 2], a, b);
+                            float m = r & 1 ? b : a;
+#pragma unroll
+                            for (int o = 16; o > 0; o >>= 1)
+                                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                            if (lane == r)
+                                exch[(warp & 3) * NR + 16 * c + r] = m;
+                        }
                     }
-                    ok = named_bar_all(kBarSoftmax, kSoftmax, ok);
+                    ok = named_bar_all(bar_group, 128, ok);
                     if (!ok)
                         break;
                     bool waits = false;                                     // this row may see its first key later
-                    if (threadIdx.x < NR) {
-                        const int r = threadIdx.x;
-                        const float top = fmaxf(fmaxf(exch[r], exch[NR + r]), fmaxf(exch[2 * NR + r], exch[3 * NR + r]));
-                        const float up = seen ? fmaxf(top, 0.f) : top > -INFINITY ? top : 0.f;
-                        row_factor[r] = up;
-                        exch[r] = seen ? ex2_approx(-up) : 1.f;             // nothing to rescale before the first key
-                        row_max[r] += up;
-                        seen = seen || top > -INFINITY;
-                        waits = !seen && row_last[r] >= (j + 1) * kTileKeys;
+                    if (tid < NR) {
+                        const float m = fmaxf(fmaxf(exch[tid], exch[NR + tid]), fmaxf(exch[2 * NR + tid], exch[3 * NR + tid])) - kLog2W;
+                        const float up = seen ? fmaxf(m, 0.f) : m > -INFINITY ? m : 0.f;
+                        row_shift[tid] = up;
+                        row_factor[tid] = seen ? ex2_approx(-up) : 1.f;     // nothing to rescale before the first key
+                        row_nmax[tid] -= up;
+                        seen = seen || m > -INFINITY;
+                        waits = !seen && row_last[tid] >= (j + G) * kTileKeys;
                     }
-                    force = named_bar_any(kBarSoftmax, kSoftmax, waits);
+                    force = named_bar_any(bar_group, 128, waits);
                     tc_fence_after_sync();
 #pragma unroll
-                    for (int c = 0; c < NR; c += 16) {
+                    for (int c = 0; c < NR / 16; ++c) {
                         float f[16];
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) {
-                            x[c + r] -= row_factor[c + r];
-                            f[r] = exch[c + r];
-                            l[c + r] *= f[r];
-                        }
-                        if (j > w.begin) {
+                        for (int r = 0; r < 16; ++r)
+                            f[r] = row_factor[16 * c + r];
 #pragma unroll
-                            for (int part = 0; part < 2; ++part) {
+                        for (int r = 0; r < 8; ++r) {
+                            l[8 * c + r] = mul_f32x2(l[8 * c + r], f32x2(f[2 * r], f[2 * r + 1]));
+                            if (kKeep)
+                                x[kKeep ? c : 0][r] = add_f32x2(x[kKeep ? c : 0][r], f32x2(-row_shift[16 * c + 2 * r],
+                                                                                           -row_shift[16 * c + 2 * r + 1]));
+                        }
+                        if (j > first) {
+#pragma unroll
+                            for (int part = 0; part < QP; ++part) {
                                 uint32_t o[16];
-                                const uint32_t at = tmem + lanes + L::kTmemO + part * NR + c;
-                                tmem_ld16_wait(at, o);
+                                __syncwarp();
+                                tmem_ld16_wait(t_o + part * NR + 16 * c, o);
 #pragma unroll
                                 for (int r = 0; r < 16; ++r)
                                     o[r] = __float_as_uint(__uint_as_float(o[r]) * f[r]);
-                                tmem_st16(at, o);
+                                tmem_st16(t_o + part * NR + 16 * c, o);
                             }
                         }
                     }
@@ -645,9 +726,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 }
                 // ---- V rows that no row of the item sees are zero; a NaN that only some see is taken out and kept
                 // in mind
-                if (edge || __any_sync(0xffffffffu, !valid)) {
-                    ok = ok && wait_bar(smem_u32(&bars->v_full[ns % NV]), (ns / NV) & 1, abort, kErrPagedSoftmax + 2);
-                    const uint32_t row = sV + (ns % NV) * L::kTileBytes + key * D;
+                if (edge) {
+                    ok = ok && wait_bar(smem_u32(&bars->v_full[vn % NV]), (vn / NV) & 1, abort, kErrPagedSoftmax + 2);
+                    const uint32_t row = sV + (vn % NV) * L::kTileBytes + tid * D;
                     if (ok && !valid) {
 #pragma unroll
                         for (int c = 0; c < D / 16; ++c)
@@ -655,12 +736,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     } else if (ok && pos >= full) {
                         for (int c = 0; c < D / 4; ++c) {
                             // 16-byte chunk c / 4 of the row lies at its swizzled place
-                            const int chunk = D == 128 ? (c / 4) ^ (key & 7) : (c / 4) ^ ((key >> 1) & 3);
-                            uint32_t* at = reinterpret_cast<uint32_t*>(smem + L::kOffV + (ns % NV) * L::kTileBytes + key * D +
+                            const int chunk = D == 128 ? (c / 4) ^ (tid & 7) : (c / 4) ^ ((tid >> 1) & 3);
+                            uint32_t* at = reinterpret_cast<uint32_t*>(smem + L::kOffV + (vn % NV) * L::kTileBytes + tid * D +
                                                                        chunk * 16 + (c & 3) * 4);
                             uint32_t u = *at;
-                            const uint32_t mag = u & 0x7f7f7f7fu;
-                            const uint32_t hit = (mag + 0x01010101u) & 0x80808080u;      // bytes 0x7F and 0xFF
+                            const uint32_t hit = ((u & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;    // bytes 0x7F, 0xFF
                             if (hit) {
                                 for (int e = 0; e < 4; ++e)
                                     if (hit >> (8 * e + 7) & 1) {
@@ -672,59 +752,87 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         }
                     }
                 }
-                // ---- weights into two E4M3 parts
-                if (ok && ns >= (uint32_t)NW)
-                    ok = wait_bar(smem_u32(&bars->pv_done[wbuf]), (ns / NW - 1) & 1, abort, kErrPagedSoftmax + 3);
-                const uint32_t w_row = sW + wbuf * L::kWBytes + key * L::kWRow;
+                // ---- weights into E4M3 parts: first to 11 bits, whose differences are exact
+                if (ok && ns > 0)
+                    ok = wait_bar(smem_u32(&bars->pv_done[g]), (ns - 1) & 1, abort, kErrPagedSoftmax + 3);
+                const uint32_t w_row = sW + g * L::kWBytes + tid * L::kWRow;
                 constexpr int kChunks = L::kWRow / 16;
-                const int swz = kChunks == 2 ? (key >> 2) & 1 : kChunks == 4 ? (key >> 1) & 3 : key & 7;
+                const int swz = kChunks == 2 ? (tid >> 2) & 1 : kChunks == 4 ? (tid >> 1) & 3 : tid & 7;
+                const uint64_t rvs2 = f32x2(rvs, rvs);
 #pragma unroll
-                for (int c = 0; c < NR; c += 16) {
-                    uint32_t up[4], lo[4];
+                for (int c = 0; c < NR / 16; ++c) {
+                    if (!kKeep)
+                        logits(16 * c, x[0]);
+                    uint32_t part[QP][4];
 #pragma unroll
-                    for (int r = 0; r < 16; r += 4) {
-                        float y[4];
+                    for (int r = 0; r < 8; ++r) {
+                        float a, b;
+                        f32x2_split(x[kKeep ? c : 0][r], a, b);
+                        a = ex2_approx(a);
+                        b = ex2_approx(b);
+                        l[8 * c + r] = fma_f32x2(f32x2(a, b), rvs2, l[8 * c + r]);
+                        uint32_t rest = f32x2_to_f16x2(a, b);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            y[e] = ex2_approx(x[c + r + e] + kLog2W);
-                            l[c + r + e] = fmaf(y[e], rvs, l[c + r + e]);
+                        for (int k = 0; k < QP; ++k) {
+                            const uint32_t e = f16x2_to_e4m3x2(rest);
+                            part[k][r / 2] = r & 1 ? part[k][r / 2] | (e << 16) : e;
+                            if (k + 1 < QP)                                 // 16 (rest - part)
+                                rest = mul_f16x2(add_f16x2(rest, e4m3x2_to_f16x2((uint16_t)e) ^ 0x80008000u), 0x4c004c00u);
                         }
-                        const uint16_t a = f32x2_to_e4m3x2(y[0], y[1]), b = f32x2_to_e4m3x2(y[2], y[3]);
-                        const float2 fa = f16x2_to_f32x2(e4m3x2_to_f16x2(a)), fb = f16x2_to_f32x2(e4m3x2_to_f16x2(b));
-                        up[r / 4] = (uint32_t)a | ((uint32_t)b << 16);
-                        lo[r / 4] = (uint32_t)f32x2_to_e4m3x2((y[0] - fa.x) * 16.f, (y[1] - fa.y) * 16.f) |
-                                    ((uint32_t)f32x2_to_e4m3x2((y[2] - fb.x) * 16.f, (y[3] - fb.y) * 16.f) << 16);
                     }
                     if (ok) {
-                        st_shared_v4(w_row + (uint32_t)(((c / 16) ^ swz) * 16), up[0], up[1], up[2], up[3]);
-                        st_shared_v4(w_row + (uint32_t)(((c / 16 + kChunks / 2) ^ swz) * 16), lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+                        for (int k = 0; k < QP; ++k)
+                            st_shared_v4(w_row + (uint32_t)(((k * (NR / 16) + c) ^ swz) * 16), part[k][0], part[k][1], part[k][2],
+                                         part[k][3]);
                     }
+                }
+                if (!kKeep) {
+                    tc_fence_before_sync();
+                    mbar_arrive(smem_u32(&bars->s_free[g]));
                 }
                 fence_proxy_async_smem();
                 if (ok)
-                    mbar_arrive(smem_u32(&bars->w_full[wbuf]));
+                    mbar_arrive(smem_u32(&bars->w_full[g]));
             }
             // ---- the piece's result
-            if (ok)
-                ok = wait_bar(smem_u32(&bars->pv_done[(ns - 1) % NW]), ((ns - 1) / NW) & 1, abort, kErrPagedSoftmax + 4);
+            const bool took = first < w.end;                               // this warpgroup had a tile
+            if (ok && took)
+                ok = wait_bar(smem_u32(&bars->pv_done[g]), (ns - 1) & 1, abort, kErrPagedSoftmax + 4);
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
-                const float s = rope::group_sum<32>(l[r]);
+                float a, b;
+                f32x2_split(l[r / 2], a, b);
+                const float s = rope::group_sum<32>(r & 1 ? b : a);
                 if (lane == (r & 31))
-                    exch[warp * NR + r] = s;
+                    exch[(warp & 3) * NR + r] = s;
             }
-            ok = named_bar_all(kBarSoftmax, kSoftmax, ok);
+            ok = named_bar_all(kBarAll, L::kSoftmax, ok);
             if (!ok)
                 break;
             tc_fence_after_sync();
             const bool whole = w.begin == 0 && w.end == w.n;
             const long long slot = (long long)blockIdx.x * 2 + (w.begin > 0 ? 0 : 1);
             if (threadIdx.x < NR) {
+                // join the warpgroups: sums s_g of exp2(logit - max_g + log2 112), weights of their O^T
                 const int r = threadIdx.x;
-                const float s = (exch[r] + exch[NR + r]) + (exch[2 * NR + r] + exch[3 * NR + r]);
-                row_factor[r] = s == 0.f ? 0.f : 1.f / s;
-                // sum of exp2(s - max) = s / 112; -inf for a row that has seen no key
-                const float lse2 = s == 0.f ? -INFINITY : row_max[r] + (log2f(s) - kLog2W);
+                float s[G], nm[G], m = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < G; ++k) {
+                    const float* e = group_rows + 7 * NR * k + 3 * NR + r;
+                    s[k] = (e[0] + e[NR]) + (e[2 * NR] + e[3 * NR]);
+                    nm[k] = group_rows[7 * NR * k + r];
+                    m = s[k] == 0.f ? m : fmaxf(m, kLog2W - nm[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < G; ++k) {
+                    nm[k] = s[k] == 0.f ? 0.f : exp2f(kLog2W - nm[k] - m);
+                    sum = fmaf(s[k], nm[k], sum);
+                }
+#pragma unroll
+                for (int k = 0; k < G; ++k)
+                    group_rows[7 * NR * k + 2 * NR + r] = sum == 0.f ? 0.f : nm[k] / sum;
+                const float lse2 = sum == 0.f ? -INFINITY : m + (log2f(sum) - kLog2W);
                 if (r < it.rows) {
                     if (!whole) {
                         p.part_lse[slot * NR + r] = lse2;
@@ -734,137 +842,135 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     }
                 }
             }
-            named_bar_sync(kBarSoftmax, kSoftmax);
-            const int d = threadIdx.x;
-            const int nan_from = d < D ? nan_at[d] : INT_MAX;
+            named_bar_sync(kBarAll, L::kSoftmax);
+            // channel tid of 16 rows at a time, from every warpgroup's accumulator
+            const int groups = w.end - w.begin < G ? w.end - w.begin : G;
+            const int nan_from = tid < D ? nan_at[tid] : INT_MAX;
 #pragma unroll
-            for (int c = 0; c < NR; c += 16) {
-                uint32_t a[16], b[16];
-                __syncwarp();
-                tmem_ld16_wait(tmem + lanes + L::kTmemO + c, a);
-                tmem_ld16_wait(tmem + lanes + L::kTmemO + NR + c, b);
-                if (c + 16 == NR) {
-                    tc_fence_before_sync();
-                    mbar_arrive(smem_u32(&bars->o_free));
+            for (int c = 0; c < NR / 16; ++c) {
+                if (NR / 16 >= G && c % G != g)
+                    continue;
+                if (NR / 16 < G && g > 0)
+                    continue;
+                float o[16];
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    o[r] = 0.f;
+#pragma unroll
+                for (int k = 0; k < G; ++k) {
+                    if (k >= groups)
+                        continue;
+                    float unit = 1.f;
+#pragma unroll
+                    for (int part = 0; part < QP; ++part, unit *= 1.f / 16.f) {
+                        uint32_t a[16];
+                        __syncwarp();
+                        tmem_ld16_wait(tmem + lanes + k * L::kGroupCols + NR + part * NR + 16 * c, a);
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            o[r] = fmaf(__uint_as_float(a[r]), unit * group_rows[7 * NR * k + 2 * NR + 16 * c + r], o[r]);
+                    }
                 }
-                if (d < D) {
+                if (tid < D) {
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
-                        if (c + r >= it.rows)
+                        const int row = 16 * c + r;
+                        if (row >= it.rows)
                             break;
-                        float o = fmaf(__uint_as_float(b[r]), 1.f / 16.f, __uint_as_float(a[r])) * row_factor[c + r];
-                        if (row_last[c + r] >= nan_from)
-                            o = NAN;
+                        const float v = row_last[row] >= nan_from ? NAN : o[r];
                         if (!whole) {
-                            p.part_o[(slot * NR + c + r) * D + d] = o;
+                            p.part_o[(slot * NR + row) * D + tid] = v;
                         } else {
-                            const int i = (it.r0 + c + r) / p.group, hh = (it.r0 + c + r) % p.group;
+                            const int i = (it.r0 + row) / p.group, hh = (it.r0 + row) % p.group;
                             reinterpret_cast<uint16_t*>(p.O)[(long long)it.b * p.o_sb + (long long)i * p.o_ss +
-                                                             (long long)(w.h * p.group + hh) * p.o_sh + d] =
-                                (uint16_t)(pack2<kBF16>(o, 0.f) & 0xffffu);
+                                                             (long long)(w.h * p.group + hh) * p.o_sh + tid] =
+                                (uint16_t)(pack2<kBF16>(v, 0.f) & 0xffffu);
                         }
                     }
                 }
             }
-            named_bar_sync(kBarSoftmax, kSoftmax);             // the rows' numbers are read
+            tc_fence_before_sync();
+            mbar_arrive(smem_u32(&bars->o_free));
+            named_bar_sync(kBarAll, L::kSoftmax);              // the rows' numbers are read
         }
     }
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == kIssuer) {
         __syncwarp();
         tc_fence_after_sync();
         tmem_dealloc(tmem, L::kTmemCols);
     }
 }
 
-// Joins the pieces of the items that several CTAs share.  Block (c, r): if
-// the item that holds the first tile of CTA c's share began in CTA c - 1's, its
-// row r is the sum over the CTAs c - 1 .. of
+// Joins the pieces of the items that several CTAs share.  Block (c, y): if
+// joins[c] names an item, its rows y kRows .. are sums over its pieces, slot 1 of CTA c - 1
+// and slot 0 of CTAs c .. :
 //     O = sum_k exp2(lse_k - LSE) O_k,   LSE = log2 sum_k exp2(lse_k).
+// Few rows have a block each, whose threads share the pieces out (there may be
+// hundreds); many rows, whose items have few pieces, go eight to a block.
 constexpr int kJoinThreads = 256;
-
-struct JoinShared {
-    long long total, x, x_first;
-    long long warp_sums[16];
-    float o[kJoinThreads];
-    float w[kJoinThreads];
-};
 
 template <int D, bool kBF16, int NR>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const Params p)
 {
     constexpr int kSlices = kJoinThreads / D;
-    __shared__ JoinShared sh;
+    constexpr int kRows = NR == 16 ? 1 : 8;
+    __shared__ float sh_o[kJoinThreads], sh_w[kJoinThreads];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int c = blockIdx.x + 1, r = blockIdx.y;
-    find_share<NR, kJoinThreads>(p, c, &sh);
-    const long long total = sh.total;
-    const long long t = share_begin(total, c, p.ctas);
-    if (t >= total)
+    const int c = blockIdx.x + 1;
+    const int4 join = p.joins[c];
+    const int n = join.w;
+    if (n == 0)
         return;
     Piece w;
-    w.x = sh.x;
-    w.n = entry_tiles<NR>(p, w.x);
-    w.h = (int)((t - sh.x_first) / w.n);
-    const long long first = sh.x_first + (long long)w.h * w.n;       // the item's first tile
-    if (first == t || first < share_begin(total, c - 1, p.ctas))
-        return;
+    w.x = (long long)(((unsigned long long)(unsigned)join.y << 32) | (unsigned)join.x);
+    w.h = join.z;
     const Item it = item_of<NR>(p, w);
-    if (r >= it.rows)
-        return;
-    // last CTA: the one that holds tile first + n - 1
-    int last = c;
-    {
-        int hi = p.ctas - 1;                               // shares are in order: bisection
-        while (last < hi) {
-            const int mid = (last + hi + 1) >> 1;
-            if (share_begin(total, mid, p.ctas) <= first + w.n - 1)
-                last = mid;
-            else
-                hi = mid - 1;
-        }
-    }
-    const int n = last - c + 2;                            // pieces: slot 1 of CTA c - 1, slot 0 of c .. last
     auto slot_of = [&](int k) -> long long { return k == 0 ? (long long)(c - 1) * 2 + 1 : (long long)(c - 1 + k) * 2; };
-    float m = -INFINITY;
-    for (int k = threadIdx.x; k < n; k += kJoinThreads)
-        m = fmaxf(m, p.part_lse[slot_of(k) * NR + r]);
-    sh.w[threadIdx.x] = m;
-    __syncthreads();
-    for (int s = kJoinThreads / 2; s > 0; s >>= 1) {
-        if (threadIdx.x < s)
-            sh.w[threadIdx.x] = fmaxf(sh.w[threadIdx.x], sh.w[threadIdx.x + s]);
+    for (int r = blockIdx.y * kRows; r < min(it.rows, (int)(blockIdx.y + 1) * kRows); ++r) {
+        float m = -INFINITY;
+        for (int k = threadIdx.x; k < n; k += kJoinThreads)
+            m = fmaxf(m, p.part_lse[slot_of(k) * NR + r]);
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+        if ((threadIdx.x & 31) == 0)
+            sh_w[threadIdx.x >> 5] = m;
         __syncthreads();
-    }
-    m = sh.w[0];
-    __syncthreads();
-    const int d = threadIdx.x % D, slice = threadIdx.x / D;
-    float o = 0.f, den = 0.f;
-#pragma unroll 4
-    for (int k = slice; k < n; k += kSlices) {
-        const long long slot = slot_of(k) * NR + r;
-        const float z = p.part_lse[slot];
-        const float f = z == -INFINITY ? 0.f : exp2f(z - m);   // a NaN stays one
-        den += f;
-        o = fmaf(f, p.part_o[slot * D + d], o);
-    }
-    sh.o[threadIdx.x] = o;
-    sh.w[threadIdx.x] = den;
-    __syncthreads();
-    if (slice == 0) {
-        for (int s = 1; s < kSlices; ++s) {
-            o += sh.o[s * D + d];
-            den += sh.w[s * D + d];
+#pragma unroll
+        for (int s = 0; s < kJoinThreads / 32; ++s)
+            m = fmaxf(m, sh_w[s]);
+        __syncthreads();
+        const int d = threadIdx.x % D, slice = threadIdx.x / D;
+        float o = 0.f, den = 0.f;
+#pragma unroll 8
+        for (int k = slice; k < n; k += kSlices) {
+            const long long slot = slot_of(k) * NR + r;
+            const float z = p.part_lse[slot];
+            const float f = z == -INFINITY ? 0.f : exp2f(z - m);   // a NaN stays one
+            den += f;
+            o = fmaf(f, p.part_o[slot * D + d], o);
         }
-        const int i = (it.r0 + r) / p.group, hh = (it.r0 + r) % p.group;
-        const long long head = (long long)w.h * p.group + hh;
-        o = den == 0.f ? 0.f : o / den;
-        reinterpret_cast<uint16_t*>(p.O)[(long long)it.b * p.o_sb + (long long)i * p.o_ss + head * p.o_sh + d] =
-            (uint16_t)(pack2<kBF16>(o, 0.f) & 0xffffu);
-        if (p.lse && d == 0)
-            p.lse[((long long)it.b * p.Hq + head) * p.Sq + i] = den == 0.f ? -INFINITY : (m + log2f(den)) * kLn2;
+        sh_o[threadIdx.x] = o;
+        sh_w[threadIdx.x] = den;
+        __syncthreads();
+        if (slice == 0) {
+#pragma unroll
+            for (int s = 1; s < kSlices; ++s) {
+                o += sh_o[s * D + d];
+                den += sh_w[s * D + d];
+            }
+            const int i = (it.r0 + r) / p.group, hh = (it.r0 + r) % p.group;
+            const long long head = (long long)w.h * p.group + hh;
+            o = den == 0.f ? 0.f : o / den;
+            reinterpret_cast<uint16_t*>(p.O)[(long long)it.b * p.o_sb + (long long)i * p.o_ss + head * p.o_sh + d] =
+                (uint16_t)(pack2<kBF16>(o, 0.f) & 0xffffu);
+            if (p.lse && d == 0)
+                p.lse[((long long)it.b * p.Hq + head) * p.Sq + i] = den == 0.f ? -INFINITY : (m + log2f(den)) * kLn2;
+        }
+        __syncthreads();
     }
 }
 

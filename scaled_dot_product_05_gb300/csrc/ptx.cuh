@@ -479,6 +479,36 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b)
     return d;
 }
 
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Two floats -> f16x2 (round to nearest even), `lo` in the low half.
+__device__ __forceinline__ uint32_t f32x2_to_f16x2(float lo, float hi)
+{
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// f16x2 -> two E4M3 bytes (round to nearest even, saturate to +-448).
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t v)
+{
+    uint16_t h;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(v));
+    return h;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // Two floats -> two E4M3 bytes (round to nearest even, saturate to +-448):
 // `lo` in the low byte.
 __device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float lo, float hi)
