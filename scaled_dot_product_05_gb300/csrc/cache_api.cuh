@@ -341,7 +341,8 @@ constexpr int kPagedCtas = 304;
 int paged_tile_rows(int Sq, int group, bool bf16)
 {
     const long long rows = static_cast<long long>(Sq) * group;
-    return rows <= 16 ? 16 : rows <= 32 || !bf16 ? 32 : 64;
+    (void)bf16;
+    return rows <= 8 ? 8 : 16;
 }
 
 // The pieces' results, their LSE, and what is to join.
@@ -367,7 +368,7 @@ cudaError_t launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const sdp
     cudaError_t e = launch_pdl(true, paged_attn_kernel<D, kBF16, NR>, dim3(p.ctas), dim3(L::kThreads), L::kSmemBytes,
                                stream, tk, tv, p);
     const long long rows = static_cast<long long>(p.Sq) * p.group;
-    const unsigned blocks = static_cast<unsigned>(NR == 16 ? rows : (rows < NR ? rows + 7 : NR) / 8);
+    const unsigned blocks = static_cast<unsigned>(NR <= 16 ? (rows < NR ? rows : NR) : (rows < NR ? rows + 7 : NR) / 8);
     if (e == cudaSuccess && p.ctas > 1)
         e = launch_pdl(true, paged_join_kernel<D, kBF16, NR>, dim3(p.ctas - 1, blocks), dim3(kJoinThreads), 0, stream, p);
     return e;
@@ -377,13 +378,7 @@ template <int D, bool kBF16>
 cudaError_t launch_paged_rows(int nr, const CUtensorMap& tk, const CUtensorMap& tv, const sdpa::paged::Params& p, int dev,
                               cudaStream_t s)
 {
-    if (nr == 16)
-        return launch_paged<D, kBF16, 16>(tk, tv, p, dev, s);
-    if constexpr (kBF16) {
-        if (nr == 64)
-            return launch_paged<D, kBF16, 64>(tk, tv, p, dev, s);
-    }
-    return launch_paged<D, kBF16, 32>(tk, tv, p, dev, s);
+    return nr == 8 ? launch_paged<D, kBF16, 8>(tk, tv, p, dev, s) : launch_paged<D, kBF16, 16>(tk, tv, p, dev, s);
 }
 
 }  // namespace
@@ -579,9 +574,17 @@ sdpa_status_t sdpa_fwd_paged(const void* Q, const sdpa_cache_t* cache, const int
     p.part_o = static_cast<float*>(workspace);
     p.part_lse = p.part_o + static_cast<long long>(p.ctas) * 2 * nr * D;
     p.joins = reinterpret_cast<int4*>(p.part_lse + static_cast<long long>(p.ctas) * 2 * nr);
+    // L2 fetches no more than a slot's bytes where the slots of a head lie
+    // apart: 256-byte fetches would bring in the neighbour head's half each
+    // time
+    auto map = [&](CUtensorMap* m, const void* base, const Strides& st) {
+        return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, Hkv, p.page, p.n_pages, st, 1, p.page,
+                        st.s == D    ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                        : D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                   : CU_TENSOR_MAP_L2_PROMOTION_L2_64B);
+    };
     CUtensorMap tk, tv;
-    if (!make_map(&tk, cache->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, Hkv, p.page, p.n_pages, ck.st, 1, p.page) ||
-        !make_map(&tv, cache->v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, Hkv, p.page, p.n_pages, cv.st, 1, p.page))
+    if (!map(&tk, cache->k, ck.st) || !map(&tv, cache->v, cv.st))
         return cuda_fail(cudaErrorInvalidValue);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == SDPA_DTYPE_BF16;

@@ -69,17 +69,18 @@ constexpr float kLog2W = 6.807354922057604f;   // log2(112)
 template <int D, bool kBF16, int NR>
 struct PagedLayout {
     static_assert(D == 64 || D == 128, "head dimension");
-    static_assert(NR == 16 || NR == 32 || (NR == 64 && kBF16), "rows of a tile");
+    static_assert(NR == 8 || NR == 16, "rows of a tile");
     static constexpr int kParts = kBF16 ? 2 : 3;
-    static constexpr int kGroups = NR == 64 ? 1 : 2;            // softmax warpgroups
+    static constexpr int kGroups = 2;                           // softmax warpgroups
     static constexpr int kSoftmax = 128 * kGroups;              // warps 0 ..
     static constexpr int kThreads = kSoftmax + 64;              // then TMA producer, MMA issuer
     static constexpr int kTileBytes = kTileKeys * D;            // a K or V tile
     // depth of the rings: what two CTAs fit into an SM
-    static constexpr int kStagesK = D == 64 ? 4 : NR == 16 ? 3 : 2;
-    static constexpr int kStagesV = D == 64 ? 4 : NR < 64 && kBF16 ? 3 : 2;
-    static constexpr int kQPartBytes = NR * D;
-    static constexpr int kWRow = (kBF16 ? 2 : 4) * NR;          // bytes of a key's weights (a power of two)
+    static constexpr int kStagesK = D == 64 ? 5 : 3;
+    static constexpr int kStagesV = D == 64 ? 5 : NR == 16 && !kBF16 ? 2 : 3;
+    static constexpr int kQRows = 16;                           // columns of S^T: 16 at least
+    static constexpr int kQPartBytes = kQRows * D;
+    static constexpr int kWRow = kParts * NR <= 32 ? 32 : 64;   // bytes of a key's weights
     static constexpr int kWBytes = kTileKeys * kWRow;
     static constexpr int kOffK = 0;
     static constexpr int kOffV = kOffK + kStagesK * kTileBytes;
@@ -89,15 +90,16 @@ struct PagedLayout {
     // per row: q's scale, last key; per warpgroup: negative maximum, shift, factor, 4 x exchange; per channel: NaN
     static constexpr int kRowsBytes = 4 * (2 * NR + 7 * NR * kGroups + D);
     static constexpr int kOffBar = (kOffRows + kRowsBytes + 15) / 16 * 16;
-    static constexpr int kBarBytes = 384;
+    static constexpr int kBarBytes = 448;
     static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;                // + alignment
     static_assert(kOffQ % 1024 == 0 && kOffW % 1024 == 0, "swizzle atoms");
     static_assert(D == 128 || kGroups * kWBytes + kParts * kQPartBytes >= kTileBytes, "operand of the unused half");
     static_assert(2 * (kSmemBytes + 1024) <= 233472, "two CTAs per SM");
     // a warpgroup's columns: S^T, then the parts of O^T
-    static constexpr int kGroupCols = (1 + kParts) * NR;
-    static constexpr uint32_t kTmemCols = kGroups * kGroupCols <= 64 ? 64 : kGroups * kGroupCols <= 128 ? 128 : 256;
-    static_assert(kGroups * kGroupCols <= 256, "two CTAs per SM");
+    static constexpr int kOCols = (kParts * NR + 15) / 16 * 16;
+    static constexpr int kGroupCols = kQRows + kOCols;
+    static constexpr uint32_t kTmemCols = kGroups * kGroupCols <= 64 ? 64 : 128;
+    static_assert(kGroups * kGroupCols <= 128, "two CTAs per SM");
 };
 
 template <int NK, int NV, int kGroups>
@@ -258,6 +260,29 @@ __device__ __forceinline__ Item item_of(const Params& p, const Piece& w)
     return t;
 }
 
+// Sums over the warp of N values a lane: lanes r 32 / N .. get that of s[r].
+// Each step hands half of the values to the lane across and adds the other
+// half of its, then what is left goes round.
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&s)[N], int lane)
+{
+#pragma unroll
+    for (int h = N / 2; h > 0; h >>= 1) {
+        const bool up = lane & (32 / N * h);
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+            const float give = up ? s[i] : s[i + h];
+            const float keep = up ? s[i + h] : s[i];
+            s[i] = keep + __shfl_xor_sync(0xffffffffu, give, 32 / N * h);
+        }
+    }
+    float v = s[0];
+#pragma unroll
+    for (int m = 32 / N / 2; m > 0; m >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, m);
+    return v;
+}
+
 // An item whose pieces several CTAs have is joined by the block of the second
 // of them, c: joins[c].w is the number of pieces (0: nothing to join there).
 __device__ __forceinline__ int4 join_of(const Params& p, long long total, const Piece& w)
@@ -291,7 +316,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     auto* bars = reinterpret_cast<Bars*>(smem + L::kOffBar);
     static_assert(sizeof(Bars) <= L::kBarBytes, "barrier block");
     volatile int* abort = &bars->abort;
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // known to be the same in the warp
     const int lane = threadIdx.x & 31;
     const uint32_t sK = smem_u32(smem + L::kOffK), sV = smem_u32(smem + L::kOffV);
     const uint32_t sW = smem_u32(smem + L::kOffW), sQ = smem_u32(smem + L::kOffQ);
@@ -346,18 +371,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         bool ok = true;
         for (; ok && more; more = next_piece<NR>(p, w)) {
             const Item it = item_of<NR>(p, w);
-            auto page_of = [&](int tile) -> int {
+            // table entries are read three tiles ahead and looked at when their
+            // tile comes, so that no tile waits for one
+            auto entry_of = [&](int tile) -> int {
                 const int ord = tile * ppt + lane;
-                if (lane >= ppt || ord >= p.max_pages || ord << p.page_shift >= it.keys)
-                    return -1;
-                const int id = p.table[(long long)it.b * p.max_pages + ord];
-                return (unsigned)id < (unsigned)p.n_pages ? id : -1;
+                return lane < ppt && tile < w.end && ord << p.page_shift < it.keys
+                           ? p.table[(long long)it.b * p.max_pages + ord]
+                           : -1;
             };
-            int next = page_of(w.begin);
+            int ahead[3] = {entry_of(w.begin), entry_of(w.begin + 1), entry_of(w.begin + 2)};
             for (int j = w.begin; ok && j < w.end; ++j, ++n) {
-                const int id = next;
-                if (j + 1 < w.end)
-                    next = page_of(j + 1);
+                const int id = (unsigned)ahead[0] < (unsigned)p.n_pages ? ahead[0] : -1;
+                ahead[0] = ahead[1];
+                ahead[1] = ahead[2];
+                ahead[2] = entry_of(j + 3);
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * p.page * D;
                 const uint32_t ks = n % NK, vs = n % NV;
                 if (n >= NK)
@@ -398,21 +425,21 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         if (lane == 0) {
             constexpr int kSwz = D;                        // bytes of a K / V row = swizzle span
             constexpr uint32_t kSwzCode = D == 128 ? 2u : 4u;
-            constexpr uint32_t kWCode = L::kWRow == 32 ? 6u : L::kWRow == 64 ? 4u : 2u;
-            constexpr uint32_t idesc_s = idesc_make(0u, kTileKeys, NR, false);
+            constexpr uint32_t kWCode = L::kWRow == 32 ? 6u : 4u;
+            constexpr uint32_t idesc_s = idesc_make(0u, kTileKeys, L::kQRows, false);
             // V^T: 128 rows of which D are the tile's; at D = 64 the others are
             // whatever lies behind the tile, and their results are not read
-            constexpr uint32_t idesc_o = idesc_make_amn(0u, 128, QP * NR, true);
+            constexpr uint32_t idesc_o = idesc_make_amn(0u, 128, L::kOCols, true);
             const uint32_t hi = (uint32_t)(smem_desc(0, 16, 8 * kSwz, kSwzCode) >> 32);
             const uint32_t hi_w = (uint32_t)(smem_desc(0, 16, 8 * L::kWRow, kWCode) >> 32);
             const uint32_t lbo_v = (uint32_t)(L::kTileBytes >> 4) << 16;
             uint32_t ks_n = 0, vs_n = 0, pieces = 0;       // S^T and O^T products issued, pieces begun
-            uint32_t ns[2] = {0, 0}, nv[2] = {0, 0};       // the same, of each warpgroup
+            uint32_t ns0 = 0, ns1 = 0, nv0 = 0, nv1 = 0;   // the same, of each warpgroup
             bool ok = true;
             for (; ok && more; more = next_piece<NR>(p, w), ++pieces) {
                 const int n = w.end - w.begin;
                 auto issue_s = [&](int g) -> bool {
-                    const uint32_t ks = ks_n % NK, done = ns[g];
+                    const uint32_t ks = ks_n % NK, done = g ? ns1 : ns0;
                     if (!wait_bar(smem_u32(&bars->k_full[ks]), (ks_n / NK) & 1, abort, kErrPagedMma) ||
                         (done > 0 && !wait_bar(smem_u32(&bars->s_free[g]), (done - 1) & 1, abort, kErrPagedMma + 1)))
                         return false;
@@ -428,7 +455,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     }
                     mma_commit(smem_u32(&bars->s_full[g]));
                     mma_commit(smem_u32(&bars->k_empty[ks]));
-                    ++ns[g];
+                    ns0 += g ? 0 : 1;
+                    ns1 += g ? 1 : 0;
                     ++ks_n;
                     return true;
                 };
@@ -441,7 +469,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         break;
                     const uint32_t vs = vs_n % NV;
                     ok = wait_bar(smem_u32(&bars->v_full[vs]), (vs_n / NV) & 1, abort, kErrPagedMma + 3) &&
-                         wait_bar(smem_u32(&bars->w_full[g]), nv[g] & 1, abort, kErrPagedMma + 4) &&
+                         wait_bar(smem_u32(&bars->w_full[g]), (g ? nv1 : nv0) & 1, abort, kErrPagedMma + 4) &&
                          (j > 0 || pieces == 0 ||
                           wait_bar(smem_u32(&bars->o_free), (pieces - 1) & 1, abort, kErrPagedMma + 5));
                     if (!ok)
@@ -451,11 +479,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     const uint32_t w_lo = ((sW + g * L::kWBytes) >> 4) | (1u << 16);
 #pragma unroll
                     for (int kk = 0; kk < kTileKeys / 32; ++kk)
-                        mma_f8_ss(tmem + g * L::kGroupCols + NR, desc_join(hi, v_lo + (uint32_t)((kk * 32 * kSwz) >> 4)),
+                        mma_f8_ss(tmem + g * L::kGroupCols + L::kQRows, desc_join(hi, v_lo + (uint32_t)((kk * 32 * kSwz) >> 4)),
                                   desc_join(hi_w, w_lo + (uint32_t)((kk * 32 * L::kWRow) >> 4)), idesc_o, j >= G || kk > 0);
                     mma_commit(smem_u32(&bars->pv_done[g]));
                     mma_commit(smem_u32(&bars->v_empty[vs]));
-                    ++nv[g];
+                    nv0 += g ? 0 : 1;
+                    nv1 += g ? 1 : 0;
                 }
             }
             mma_commit(smem_u32(&bars->drain));
@@ -476,7 +505,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         float* exch = row_nmax + 3 * NR;                                    // [4][NR]
         int* nan_at = reinterpret_cast<int*>(group_rows + 7 * NR * G);      // [D]: first masked key with a NaN there
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t t_s = tmem + lanes + g * L::kGroupCols, t_o = t_s + NR;
+        const uint32_t t_s = tmem + lanes + g * L::kGroupCols, t_o = t_s + L::kQRows;
         uint32_t ns = 0;                                                    // tiles of this warpgroup so far
         uint32_t nv = 0;                                                    // tiles of the CTA before this piece
         bool ok = true;
@@ -484,70 +513,57 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             const Item it = item_of<NR>(p, w);
             // ---- q into E4M3 parts, and each row's numbers
             {
-                constexpr int kPer = L::kSoftmax / NR;                      // threads of a row
-                constexpr int kSegs = (D / 16 + kPer - 1) / kPer;           // 16-element runs of a thread
-                const int r = threadIdx.x / kPer, sub = threadIdx.x % kPer;
+                constexpr int kPer = L::kSoftmax / L::kQRows;               // threads of a row
+                static_assert(kPer >= D / 16, "a 16-element run a thread");
+                const int r = threadIdx.x / kPer, seg = threadIdx.x % kPer;
                 const bool live = r < it.rows;
                 const int i = (it.r0 + r) / p.group, hh = (it.r0 + r) % p.group;
                 const uint16_t* q = reinterpret_cast<const uint16_t*>(p.Q) + (long long)it.b * p.q_sb + (long long)i * p.q_ss +
                                     (long long)(w.h * p.group + hh) * p.q_sh;
-                float v[kSegs][16];
-                float amax = 0.f;
-                bool finite = true;
-#pragma unroll
-                for (int s = 0; s < kSegs; ++s) {
-                    const int seg = sub + kPer * s;
-                    uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-                    if (live && seg < D / 16) {
-                        u[0] = reinterpret_cast<const uint4*>(q)[2 * seg];
-                        u[1] = reinterpret_cast<const uint4*>(q)[2 * seg + 1];
-                    }
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        rope::unpack4<kBF16>(make_uint2(u[c].x, u[c].y), &v[s][8 * c]);
-                        rope::unpack4<kBF16>(make_uint2(u[c].z, u[c].w), &v[s][8 * c + 4]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        finite = finite && fabsf(v[s][e]) < INFINITY;
-                        amax = fmaxf(amax, fabsf(v[s][e]));
-                    }
+                float v[16];
+                uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                if (live && seg < D / 16) {
+                    u[0] = reinterpret_cast<const uint4*>(q)[2 * seg];
+                    u[1] = reinterpret_cast<const uint4*>(q)[2 * seg + 1];
                 }
 #pragma unroll
-                for (int m = 1; m < kPer; m <<= 1) {
-                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-                    finite = __shfl_xor_sync(0xffffffffu, (int)finite, m) && finite;
+                for (int c = 0; c < 2; ++c) {
+                    rope::unpack4<kBF16>(make_uint2(u[c].x, u[c].y), &v[8 * c]);
+                    rope::unpack4<kBF16>(make_uint2(u[c].z, u[c].w), &v[8 * c + 4]);
                 }
-                const float qs = cache::pow2_scale(amax), inv = 1.f / qs;
+                // the largest magnitude; infinities and NaN have the largest bits
+                uint32_t top = 0;
 #pragma unroll
-                for (int s = 0; s < kSegs; ++s) {
-                    const int seg = sub + kPer * s;
-                    if (seg >= D / 16)
-                        continue;
-                    const int chunk = D == 128 ? seg ^ (r & 7) : seg ^ ((r >> 1) & 3);
+                for (int e = 0; e < 16; ++e)
+                    top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+#pragma unroll
+                for (int m = 1; m < kPer; m <<= 1)
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+                const bool finite = top < 0x7f800000u;
+                const float qs = cache::pow2_scale(__uint_as_float(top)), inv = 1.f / qs;
+                const int chunk = D == 128 ? seg ^ (r & 7) : seg ^ ((r >> 1) & 3);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    v[e] *= inv;
+                if (seg < D / 16) {
 #pragma unroll
                     for (int part = 0; part < QP; ++part) {
                         uint32_t o[4];
 #pragma unroll
                         for (int e = 0; e < 16; e += 4) {
-                            if (part == 0) {
-#pragma unroll
-                                for (int c = 0; c < 4; ++c)
-                                    v[s][e + c] *= inv;
-                            }
-                            const uint16_t lo = f32x2_to_e4m3x2(v[s][e], v[s][e + 1]);
-                            const uint16_t up = f32x2_to_e4m3x2(v[s][e + 2], v[s][e + 3]);
+                            const uint16_t lo = f32x2_to_e4m3x2(v[e], v[e + 1]);
+                            const uint16_t up = f32x2_to_e4m3x2(v[e + 2], v[e + 3]);
                             const float2 a = f16x2_to_f32x2(e4m3x2_to_f16x2(lo)), b = f16x2_to_f32x2(e4m3x2_to_f16x2(up));
-                            v[s][e] -= a.x;
-                            v[s][e + 1] -= a.y;
-                            v[s][e + 2] -= b.x;
-                            v[s][e + 3] -= b.y;
+                            v[e] -= a.x;
+                            v[e + 1] -= a.y;
+                            v[e + 2] -= b.x;
+                            v[e + 3] -= b.y;
                             o[e / 4] = (uint32_t)lo | ((uint32_t)up << 16);
                         }
                         st_shared_v4(sQ + part * L::kQPartBytes + r * D + chunk * 16, o[0], o[1], o[2], o[3]);
                     }
                 }
-                if (sub == 0) {
+                if (seg == 0 && r < NR) {
                     const long long last = p.causal ? it.start + i : it.start + it.count - 1;
                     row_scale[r] = finite ? qs * p.scale_log2 : NAN;
                     row_last[r] = !live || last < 0 ? -1 : (int)(last < it.keys ? last : it.keys - 1);
@@ -571,37 +587,37 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 l[r] = 0;
             bool seen = false;                                              // row tid has a maximum
             bool force = true;                                              // some row has none yet
-            // this thread's page, one and two tiles ahead, and its scales
-            auto page_of = [&](int tile) -> int {
+            // this thread's table entry two tiles of the warpgroup ahead, its
+            // scales one ahead: each is looked at when the next is on its way
+            const int* table = p.table + (long long)it.b * p.max_pages;
+            auto entry_of = [&](int tile) -> int {
                 const int pos = tile * kTileKeys + tid;
-                if (tile >= w.end || pos >= it.keys)
-                    return -1;
-                const int id = p.table[(long long)it.b * p.max_pages + (pos >> p.page_shift)];
-                if ((unsigned)id < (unsigned)p.n_pages)
-                    return id;
-                atomicCAS(&g_sdpa_error, 0u, (unsigned)cache::kErrPage);
-                return -1;
+                return tile < w.end && pos < it.keys ? table[pos >> p.page_shift] : INT_MIN;
             };
-            auto scales_of = [&](int id, float& a, float& b) {
+            auto scales_of = [&](int entry, float& a, float& b) -> bool {
                 a = b = 1.f;
-                if (id >= 0) {
-                    a = p.k.scale[(long long)id * p.Hkv + w.h];
-                    b = p.v.scale[(long long)id * p.Hkv + w.h];
+                const bool ok = (unsigned)entry < (unsigned)p.n_pages;
+                if (ok) {
+                    a = p.k.scale[(long long)entry * p.Hkv + w.h];
+                    b = p.v.scale[(long long)entry * p.Hkv + w.h];
+                } else if (entry != INT_MIN) {
+                    atomicCAS(&g_sdpa_error, 0u, (unsigned)cache::kErrPage);
                 }
+                return ok;
             };
-            int id = page_of(w.begin + g);
-            int id_next = page_of(w.begin + g + G);
+            int entry = entry_of(w.begin + g);
+            int entry_next = entry_of(w.begin + g + G);
             float k_scale, v_scale;
-            scales_of(id, k_scale, v_scale);
+            bool valid_next = scales_of(entry, k_scale, v_scale);
             const int first = w.begin + g;                                  // this warpgroup's first tile
             for (int j = first; j < w.end; j += G, ++ns) {
-                const bool valid = id >= 0;
+                const bool valid = valid_next;
                 const float ks = k_scale;
                 const float vs = fminf(fmaxf(v_scale, 8.673617379884035e-19f), 1.152921504606847e18f);   // 2^-60 .. 2^60
                 const float lvs = __log2f(vs), rvs = __fdividef(1.f, vs);
-                id = id_next;
-                scales_of(id, k_scale, v_scale);
-                id_next = page_of(j + 2 * G);
+                entry = entry_next;
+                entry_next = entry_of(j + 2 * G);
+                valid_next = scales_of(entry, k_scale, v_scale);
                 const uint32_t vn = nv + (uint32_t)(j - w.begin);           // V ring position
                 const int pos = j * kTileKeys + tid;
                 // tiles in which some row does not see some key, by the item's rows or by a page that is none
@@ -610,14 +626,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 tc_fence_after_sync();
                 // s + log2(v_scale): the logarithm of a weight but for the maximum, which comes off with log2(112) on top
                 const uint64_t ks2 = f32x2(ks, ks), lvs2 = f32x2(lvs, lvs);
-                auto logits = [&](int c, uint64_t (&x)[8]) -> float {
-                    uint32_t s[16];
-                    __syncwarp();
-                    tmem_ld16_wait(t_s + c, s);
+                uint64_t x[NR / 2];
+                float top;
+                {
+                    uint32_t s[NR];
+                    if constexpr (NR == 8)
+                        tmem_ld8_wait(t_s, s);
+                    else
+                        tmem_ld16_wait(t_s, s);
+                    tc_fence_before_sync();
+                    mbar_arrive(smem_u32(&bars->s_free[g]));
 #pragma unroll
-                    for (int r = 0; r < 16; r += 4) {
-                        const ulonglong2 sc = *reinterpret_cast<const ulonglong2*>(row_scale + c + r);
-                        const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(row_nmax + c + r);
+                    for (int r = 0; r < NR; r += 4) {
+                        const ulonglong2 sc = *reinterpret_cast<const ulonglong2*>(row_scale + r);
+                        const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(row_nmax + r);
                         x[r / 2] = fma_f32x2(f32x2(__uint_as_float(s[r]), __uint_as_float(s[r + 1])), mul_f32x2(sc.x, ks2),
                                              add_f32x2(nm.x, lvs2));
                         x[r / 2 + 1] = fma_f32x2(f32x2(__uint_as_float(s[r + 2]), __uint_as_float(s[r + 3])),
@@ -625,61 +647,38 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     }
                     if (edge) {
 #pragma unroll
-                        for (int r = 0; r < 16; r += 2) {
+                        for (int r = 0; r < NR; r += 2) {
                             float a, b;
                             f32x2_split(x[r / 2], a, b);
-                            x[r / 2] = f32x2(valid && pos <= row_last[c + r] ? a : -INFINITY,
-                                             valid && pos <= row_last[c + r + 1] ? b : -INFINITY);
+                            x[r / 2] = f32x2(valid && pos <= row_last[r] ? a : -INFINITY,
+                                             valid && pos <= row_last[r + 1] ? b : -INFINITY);
                         }
                     }
                     float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-                    for (int r = 0; r < 8; r += 2) {
+                    for (int r = 0; r < NR / 2; r += 2) {
                         float a, b;
                         f32x2_split(x[r], a, b);
                         m0 = fmax3(m0, a, b);
                         f32x2_split(x[r + 1], a, b);
                         m1 = fmax3(m1, a, b);
                     }
-                    return fmaxf(m0, m1);
-                };
-                // up to 32 rows stay in registers between the vote and the weights; 64 are read again
-                constexpr bool kKeep = NR <= 32;
-                uint64_t x[kKeep ? NR / 16 : 1][8];
-                float top = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < NR / 16; ++c)
-                    top = fmaxf(top, logits(16 * c, x[kKeep ? c : 0]));
-                if (kKeep) {
-                    tc_fence_before_sync();
-                    mbar_arrive(smem_u32(&bars->s_free[g]));
+                    top = fmaxf(m0, m1);
                 }
                 if (named_bar_any(bar_group, 128, top > kLag + kLog2W || force || !ok)) {
                     // ---- a weight above 2^kLag, or a row's first key: everything to the rows' new maxima
                     if (ok && j > first)
                         ok = wait_bar(smem_u32(&bars->pv_done[g]), (ns - 1) & 1, abort, kErrPagedSoftmax + 1);
+                    float mine = 0.f;                                       // lane r: the warp's maximum of row r
 #pragma unroll
-                    for (int c = 0; c < NR / 16; ++c) {
-                        uint64_t y[8];
-                        if (kKeep) {
-#pragma unroll
-                            for (int r = 0; r < 8; ++r)
-                                y[r] = x[kKeep ? c : 0][r];
-                        } else {
-                            logits(16 * c, y);
-                        }
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) {
-                            float a, b;
-                            f32x2_split(y[r / 2], a, b);
-                            float m = r & 1 ? b : a;
-#pragma unroll
-                            for (int o = 16; o > 0; o >>= 1)
-                                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                            if (lane == r)
-                                exch[(warp & 3) * NR + 16 * c + r] = m;
-                        }
+                    for (int r = 0; r < NR; ++r) {
+                        float a, b;
+                        f32x2_split(x[r / 2], a, b);
+                        const float m = warp_max(r & 1 ? b : a);
+                        mine = lane == r ? m : mine;
                     }
+                    if (lane < NR)
+                        exch[(warp & 3) * NR + lane] = mine;
                     ok = named_bar_all(bar_group, 128, ok);
                     if (!ok)
                         break;
@@ -695,30 +694,30 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     }
                     force = named_bar_any(bar_group, 128, waits);
                     tc_fence_after_sync();
+                    float f[NR];
 #pragma unroll
-                    for (int c = 0; c < NR / 16; ++c) {
-                        float f[16];
+                    for (int r = 0; r < NR; ++r)
+                        f[r] = row_factor[r];
 #pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            f[r] = row_factor[16 * c + r];
+                    for (int r = 0; r < NR / 2; ++r) {
+                        l[r] = mul_f32x2(l[r], f32x2(f[2 * r], f[2 * r + 1]));
+                        x[r] = add_f32x2(x[r], f32x2(-row_shift[2 * r], -row_shift[2 * r + 1]));
+                    }
+                    if (j > first) {
+#pragma unroll 1
+                        for (int part = 0; part < QP; ++part) {
+                            uint32_t o[NR];
+                            if constexpr (NR == 8)
+                                tmem_ld8_wait(t_o + part * NR, o);
+                            else
+                                tmem_ld16_wait(t_o + part * NR, o);
 #pragma unroll
-                        for (int r = 0; r < 8; ++r) {
-                            l[8 * c + r] = mul_f32x2(l[8 * c + r], f32x2(f[2 * r], f[2 * r + 1]));
-                            if (kKeep)
-                                x[kKeep ? c : 0][r] = add_f32x2(x[kKeep ? c : 0][r], f32x2(-row_shift[16 * c + 2 * r],
-                                                                                           -row_shift[16 * c + 2 * r + 1]));
-                        }
-                        if (j > first) {
-#pragma unroll
-                            for (int part = 0; part < QP; ++part) {
-                                uint32_t o[16];
-                                __syncwarp();
-                                tmem_ld16_wait(t_o + part * NR + 16 * c, o);
-#pragma unroll
-                                for (int r = 0; r < 16; ++r)
-                                    o[r] = __float_as_uint(__uint_as_float(o[r]) * f[r]);
-                                tmem_st16(t_o + part * NR + 16 * c, o);
-                            }
+                            for (int r = 0; r < NR; ++r)
+                                o[r] = __float_as_uint(__uint_as_float(o[r]) * f[r]);
+                            if constexpr (NR == 8)
+                                tmem_st8(t_o + part * NR, o);
+                            else
+                                tmem_st16(t_o + part * NR, o);
                         }
                     }
                     tmem_st_wait();
@@ -756,40 +755,35 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (ok && ns > 0)
                     ok = wait_bar(smem_u32(&bars->pv_done[g]), (ns - 1) & 1, abort, kErrPagedSoftmax + 3);
                 const uint32_t w_row = sW + g * L::kWBytes + tid * L::kWRow;
-                constexpr int kChunks = L::kWRow / 16;
-                const int swz = kChunks == 2 ? (tid >> 2) & 1 : kChunks == 4 ? (tid >> 1) & 3 : tid & 7;
+                const int swz = L::kWRow == 32 ? (tid >> 2) & 1 : (tid >> 1) & 3;
                 const uint64_t rvs2 = f32x2(rvs, rvs);
+                constexpr int kWords = NR / 4;                              // 32-bit words of a part
+                uint32_t words[(QP * kWords + 3) / 4 * 4];
 #pragma unroll
-                for (int c = 0; c < NR / 16; ++c) {
-                    if (!kKeep)
-                        logits(16 * c, x[0]);
-                    uint32_t part[QP][4];
+                for (int r = 0; r < NR / 2; ++r) {
+                    float a, b;
+                    f32x2_split(x[r], a, b);
+                    a = ex2_approx(a);
+                    b = ex2_approx(b);
+                    l[r] = fma_f32x2(f32x2(a, b), rvs2, l[r]);
+                    uint32_t rest = f32x2_to_f16x2(a, b);
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) {
-                        float a, b;
-                        f32x2_split(x[kKeep ? c : 0][r], a, b);
-                        a = ex2_approx(a);
-                        b = ex2_approx(b);
-                        l[8 * c + r] = fma_f32x2(f32x2(a, b), rvs2, l[8 * c + r]);
-                        uint32_t rest = f32x2_to_f16x2(a, b);
-#pragma unroll
-                        for (int k = 0; k < QP; ++k) {
-                            const uint32_t e = f16x2_to_e4m3x2(rest);
-                            part[k][r / 2] = r & 1 ? part[k][r / 2] | (e << 16) : e;
-                            if (k + 1 < QP)                                 // 16 (rest - part)
-                                rest = mul_f16x2(add_f16x2(rest, e4m3x2_to_f16x2((uint16_t)e) ^ 0x80008000u), 0x4c004c00u);
-                        }
-                    }
-                    if (ok) {
-#pragma unroll
-                        for (int k = 0; k < QP; ++k)
-                            st_shared_v4(w_row + (uint32_t)(((k * (NR / 16) + c) ^ swz) * 16), part[k][0], part[k][1], part[k][2],
-                                         part[k][3]);
+                    for (int k = 0; k < QP; ++k) {
+                        const uint32_t e = f16x2_to_e4m3x2(rest);
+                        uint32_t& at = words[k * kWords + r / 2];
+                        at = r & 1 ? at | (e << 16) : e;
+                        if (k + 1 < QP)                                     // 16 (rest - part)
+                            rest = mul_f16x2(add_f16x2(rest, e4m3x2_to_f16x2((uint16_t)e) ^ 0x80008000u), 0x4c004c00u);
                     }
                 }
-                if (!kKeep) {
-                    tc_fence_before_sync();
-                    mbar_arrive(smem_u32(&bars->s_free[g]));
+#pragma unroll
+                for (int i = QP * kWords; i < (QP * kWords + 3) / 4 * 4; ++i)
+                    words[i] = 0;
+                if (ok) {
+#pragma unroll
+                    for (int i = 0; i < (QP * kWords + 3) / 4; ++i)
+                        st_shared_v4(w_row + (uint32_t)((i ^ swz) * 16), words[4 * i], words[4 * i + 1], words[4 * i + 2],
+                                     words[4 * i + 3]);
                 }
                 fence_proxy_async_smem();
                 if (ok)
@@ -799,13 +793,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             const bool took = first < w.end;                               // this warpgroup had a tile
             if (ok && took)
                 ok = wait_bar(smem_u32(&bars->pv_done[g]), (ns - 1) & 1, abort, kErrPagedSoftmax + 4);
+            {
+                float s[NR];
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                float a, b;
-                f32x2_split(l[r / 2], a, b);
-                const float s = rope::group_sum<32>(r & 1 ? b : a);
-                if (lane == (r & 31))
-                    exch[(warp & 3) * NR + r] = s;
+                for (int r = 0; r < NR / 2; ++r)
+                    f32x2_split(l[r], s[2 * r], s[2 * r + 1]);
+                const float sum = warp_sums<NR>(s, lane);
+                if (lane % (32 / NR) == 0)
+                    exch[(warp & 3) * NR + lane / (32 / NR)] = sum;
             }
             ok = named_bar_all(kBarAll, L::kSoftmax, ok);
             if (!ok)
@@ -843,45 +838,40 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 }
             }
             named_bar_sync(kBarAll, L::kSoftmax);
-            // channel tid of 16 rows at a time, from every warpgroup's accumulator
-            const int groups = w.end - w.begin < G ? w.end - w.begin : G;
-            const int nan_from = tid < D ? nan_at[tid] : INT_MAX;
+            // channel tid of every row, from both warpgroups' accumulators
+            if (g == 0) {
+                const int groups = w.end - w.begin < G ? w.end - w.begin : G;
+                const int nan_from = tid < D ? nan_at[tid] : INT_MAX;
+                float o[NR];
 #pragma unroll
-            for (int c = 0; c < NR / 16; ++c) {
-                if (NR / 16 >= G && c % G != g)
-                    continue;
-                if (NR / 16 < G && g > 0)
-                    continue;
-                float o[16];
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
+                for (int r = 0; r < NR; ++r)
                     o[r] = 0.f;
-#pragma unroll
-                for (int k = 0; k < G; ++k) {
-                    if (k >= groups)
-                        continue;
+#pragma unroll 1
+                for (int k = 0; k < groups; ++k) {
                     float unit = 1.f;
-#pragma unroll
+#pragma unroll 1
                     for (int part = 0; part < QP; ++part, unit *= 1.f / 16.f) {
-                        uint32_t a[16];
-                        __syncwarp();
-                        tmem_ld16_wait(tmem + lanes + k * L::kGroupCols + NR + part * NR + 16 * c, a);
+                        uint32_t a[NR];
+                        const uint32_t at = tmem + lanes + k * L::kGroupCols + L::kQRows + part * NR;
+                        if constexpr (NR == 8)
+                            tmem_ld8_wait(at, a);
+                        else
+                            tmem_ld16_wait(at, a);
 #pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            o[r] = fmaf(__uint_as_float(a[r]), unit * group_rows[7 * NR * k + 2 * NR + 16 * c + r], o[r]);
+                        for (int r = 0; r < NR; ++r)
+                            o[r] = fmaf(__uint_as_float(a[r]), unit * group_rows[7 * NR * k + 2 * NR + r], o[r]);
                     }
                 }
                 if (tid < D) {
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int row = 16 * c + r;
-                        if (row >= it.rows)
+                    for (int r = 0; r < NR; ++r) {
+                        if (r >= it.rows)
                             break;
-                        const float v = row_last[row] >= nan_from ? NAN : o[r];
+                        const float v = row_last[r] >= nan_from ? NAN : o[r];
                         if (!whole) {
-                            p.part_o[(slot * NR + row) * D + tid] = v;
+                            p.part_o[(slot * NR + r) * D + tid] = v;
                         } else {
-                            const int i = (it.r0 + row) / p.group, hh = (it.r0 + row) % p.group;
+                            const int i = (it.r0 + r) / p.group, hh = (it.r0 + r) % p.group;
                             reinterpret_cast<uint16_t*>(p.O)[(long long)it.b * p.o_sb + (long long)i * p.o_ss +
                                                              (long long)(w.h * p.group + hh) * p.o_sh + tid] =
                                 (uint16_t)(pack2<kBF16>(v, 0.f) & 0xffffu);
@@ -915,7 +905,7 @@ template <int D, bool kBF16, int NR>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const Params p)
 {
     constexpr int kSlices = kJoinThreads / D;
-    constexpr int kRows = NR == 16 ? 1 : 8;
+    constexpr int kRows = NR <= 16 ? 1 : 8;
     __shared__ float sh_o[kJoinThreads], sh_w[kJoinThreads];
     grid_dependency_wait();
     grid_launch_dependents();

@@ -300,7 +300,7 @@ bool valid_scale(float x)
 // bytes, or 64 when a row is 64 bytes), 1 head, 128 rows, 1 batch}, matching
 // swizzle, zero fill out of bounds (ragged sequence tails).
 bool encode_map(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int elem_bytes, int D, int H, int S, int B,
-                const Strides& st, int box_h, int box_s)
+                const Strides& st, int box_h, int box_s, CUtensorMapL2promotion promotion)
 {
     EncodeTiledFn enc = encode_fn();
     if (!enc)
@@ -314,7 +314,7 @@ bool encode_map(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int 
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return enc(map, dt, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                swz == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // A tensor map depends only on these fields, so an encoded map can be reused
@@ -323,7 +323,7 @@ bool encode_map(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int 
 struct MapKey {
     const void* base;
     long long sb, ss, sh;
-    int dt, elem_bytes, D, H, S, B, box_h, box_s;
+    int dt, elem_bytes, D, H, S, B, box_h, box_s, promotion;
 };
 
 // Tensor maps of earlier calls, per host thread.  Encoding one costs ~2 us of
@@ -362,7 +362,8 @@ uint64_t map_key_hash(const MapKey& k)
 // box_h x box_s (heads x rows) per copy: 1 x 128, or G x 128 / G for packed
 // query tiles.
 bool make_map(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int elem_bytes, int D, int H, int S, int B,
-              const Strides& st, int box_h = 1, int box_s = sdpa::kBlockM)
+              const Strides& st, int box_h = 1, int box_s = sdpa::kBlockM,
+              CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B)
 {
     MapKey k;
     std::memset(&k, 0, sizeof k);                    // padding bytes take part in the comparison
@@ -378,6 +379,7 @@ bool make_map(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int el
     k.B = B;
     k.box_h = box_h;
     k.box_s = box_s;
+    k.promotion = static_cast<int>(promotion);
     MapCache& c = t_maps;
     const uint32_t h = static_cast<uint32_t>(map_key_hash(k));
     uint32_t free_slot = MapCache::kSlots;
@@ -391,7 +393,7 @@ bool make_map(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int el
             return true;
         }
     }
-    if (!encode_map(map, base, dt, elem_bytes, D, H, S, B, st, box_h, box_s))
+    if (!encode_map(map, base, dt, elem_bytes, D, H, S, B, st, box_h, box_s, promotion))
         return false;
     const uint32_t slot = free_slot != MapCache::kSlots
                               ? free_slot
