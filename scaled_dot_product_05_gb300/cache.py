@@ -5,12 +5,23 @@ marshalling only)."""
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
 
 from . import _DTYPE, _layout, _lse_ptr, _run, _stream_ptr, _abi
-from ._abi import lib
+from ._abi import check, lib
+
+_lib = None
+
+
+def _bound():
+    """The loaded library, kept here after the first call."""
+    global _lib
+    _lib = lib()
+    return _lib
+
 
 _WEIGHT_DTYPE = dict(_DTYPE)
 _WEIGHT_DTYPE[torch.float32] = _abi.SDPA_DTYPE_F32
@@ -26,65 +37,90 @@ def rope_table(n_pos: int, rot_dim: int, *, base: float = 10000.0, device="cuda"
     return torch.stack((a.cos(), a.sin()), dim=-1).to(torch.float32)
 
 
-def _on(device, *tensors):
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError("tensors must be on one CUDA device")
+# A decoding step makes a few such calls for each layer, and their kernels run
+# for a few microseconds: the checks below read each tensor attribute once and
+# compare device numbers instead of device objects.
+
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _call(device: int, fn, *args) -> None:
+    """Calls the library with the tensors' device current."""
+    if _get_device() == device:
+        status = fn(*args)
+        if status:
+            check(status)
+    else:
+        _run(device, fn, *args)
+
+
+@functools.lru_cache(maxsize=1024)
+def _layout_ref(strides):
+    """sdpa_layout_t of a 4-D tensor's strides, by value."""
+    if len(strides) != 4 or strides[3] != 1:
+        raise ValueError("tensors must be 4-D [B, S, H, D] views with a contiguous last dimension")
+    return ctypes.byref(_abi.Layout(*strides[:3]))
 
 
 def _strides(t):
     """The tensor's layout argument: None where it is contiguous."""
-    return None if t is None or t.is_contiguous() else ctypes.byref(_layout(t))
+    return None if t.is_contiguous() else _layout_ref(t.stride())
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _like(t, like, device, name):
+    """The layout argument of an output (or gradient) that the caller gave."""
+    if t.shape != like.shape or t.dtype != like.dtype or t.get_device() != device:
+        raise ValueError(f"{name} must be shaped and typed like its input, on its device")
+    return _strides(t)
 
 
 def _rope_arg(rope, interleaved, device):
     if rope is None:
         return None
-    if rope.device != device or rope.dtype != torch.float32 or rope.dim() != 3 or rope.shape[2] != 2 \
+    shape = rope.shape
+    if rope.get_device() != device or rope.dtype != torch.float32 or len(shape) != 3 or shape[2] != 2 \
             or not rope.is_contiguous():
         raise ValueError("rope must be a contiguous float32 table [n_pos, rot_dim / 2, 2] on the tensors' device")
-    return ctypes.byref(_abi.Rope(rope.data_ptr(), rope.shape[0], 2 * rope.shape[1], int(bool(interleaved))))
+    return ctypes.byref(_abi.Rope(rope.data_ptr(), shape[0], 2 * shape[1], 1 if interleaved else 0))
 
 
 def _int32(t, shape, device, name):
     if t is None:
         return None
-    if t.device != device or t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.get_device() != device or t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on the tensors' device")
     return t.data_ptr()
 
 
 def _weights(qw, kw, D, device):
-    dt = None
-    for w in (qw, kw):
+    """(address, address, dtype code) of the norm's weights."""
+    code, ptrs = _abi.SDPA_DTYPE_F32, [None, None]
+    for i, w in enumerate((qw, kw)):
         if w is None:
             continue
-        if w.device != device or tuple(w.shape) != (D,) or not w.is_contiguous() or (dt is not None and w.dtype != dt):
+        if w.get_device() != device or w.shape != (D,) or not w.is_contiguous() or \
+                (i and qw is not None and w.dtype != qw.dtype):
             raise ValueError("weights must be contiguous [D] tensors of one dtype on the tensors' device")
-        dt = w.dtype
-    return _WEIGHT_DTYPE.get(dt, 99) if dt is not None else _abi.SDPA_DTYPE_F32
+        code, ptrs[i] = _WEIGHT_DTYPE.get(w.dtype, 99), w.data_ptr()
+    return ptrs[0], ptrs[1], code
 
 
 def _pair_shapes(q, k):
-    if not q.is_cuda:
+    """(device, B, S, Hq, Hkv, D, layout arguments of q and k) of a pair of inputs."""
+    device = q.get_device()
+    if device < 0:
         raise ValueError("tensors must be CUDA tensors")
-    if q.dim() != 4:
+    shape = q.shape
+    if len(shape) != 4:
         raise ValueError("q must be [B, S, Hq, D]")
-    B, S, Hq, D = q.shape
+    B, S, Hq, D = shape
     if k is None:
-        return B, S, Hq, 0, D
-    if k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != D or k.dtype != q.dtype:
-        raise ValueError("k must be [B, S, Hkv, D] like q, with q's dtype")
-    return B, S, Hq, k.shape[2], D
-
-
-def _like(t, like, name):
-    if t is not None and (like is None or t.shape != like.shape or t.dtype != like.dtype):
-        raise ValueError(f"{name} must be shaped and typed like its input")
+        return device, B, S, Hq, 0, D, _strides(q), None
+    kshape = k.shape
+    if len(kshape) != 4 or kshape[0] != B or kshape[1] != S or kshape[3] != D or k.dtype != q.dtype \
+            or k.get_device() != device:
+        raise ValueError("k must be [B, S, Hkv, D] like q, with q's dtype, on its device")
+    return device, B, S, Hq, kshape[2], D, _strides(q), _strides(k)
 
 
 def sdpa_qk_norm_rope(q, k=None, q_out=None, k_out=None, *, norm: bool = True, q_weight=None, k_weight=None,
@@ -98,25 +134,42 @@ def sdpa_qk_norm_rope(q, k=None, q_out=None, k_out=None, *, norm: bool = True, q
     int32 [B, S] (None: 0 .. S - 1), weights [D] in float32 or q's dtype
     (None: ones).  Returns (q_out, k_out), allocated contiguous when not
     given; a tensor may be its own output."""
-    B, S, Hq, Hkv, D = _pair_shapes(q, k)
-    dev = q.device
+    dev, B, S, Hq, Hkv, D, lq, lk = _pair_shapes(q, k)
+    lqo = lko = kp = kop = None
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    if k_out is None and k is not None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
-    _like(q_out, q, "q_out")
-    _like(k_out, k, "k_out")
-    _on(dev, k, q_out, k_out)
-    _run(dev.index, lib().sdpa_qk_norm_rope, q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), B, S, Hq, Hkv, D,
-         _strides(q), _strides(k), _strides(q_out), _strides(k_out), int(bool(norm)), _ptr(q_weight), _ptr(k_weight),
-         _weights(q_weight, k_weight, D, dev), float(eps), _rope_arg(rope, interleaved, dev),
-         _int32(positions, (B, S), dev, "positions"), _DTYPE.get(q.dtype, 99), _stream_ptr(stream, dev.index))
+        q_out = q.new_empty((B, S, Hq, D))
+    else:
+        lqo = _like(q_out, q, dev, "q_out")
+    if k is not None:
+        if k_out is None:
+            k_out = k.new_empty((B, S, Hkv, D))
+        else:
+            lko = _like(k_out, k, dev, "k_out")
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    qw, kw, wdt = _weights(q_weight, k_weight, D, dev)
+    _call(dev, (_lib or _bound()).sdpa_qk_norm_rope, q.data_ptr(), kp, q_out.data_ptr(), kop, B, S, Hq, Hkv, D, lq, lk, lqo,
+          lko, 1 if norm else 0, qw, kw, wdt, eps, _rope_arg(rope, interleaved, dev),
+          _int32(positions, (B, S), dev, "positions"), _DTYPE.get(q.dtype, 99), _stream_ptr(stream, dev))
     return q_out, k_out
 
 
 def qk_norm_rope_bwd_workspace_bytes(B: int, S: int, Hq: int, Hkv: int, D: int) -> int:
     """Workspace bytes :func:`sdpa_qk_norm_rope_bwd` needs."""
     return int(lib().sdpa_qk_norm_rope_bwd_workspace_bytes(B, S, Hq, Hkv, D))
+
+
+def _weight_grad(t, D, device):
+    if t.dtype != torch.float32 or t.shape != (D,) or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError("weight gradients must be contiguous float32 [D] tensors on the tensors' device")
+    return t.data_ptr()
+
+
+def _workspace(t, device):
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the tensors' device")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def sdpa_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq=None, dk=None, *, norm: bool = True, q_weight=None, k_weight=None,
@@ -127,42 +180,43 @@ def sdpa_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq=None, dk=None, *, norm: bool 
     the same arguments.  The weights' gradients are float32 [D] (None without
     norm, and for an absent k); outputs and the workspace are allocated when
     not given."""
-    B, S, Hq, Hkv, D = _pair_shapes(q, k)
-    dev = q.device
-    if (k is None) != (dk_out is None):
-        raise ValueError("k and dk_out go together")
-    if dq_out is None:
-        raise ValueError("dq_out is required")
-    dq = torch.empty(q.shape, dtype=q.dtype, device=dev) if dq is None else dq
-    if k is not None and dk is None:
-        dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
-    _like(dq, q, "dq")
-    _like(dk, k, "dk")
-    _like(dq_out, q, "dq_out")
-    _like(dk_out, k, "dk_out")
+    dev, B, S, Hq, Hkv, D, lq, lk = _pair_shapes(q, k)
+    if dq_out is None or (k is None) != (dk_out is None):
+        raise ValueError("dq_out is required; k and dk_out go together")
+    if k is None and (dk is not None or dk_weight is not None):
+        raise ValueError("dk and dk_weight without k")
+    lgq = _like(dq_out, q, dev, "dq_out")
+    ldq = ldk = lgk = kp = gkp = dkp = dwq = dwk = ws = None
+    ws_bytes = 0
+    if dq is None:
+        dq = q.new_empty((B, S, Hq, D))
+    else:
+        ldq = _like(dq, q, dev, "dq")
+    if k is not None:
+        lgk = _like(dk_out, k, dev, "dk_out")
+        if dk is None:
+            dk = k.new_empty((B, S, Hkv, D))
+        else:
+            ldk = _like(dk, k, dev, "dk")
+        kp, gkp, dkp = k.data_ptr(), dk_out.data_ptr(), dk.data_ptr()
     if norm:
         if dq_weight is None:
-            dq_weight = torch.empty(D, dtype=torch.float32, device=dev)
-        if dk_weight is None and k is not None:
-            dk_weight = torch.empty(D, dtype=torch.float32, device=dev)
+            dq_weight = q.new_empty((D,), dtype=torch.float32)
+        dwq = _weight_grad(dq_weight, D, dev)
+        if k is not None:
+            if dk_weight is None:
+                dk_weight = q.new_empty((D,), dtype=torch.float32)
+            dwk = _weight_grad(dk_weight, D, dev)
         if workspace is None:
-            workspace = torch.empty(qk_norm_rope_bwd_workspace_bytes(B, S, Hq, Hkv, D), dtype=torch.uint8, device=dev)
+            workspace = q.new_empty((qk_norm_rope_bwd_workspace_bytes(B, S, Hq, Hkv, D),), dtype=torch.uint8)
+        ws, ws_bytes = _workspace(workspace, dev)
     else:
         dq_weight = dk_weight = None
-    if k is None and dk_weight is not None:
-        raise ValueError("dk_weight without k")
-    for t in (dq_weight, dk_weight):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (D,) or not t.is_contiguous()):
-            raise ValueError("weight gradients must be contiguous float32 [D] tensors")
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _on(dev, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace)
-    _run(dev.index, lib().sdpa_qk_norm_rope_bwd, q.data_ptr(), _ptr(k), dq_out.data_ptr(), _ptr(dk_out), dq.data_ptr(),
-         _ptr(dk), _ptr(dq_weight), _ptr(dk_weight), B, S, Hq, Hkv, D, _strides(q), _strides(k), _strides(dq_out),
-         _strides(dk_out), _strides(dq), _strides(dk), int(bool(norm)), _ptr(q_weight), _ptr(k_weight),
-         _weights(q_weight, k_weight, D, dev), float(eps), _rope_arg(rope, interleaved, dev),
-         _int32(positions, (B, S), dev, "positions"), _DTYPE.get(q.dtype, 99), _ptr(workspace),
-         0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_ptr(stream, dev.index))
+    qw, kw, wdt = _weights(q_weight, k_weight, D, dev)
+    _call(dev, (_lib or _bound()).sdpa_qk_norm_rope_bwd, q.data_ptr(), kp, dq_out.data_ptr(), gkp, dq.data_ptr(), dkp, dwq,
+          dwk, B, S, Hq, Hkv, D, lq, lk, lgq, lgk, ldq, ldk, 1 if norm else 0, qw, kw, wdt, eps,
+          _rope_arg(rope, interleaved, dev), _int32(positions, (B, S), dev, "positions"), _DTYPE.get(q.dtype, 99), ws,
+          ws_bytes, _stream_ptr(stream, dev))
     return dq, dk, dq_weight, dk_weight
 
 
@@ -189,6 +243,7 @@ class PagedCache:
         self._c = _abi.Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), self.n_pages,
                              self.page_size, ctypes.pointer(self._layouts[0]), ctypes.pointer(self._layouts[1]))
         self._ref = ctypes.byref(self._c)
+        self._device = k.get_device()
 
     @classmethod
     def empty(cls, n_pages: int, page_size: int, n_heads: int, head_dim: int, device="cuda") -> "PagedCache":
@@ -204,12 +259,12 @@ class PagedCache:
 
 
 def _cache_args(cache, block_table, start, count, B):
-    dev = cache.k.device
-    if block_table.dim() != 2:
+    dev = cache._device
+    shape = block_table.shape
+    if len(shape) != 2:
         raise ValueError("block_table must be [B, max_pages]")
-    width = block_table.shape[1]
-    return (_int32(block_table, (B, width), dev, "block_table"), _int32(start, (B,), dev, "start"),
-            _int32(count, (B,), dev, "count"), width)
+    return (_int32(block_table, (B, shape[1]), dev, "block_table"), _int32(start, (B,), dev, "start"),
+            _int32(count, (B,), dev, "count"), shape[1])
 
 
 def sdpa_cache_append(k, v, cache: PagedCache, block_table, start, count=None, *, rope=None, interleaved: bool = False,
@@ -219,17 +274,19 @@ def sdpa_cache_append(k, v, cache: PagedCache, block_table, start, count=None, *
     goes to position start[b] + i: page block_table[b, position / page_size].
     block_table (int32 [B, max_pages]), start and count (int32 [B]; None: S
     tokens each) are CUDA tensors; nothing is read back to the host."""
-    dev = cache.k.device
-    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+    dev = cache._device
+    shape = k.shape
+    if len(shape) != 4 or v.shape != shape or k.dtype != v.dtype:
         raise ValueError("k and v must be [B, S, Hkv, D] tensors of one shape and dtype")
-    B, S, Hkv, D = k.shape
+    B, S, Hkv, D = shape
     if Hkv != cache.n_heads or D != cache.head_dim:
         raise ValueError("k and v must have the cache's heads and head dimension")
-    _on(dev, k, v)
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("k and v must be on the cache's device")
     table_p, start_p, count_p, width = _cache_args(cache, block_table, start, count, B)
-    _run(dev.index, lib().sdpa_cache_append, k.data_ptr(), v.data_ptr(), cache._ref, table_p, start_p, count_p, B, S, Hkv,
-         D, width, _strides(k), _strides(v), _rope_arg(rope, interleaved, dev), _DTYPE.get(k.dtype, 99),
-         _stream_ptr(stream, dev.index))
+    _call(dev, (_lib or _bound()).sdpa_cache_append, k.data_ptr(), v.data_ptr(), cache._ref, table_p, start_p, count_p, B, S,
+          Hkv, D, width, _strides(k), _strides(v), _rope_arg(rope, interleaved, dev), _DTYPE.get(k.dtype, 99),
+          _stream_ptr(stream, dev))
 
 
 def paged_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, D: int) -> int:
@@ -245,24 +302,28 @@ def sdpa_fwd_paged(q, cache: PagedCache, block_table, start, count=None, o=None,
     all 0 .. start[b] + count[b] - 1.  Rows behind count[b] of ``o`` and
     ``lse`` ([B, Hq, Sq] float32) are left as they are.  ``o`` (like q) and
     the workspace are allocated when not given.  Returns ``o``."""
-    dev = cache.k.device
-    if q.dim() != 4 or q.shape[3] != cache.head_dim:
+    dev = cache._device
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != cache.head_dim:
         raise ValueError("q must be [B, Sq, Hq, D] with the cache's head dimension")
-    B, Sq, Hq, D = q.shape
+    if q.get_device() != dev:
+        raise ValueError("q must be on the cache's device")
+    B, Sq, Hq, D = shape
     Hkv = cache.n_heads
+    lo = None
     if o is None:
-        o = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    _like(o, q, "o")
+        o = q.new_empty((B, Sq, Hq, D))
+    else:
+        lo = _like(o, q, dev, "o")
+    if lse is not None and lse.get_device() != dev:
+        raise ValueError("lse must be on the cache's device")
     if workspace is None:
-        workspace = torch.empty(paged_workspace_bytes(B, Hq, Hkv, Sq, D), dtype=torch.uint8, device=dev)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _on(dev, q, o, lse, workspace)
+        workspace = q.new_empty((paged_workspace_bytes(B, Hq, Hkv, Sq, D),), dtype=torch.uint8)
+    ws, ws_bytes = _workspace(workspace, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     table_p, start_p, count_p, width = _cache_args(cache, block_table, start, count, B)
-    _run(dev.index, lib().sdpa_fwd_paged, q.data_ptr(), cache._ref, table_p, start_p, count_p, o.data_ptr(),
-         _lse_ptr(lse, B, Hq, Sq), B, Hq, Hkv, Sq, D, width, _strides(q), _strides(o), float(scale), int(bool(causal)),
-         _DTYPE.get(q.dtype, 99), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-         _stream_ptr(stream, dev.index))
+    _call(dev, (_lib or _bound()).sdpa_fwd_paged, q.data_ptr(), cache._ref, table_p, start_p, count_p, o.data_ptr(),
+          _lse_ptr(lse, B, Hq, Sq), B, Hq, Hkv, Sq, D, width, _strides(q), lo, scale, 1 if causal else 0,
+          _DTYPE.get(q.dtype, 99), ws, ws_bytes, _stream_ptr(stream, dev))
     return o
