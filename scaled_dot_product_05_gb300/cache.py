@@ -13,6 +13,7 @@ import torch
 from . import _DTYPE, _layout, _lse_ptr, _run, _stream_ptr, _abi
 from ._abi import check, lib
 
+_DENSE = torch.contiguous_format
 _lib = None
 
 
@@ -137,12 +138,12 @@ def sdpa_qk_norm_rope(q, k=None, q_out=None, k_out=None, *, norm: bool = True, q
     dev, B, S, Hq, Hkv, D, lq, lk = _pair_shapes(q, k)
     lqo = lko = kp = kop = None
     if q_out is None:
-        q_out = q.new_empty((B, S, Hq, D))
+        q_out = torch.empty_like(q, memory_format=_DENSE)
     else:
         lqo = _like(q_out, q, dev, "q_out")
     if k is not None:
         if k_out is None:
-            k_out = k.new_empty((B, S, Hkv, D))
+            k_out = torch.empty_like(k, memory_format=_DENSE)
         else:
             lko = _like(k_out, k, dev, "k_out")
         kp, kop = k.data_ptr(), k_out.data_ptr()
@@ -189,23 +190,23 @@ def sdpa_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq=None, dk=None, *, norm: bool 
     ldq = ldk = lgk = kp = gkp = dkp = dwq = dwk = ws = None
     ws_bytes = 0
     if dq is None:
-        dq = q.new_empty((B, S, Hq, D))
+        dq = torch.empty_like(q, memory_format=_DENSE)
     else:
         ldq = _like(dq, q, dev, "dq")
     if k is not None:
         lgk = _like(dk_out, k, dev, "dk_out")
         if dk is None:
-            dk = k.new_empty((B, S, Hkv, D))
+            dk = torch.empty_like(k, memory_format=_DENSE)
         else:
             ldk = _like(dk, k, dev, "dk")
         kp, gkp, dkp = k.data_ptr(), dk_out.data_ptr(), dk.data_ptr()
     if norm:
         if dq_weight is None:
-            dq_weight = q.new_empty((D,), dtype=torch.float32)
+            dq_weight = torch.empty(D, dtype=torch.float32, device=dev)
         dwq = _weight_grad(dq_weight, D, dev)
         if k is not None:
             if dk_weight is None:
-                dk_weight = q.new_empty((D,), dtype=torch.float32)
+                dk_weight = torch.empty(D, dtype=torch.float32, device=dev)
             dwk = _weight_grad(dk_weight, D, dev)
         if workspace is None:
             workspace = q.new_empty((qk_norm_rope_bwd_workspace_bytes(B, S, Hq, Hkv, D),), dtype=torch.uint8)
@@ -312,7 +313,7 @@ def sdpa_fwd_paged(q, cache: PagedCache, block_table, start, count=None, o=None,
     Hkv = cache.n_heads
     lo = None
     if o is None:
-        o = q.new_empty((B, Sq, Hq, D))
+        o = torch.empty_like(q, memory_format=_DENSE)
     else:
         lo = _like(o, q, dev, "o")
     if lse is not None and lse.get_device() != dev:

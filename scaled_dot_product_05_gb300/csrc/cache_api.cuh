@@ -3,8 +3,11 @@
 // after its helpers.
 #pragma once
 
+#include <type_traits>
+
 #include "cache_append.cuh"
 #include "paged_attn.cuh"
+#include "paged_wide.cuh"
 #include "qk_norm_rope.cuh"
 
 namespace {
@@ -333,22 +336,27 @@ cudaError_t launch_append_d(const sdpa::cache::AppendParams& p, bool bf16, bool 
     return inter ? launch_append<D, false, true>(p, s) : launch_append<D, false, false>(p, s);
 }
 
-// Attention over a paged cache: rows of a tile (16 for up to 16 rows of a KV
-// head; else 32, or 64 for bf16 and more than 32 rows), and the CTAs that
-// share the key tiles: two on each of 152 SMs.
+// Attention over a paged cache: rows of a tile (8, 16, or 128 with the wide
+// kernel), and the CTAs that share the key tiles (two on each of 152 SMs, one
+// of the wide kernel).
 constexpr int kPagedCtas = 304;
 
-int paged_tile_rows(int Sq, int group, bool bf16)
+int paged_tile_rows(int Sq, int group)
 {
     const long long rows = static_cast<long long>(Sq) * group;
-    (void)bf16;
-    return rows <= 8 ? 8 : 16;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : sdpa::paged::kWideRows;
+}
+
+int paged_ctas(int tile_rows)
+{
+    return tile_rows == sdpa::paged::kWideRows ? kPagedCtas / 2 : kPagedCtas;
 }
 
 // The pieces' results, their LSE, and what is to join.
 size_t paged_workspace(int Hq, int Hkv, int Sq, int D)
 {
-    return static_cast<size_t>(kPagedCtas) * (2 * paged_tile_rows(Sq, Hq / Hkv, true) * (D + 1) * sizeof(float) + sizeof(int4));
+    const int nr = paged_tile_rows(Sq, Hq / Hkv);
+    return static_cast<size_t>(paged_ctas(nr)) * (2 * nr * (D + 1) * sizeof(float) + sizeof(int4));
 }
 
 template <int D, bool kBF16, int NR>
@@ -356,19 +364,24 @@ cudaError_t launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const sdp
                          cudaStream_t stream)
 {
     using namespace sdpa::paged;
-    using L = PagedLayout<D, kBF16, NR>;
     static std::once_flag once[kMaxDevices];
     static cudaError_t attr[kMaxDevices];
+    constexpr bool kWide = NR == kWideRows;
+    auto* kernel = [] {
+        if constexpr (kWide)
+            return paged_wide_kernel<D, kBF16>;
+        else
+            return paged_attn_kernel<D, kBF16, NR>;
+    }();
+    using L = std::conditional_t<kWide, WideLayout<D, kBF16>, PagedLayout<D, kBF16, kWide ? 16 : NR>>;
     std::call_once(once[dev], [&] {
-        attr[dev] = cudaFuncSetAttribute(paged_attn_kernel<D, kBF16, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         L::kSmemBytes);
+        attr[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
     });
     if (attr[dev] != cudaSuccess)
         return attr[dev];
-    cudaError_t e = launch_pdl(true, paged_attn_kernel<D, kBF16, NR>, dim3(p.ctas), dim3(L::kThreads), L::kSmemBytes,
-                               stream, tk, tv, p);
+    cudaError_t e = launch_pdl(true, kernel, dim3(p.ctas), dim3(L::kThreads), L::kSmemBytes, stream, tk, tv, p);
     const long long rows = static_cast<long long>(p.Sq) * p.group;
-    const unsigned blocks = static_cast<unsigned>(NR <= 16 ? (rows < NR ? rows : NR) : (rows < NR ? rows + 7 : NR) / 8);
+    const unsigned blocks = static_cast<unsigned>(kWide ? (rows < NR ? rows + 7 : NR) / 8 : rows < NR ? rows : NR);
     if (e == cudaSuccess && p.ctas > 1)
         e = launch_pdl(true, paged_join_kernel<D, kBF16, NR>, dim3(p.ctas - 1, blocks), dim3(kJoinThreads), 0, stream, p);
     return e;
@@ -378,7 +391,9 @@ template <int D, bool kBF16>
 cudaError_t launch_paged_rows(int nr, const CUtensorMap& tk, const CUtensorMap& tv, const sdpa::paged::Params& p, int dev,
                               cudaStream_t s)
 {
-    return nr == 8 ? launch_paged<D, kBF16, 8>(tk, tv, p, dev, s) : launch_paged<D, kBF16, 16>(tk, tv, p, dev, s);
+    return nr == 8    ? launch_paged<D, kBF16, 8>(tk, tv, p, dev, s)
+           : nr == 16 ? launch_paged<D, kBF16, 16>(tk, tv, p, dev, s)
+                      : launch_paged<D, kBF16, sdpa::paged::kWideRows>(tk, tv, p, dev, s);
 }
 
 }  // namespace
@@ -564,12 +579,13 @@ sdpa_status_t sdpa_fwd_paged(const void* Q, const sdpa_cache_t* cache, const int
     p.causal = causal ? 1 : 0;
     p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
     p.page_shift = p.page == 16 ? 4 : p.page == 32 ? 5 : p.page == 64 ? 6 : 7;
-    const int nr = paged_tile_rows(Sq, p.group, dtype == SDPA_DTYPE_BF16);
+    const int nr = paged_tile_rows(Sq, p.group);
     p.row_tiles = static_cast<int>((static_cast<long long>(Sq) * p.group + nr - 1) / nr);
     // no more CTAs than there can be tiles
     const __int128 most = static_cast<__int128>(B) * Hkv * p.row_tiles *
                           ((static_cast<long long>(max_pages) * p.page + sdpa::paged::kTileKeys - 1) / sdpa::paged::kTileKeys);
-    p.ctas = 2 * sm_count < kPagedCtas ? 2 * sm_count : kPagedCtas;
+    const int per_sm = nr == sdpa::paged::kWideRows ? 1 : 2;
+    p.ctas = per_sm * sm_count < paged_ctas(nr) ? per_sm * sm_count : paged_ctas(nr);
     p.ctas = most < p.ctas ? static_cast<int>(most) : p.ctas;
     p.part_o = static_cast<float*>(workspace);
     p.part_lse = p.part_o + static_cast<long long>(p.ctas) * 2 * nr * D;
