@@ -7,13 +7,14 @@
 //     S[128 rows][128 keys] = Q K8^T          FP8, q in two or three E4M3 parts
 //     O[128 rows][D] += W V                   f16, W = exp(s - m) v_scale
 // The weights keep 11 bits: they are rounded to f16 (weight 1 as 2^7, the
-// smallest step 2^-31 of that), stay in tensor memory over the scores they
-// come from, and V's codes are turned into f16, which holds them exactly, by
-// two warps of their own.  The two softmax warpgroups take alternate key
-// tiles of the same rows, each with its own maxima, sums and accumulator,
-// joined when the item is done, so one's scores are computed while the other
-// works on its own.  Bound by the tensor cores: 128 x 128 x D FP8 products for each part
-// of q and the f16 product, 1056 cycles a tile at D = 128 and bf16.
+// smallest step 2^-31 of that) and stay in tensor memory, and V's codes are
+// turned into f16, which holds them exactly, by two warps of their own.  The
+// two softmax warpgroups take alternate key tiles of the same rows, each with
+// its own maxima, sums and accumulator, joined when the item is done; the
+// scores of both go through one region of tensor memory, which is free for
+// the next tile's as soon as they are read.  Bound by the tensor cores (128 x
+// 128 x D FP8 products for each part of q and the f16 product: 1056 cycles a
+// tile at D = 128 and bf16) and the exponentials (1024 cycles).
 #pragma once
 
 #include "paged_attn.cuh"
@@ -33,30 +34,35 @@ struct WideLayout {
     static constexpr int kV16Bytes = kTileKeys * D * 2;
     static constexpr int kStagesK = D == 64 ? 4 : 3;
     static constexpr int kStagesV = D == 64 ? 4 : 2;
+    static constexpr int kPageBufs = 4;
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kOffQ + kParts * kTileBytes;
     static constexpr int kOffV8 = kOffK + kStagesK * kTileBytes;
     static constexpr int kOffV16 = kOffV8 + kStagesV * kTileBytes;
-    static constexpr int kOffPages = kOffV16 + 2 * kV16Bytes;   // [2][8] float4: scales of 16 keys each
-    static constexpr int kOffRows = kOffPages + 2 * 8 * 16;     // [2][128] maxima and [2][128] sums; [D] NaN; any NaN
+    static constexpr int kOffPages = kOffV16 + 2 * kV16Bytes;   // [kPageBufs][8] float4: scales of 16 keys each
+    static constexpr int kOffRows = kOffPages + kPageBufs * 8 * 16;     // [2][128] maxima and [2][128] sums; [D] NaN; any NaN
     static constexpr int kOffBar = kOffRows + 4 * (4 * kWideRows + D + 4);
-    static constexpr int kBarBytes = 512;
+    static constexpr int kBarBytes = 640;
     static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory budget");
-    static constexpr uint32_t kTmemCols = 512;                  // of warpgroup g: S, W at 256 g; O at 256 g + 128
+    static constexpr uint32_t kTmemCols = 512;                  // S at 0; of warpgroup g: W at 128 + 64 g, O at 256 + 128 g
 };
 
 template <int NK, int NV>
 struct WideBarriers {
     uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV];
-    uint64_t v16_full[2], v16_empty[2];    // converted V tile (and its pages' scales) written / multiplied
-    uint64_t pages_free[2];                // scales read
-    uint64_t s_full[2], w_full[2], pv_done[2];
+    uint64_t v16_full[2], v16_empty[2];    // converted V tile written / multiplied
+    uint64_t pages_full[4], pages_free[4]; // a tile's scales written / read
+    uint64_t s_full[2], s_free[2], w_full[2], pv_done[2];
     uint64_t q_full, o_free, drain;
     uint32_t tmem_base;
     int abort;
     long long total, x, x_first;
     long long warp_sums[12];
+    // the piece at hand, kept here while the softmax threads' registers hold
+    // their scores
+    Piece piece;
+    Item item;
 };
 
 template <int D, bool kBF16>
@@ -94,10 +100,14 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&bars->v16_full[i]), 64);
             mbar_init(smem_u32(&bars->v16_empty[i]), 1);
-            mbar_init(smem_u32(&bars->pages_free[i]), 128);
             mbar_init(smem_u32(&bars->s_full[i]), 1);
+            mbar_init(smem_u32(&bars->s_free[i]), 128);
             mbar_init(smem_u32(&bars->w_full[i]), 128);
             mbar_init(smem_u32(&bars->pv_done[i]), 1);
+        }
+        for (int i = 0; i < L::kPageBufs; ++i) {
+            mbar_init(smem_u32(&bars->pages_full[i]), 8);
+            mbar_init(smem_u32(&bars->pages_free[i]), 128);
         }
         mbar_init(smem_u32(&bars->q_full), 256);
         mbar_init(smem_u32(&bars->o_free), 256);
@@ -181,9 +191,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             __syncwarp();
         } else if (warp == 9) {
             // ========================== MMA issuer ==========================
-            // S(0), S(1), then for each tile W V and the next S of the same
-            // warpgroup: S goes over the W of two tiles before, which the product
-            // issued just ahead of it reads
+            // S(0), S(1), then for each tile j S(j + 2) and W V of tile j: a
+            // warpgroup finds its next scores when it has written its weights
             if (lane == 0) {
                 constexpr uint32_t kSwzCode = D == 128 ? 2u : 4u;
                 constexpr uint32_t idesc_s = idesc_make(0u, NR, kTileKeys, false);
@@ -192,12 +201,18 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 const uint32_t hi_v = (uint32_t)(smem_desc(0, 16, 1024, 2u) >> 32);
                 constexpr uint32_t kLboV = (uint32_t)((kTileKeys * 128) >> 4) << 16;    // next 64 channels
                 uint32_t ns = 0, nv = 0, pieces = 0, w0 = 0, w1 = 0;
+                uint32_t f0 = 0, f1 = 0;                   // S issued for each warpgroup
+                int prev = -1;                             // warpgroup of the last S
                 bool ok = true;
                 for (; ok && more; more = next_piece<NR>(p, w), ++pieces) {
                     const int n = w.end - w.begin;
                     auto issue_s = [&](int g) -> bool {
                         const uint32_t ks = ns % NK;
                         if (!wait_bar(smem_u32(&bars->k_full[ks]), (ns / NK) & 1, abort, kErrPagedMma))
+                            return false;
+                        // the S before has been read out of the region
+                        if (prev >= 0 &&
+                            !wait_bar(smem_u32(&bars->s_free[prev]), ((prev ? f1 : f0) - 1) & 1, abort, kErrPagedMma + 1))
                             return false;
                         tc_fence_after_sync();
                         const uint32_t k_lo = ((sK + ks * L::kTileBytes) >> 4) | (1u << 16);
@@ -206,20 +221,26 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                             const uint32_t q_lo = ((sQ + q * L::kTileBytes) >> 4) | (1u << 16);
 #pragma unroll
                             for (int kk = 0; kk < D / 32; ++kk)
-                                mma_f8_ss(tmem + 256 * g, desc_join(hi, q_lo + 2 * kk), desc_join(hi, k_lo + 2 * kk), idesc_s,
+                                mma_f8_ss(tmem, desc_join(hi, q_lo + 2 * kk), desc_join(hi, k_lo + 2 * kk), idesc_s,
                                           q > 0 || kk > 0);
                         }
                         mma_commit(smem_u32(&bars->s_full[g]));
                         mma_commit(smem_u32(&bars->k_empty[ks]));
                         ++ns;
+                        f0 += g ? 0 : 1;
+                        f1 += g ? 1 : 0;
+                        prev = g;
                         return true;
                     };
-                    // the pieces before have been read out: o_free also covers their W
-                    ok = wait_bar(smem_u32(&bars->q_full), pieces & 1, abort, kErrPagedMma + 2) &&
-                         (pieces == 0 || wait_bar(smem_u32(&bars->o_free), (pieces - 1) & 1, abort, kErrPagedMma + 5)) &&
-                         issue_s(0) && (n == 1 || issue_s(1));
+                    ok = wait_bar(smem_u32(&bars->q_full), pieces & 1, abort, kErrPagedMma + 2) && issue_s(0) &&
+                         (n == 1 || issue_s(1));
                     for (int j = 0; ok && j < n; ++j, ++nv) {
                         const int g = j & 1;
+                        if (j + 2 < n && !(ok = issue_s(g)))
+                            break;
+                        if (j == 0 && pieces > 0 &&
+                            !(ok = wait_bar(smem_u32(&bars->o_free), (pieces - 1) & 1, abort, kErrPagedMma + 5)))
+                            break;
                         ok = wait_bar(smem_u32(&bars->v16_full[nv & 1]), (nv / 2) & 1, abort, kErrPagedMma + 3) &&
                              wait_bar(smem_u32(&bars->w_full[g]), (g ? w1 : w0) & 1, abort, kErrPagedMma + 4);
                         if (!ok)
@@ -228,14 +249,12 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         const uint32_t v_lo = ((sV16 + (nv & 1) * L::kV16Bytes) >> 4) | kLboV;
 #pragma unroll
                         for (int kk = 0; kk < kTileKeys / 16; ++kk)
-                            mma_f16_ts(tmem + 256 * g + 128, tmem + 256 * g + kk * 8,
+                            mma_f16_ts(tmem + 256 + 128 * g, tmem + 128 + 64 * g + kk * 8,
                                        desc_join(hi_v, v_lo + (uint32_t)((kk * 16 * 128) >> 4)), idesc_o, j >= 2 || kk > 0);
                         mma_commit(smem_u32(&bars->pv_done[g]));
                         mma_commit(smem_u32(&bars->v16_empty[nv & 1]));
                         w0 += g ? 0 : 1;
                         w1 += g ? 1 : 0;
-                        if (j + 2 < n)
-                            ok = issue_s(g);
                     }
                 }
                 mma_commit(smem_u32(&bars->drain));
@@ -284,52 +303,66 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     entry = entry_next;
                     entry_next = entry_of(j + 2);
                     valid_next = scales_of(entry, k_scale, v_scale);
-                    const uint32_t b = n & 1, ring = n % NV;
-                    // one warp writes the scales: buffer j & 1 of the piece, as the warpgroups go
+                    const uint32_t b = n & 1, ring = n % NV, pb = n % L::kPageBufs;
                     const uint32_t valid_parts = __ballot_sync(0xffffffffu, valid) & 0xffu;
+                    // the scales go ahead of the tile
+                    if (n >= L::kPageBufs)
+                        ok = wait_bar(smem_u32(&bars->pages_free[pb]), (n / L::kPageBufs - 1) & 1, abort, kErrPagedSoftmax + 6);
+                    if (ok && tid < 8) {
+                        pages[pb * 8 + tid] = make_float4(ks * p.scale_log2, valid ? __log2f(vs) : -INFINITY, __fdividef(1.f, vs), 0.f);
+                        mbar_arrive(smem_u32(&bars->pages_full[pb]));
+                    }
                     if (n >= 2)
-                        ok = wait_bar(smem_u32(&bars->v16_empty[b]), (n / 2 - 1) & 1, abort, kErrPagedSoftmax + 5) &&
-                             wait_bar(smem_u32(&bars->pages_free[b]), (n / 2 - 1) & 1, abort, kErrPagedSoftmax + 6);
+                        ok = ok && wait_bar(smem_u32(&bars->v16_empty[b]), (n / 2 - 1) & 1, abort, kErrPagedSoftmax + 5);
                     ok = ok && wait_bar(smem_u32(&bars->v_full[ring]), (n / NV) & 1, abort, kErrPagedSoftmax + 7);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok)
                         break;
-                    if (tid < 8)
-                        pages[b * 8 + tid] = make_float4(ks * p.scale_log2, valid ? __log2f(vs) : -INFINITY, __fdividef(1.f, vs), 0.f);
-                    const bool edge = (j + 1) * kTileKeys > full;
-                    const uint8_t* src = smem + L::kOffV8 + ring * L::kTileBytes;
-                    const uint32_t dst = sV16 + b * L::kV16Bytes;
-#pragma unroll 4
-                    for (int i = tid; i < kTileKeys * (D / 16); i += 64) {
-                        const int key = i / (D / 16), c = i % (D / 16);
-                        const int at = D == 128 ? c ^ (key & 7) : c ^ ((key >> 1) & 3);
-                        uint4 u = *reinterpret_cast<const uint4*>(src + key * D + at * 16);
-                        const int pos = j * kTileKeys + key;
-                        if (pos >= it.keys || !(valid_parts >> (key / 16) & 1)) {
-                            u = make_uint4(0, 0, 0, 0);
-                        } else if (edge && pos >= full) {
-                            uint32_t q[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t hit = ((q[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;    // 0x7F, 0xFF
-                                if (hit) {
+                    // this thread's 16 channels c of keys key0, key0 + kStep, ..:
+                    // a multiple of 8 apart, so all at one swizzled place
+                    constexpr int kPer = D / 16, kStep = 64 / kPer, kTurns = kTileKeys / kStep;
+                    const int key0 = tid / kPer, c = tid % kPer;
+                    const int at = D == 128 ? c ^ (key0 & 7) : c ^ ((key0 >> 1) & 3);
+                    uint8_t* src = smem + L::kOffV8 + ring * L::kTileBytes + key0 * D + at * 16;
+                    const uint32_t row = sV16 + b * L::kV16Bytes + (c / 4) * (kTileKeys * 128) + key0 * 128;
+                    const uint32_t dst0 = row + (((c % 4) * 2) ^ (key0 & 7)) * 16, dst1 = row + (((c % 4) * 2 + 1) ^ (key0 & 7)) * 16;
+                    if ((j + 1) * kTileKeys > full || valid_parts != 0xffu) {
+#pragma unroll 1
+                        for (int i = 0; i < kTurns; ++i) {
+                            const int key = key0 + i * kStep, pos = j * kTileKeys + key;
+                            uint32_t* u = reinterpret_cast<uint32_t*>(src + i * kStep * D);
+                            if (pos >= it.keys || !(valid_parts >> (key / 16) & 1)) {
+                                for (int e = 0; e < 4; ++e)
+                                    u[e] = 0;
+                            } else if (pos >= full) {
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t hit = ((u[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;    // 0x7F, 0xFF
+                                    if (!hit)
+                                        continue;
                                     *any_nan = 1;
                                     for (int f = 0; f < 4; ++f)
                                         if (hit >> (8 * f + 7) & 1) {
                                             atomicMin(&nan_at[16 * c + 4 * e + f], pos);
-                                            q[e] &= ~(0xffu << (8 * f));
+                                            u[e] &= ~(0xffu << (8 * f));
                                         }
                                 }
                             }
-                            u = make_uint4(q[0], q[1], q[2], q[3]);
                         }
-                        const uint32_t row = dst + (c / 4) * (kTileKeys * 128) + key * 128;
-                        const int c0 = (c % 4) * 2;
-                        st_shared_v4(row + ((c0 ^ (key & 7)) << 4), e4m3x2_to_f16x2((uint16_t)u.x), e4m3x2_to_f16x2((uint16_t)(u.x >> 16)),
-                                     e4m3x2_to_f16x2((uint16_t)u.y), e4m3x2_to_f16x2((uint16_t)(u.y >> 16)));
-                        st_shared_v4(row + (((c0 + 1) ^ (key & 7)) << 4), e4m3x2_to_f16x2((uint16_t)u.z),
-                                     e4m3x2_to_f16x2((uint16_t)(u.z >> 16)), e4m3x2_to_f16x2((uint16_t)u.w),
-                                     e4m3x2_to_f16x2((uint16_t)(u.w >> 16)));
+                    }
+#pragma unroll
+                    for (int i0 = 0; i0 < kTurns; i0 += 8) {
+                        uint4 u[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            u[i] = *reinterpret_cast<const uint4*>(src + (i0 + i) * kStep * D);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t off = (uint32_t)((i0 + i) * kStep * 128);
+                            st_shared_v4(dst0 + off, e4m3x2_to_f16x2((uint16_t)u[i].x), e4m3x2_to_f16x2((uint16_t)(u[i].x >> 16)),
+                                         e4m3x2_to_f16x2((uint16_t)u[i].y), e4m3x2_to_f16x2((uint16_t)(u[i].y >> 16)));
+                            st_shared_v4(dst1 + off, e4m3x2_to_f16x2((uint16_t)u[i].z), e4m3x2_to_f16x2((uint16_t)(u[i].z >> 16)),
+                                         e4m3x2_to_f16x2((uint16_t)u[i].w), e4m3x2_to_f16x2((uint16_t)(u[i].w >> 16)));
+                        }
                     }
                     fence_proxy_async_smem();
                     mbar_arrive(smem_u32(&bars->v_empty[ring]));
@@ -343,12 +376,12 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const int g = warp >> 2;
         const int row = threadIdx.x & 127;                                  // of the tile; TMEM lane
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t t_s = tmem + lanes + 256 * g, t_o = t_s + 128;
+        const uint32_t t_s = tmem + lanes, t_w = t_s + 128 + 64 * g, t_o = t_s + 256 + 128 * g;
         uint32_t ns = 0;                                                    // tiles of this warpgroup so far
         uint32_t nv = 0;                                                    // tiles of the CTA before this piece
         bool ok = true;
         for (; more; nv += w.end - w.begin, more = next_piece<NR>(p, w)) {
-            const Item it = item_of<NR>(p, w);
+            Item it = item_of<NR>(p, w);
             // ---- q into E4M3 parts: two threads a row, half of its channels each
             float scale;                                                    // of this thread's row in the loop below
             {
@@ -407,6 +440,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (threadIdx.x < D)
                     nan_at[threadIdx.x] = INT_MAX;
                 if (threadIdx.x == 0) {
+                    bars->piece = w;
+                    bars->item = it;
                     *any_nan = 0;
                     if (it.start + it.count > (long long)p.max_pages * p.page)
                         atomicCAS(&g_sdpa_error, 0u, (unsigned)cache::kErrTable);
@@ -424,19 +459,21 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             float nmax = kWideLog2W;                                        // 7 - maximum
             float l = 0.f;                                                  // sum of exp2(s - maximum + 7)
             bool seen = false;
-            const int first = w.begin + g;
-            for (int j = first; j < w.end; j += 2, ++ns) {
-                const uint32_t vn = nv + (uint32_t)(j - w.begin), buf = vn & 1;
+            // j counts the piece's tiles
+            const int tiles = w.end - w.begin, ahead = full - w.begin * kTileKeys, seen_end = last - w.begin * kTileKeys;
+            for (int j = g; j < tiles; j += 2, ++ns) {
+                const uint32_t vn = nv + (uint32_t)j, buf = vn % L::kPageBufs;
                 ok = ok && wait_bar(smem_u32(&bars->s_full[g]), ns & 1, abort, kErrPagedSoftmax);
-                // the tile's scales come with its V
-                ok = ok && wait_bar(smem_u32(&bars->v16_full[buf]), (vn / 2) & 1, abort, kErrPagedSoftmax + 1);
+                ok = ok && wait_bar(smem_u32(&bars->pages_full[buf]), (vn / L::kPageBufs) & 1, abort, kErrPagedSoftmax + 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok)
                     break;
                 tc_fence_after_sync();
                 uint32_t r[128];
                 tmem_ld128_wait(t_s, t_s + 32, t_s + 64, t_s + 96, r);
-                const bool edge = (j + 1) * kTileKeys > full;
+                tc_fence_before_sync();
+                mbar_arrive(smem_u32(&bars->s_free[g]));
+                const bool edge = (j + 1) * kTileKeys > ahead;
                 float mx = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
@@ -457,7 +494,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     }
                 }
                 if (edge) {
-                    const int seen_keys = last - j * kTileKeys;             // of the tile, less one
+                    const int seen_keys = seen_end - j * kTileKeys;             // of the tile, less one
 #pragma unroll
                     for (int e = 0; e < 128; ++e)
                         if (e > seen_keys)
@@ -516,7 +553,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (!ok)
                     break;
                 tc_fence_after_sync();
-                if (j > first && __any_sync(0xffffffffu, factor != 1.f)) {
+                if (j > g && __any_sync(0xffffffffu, factor != 1.f)) {
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         uint32_t o[32];
@@ -527,14 +564,16 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         tmem_st32(t_o + c, o);
                     }
                 }
-                tmem_st32(t_s, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
-                tmem_st32(t_s + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
+                tmem_st32(t_w, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
+                tmem_st32(t_w + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
                 tmem_st_wait();
                 tc_fence_before_sync();
                 mbar_arrive(smem_u32(&bars->w_full[g]));
             }
             // ---- the piece's result: both warpgroups' accumulators, a half of the channels each
-            if (ok && first < w.end)
+            w = bars->piece;
+            it = bars->item;
+            if (ok && g < w.end - w.begin)
                 ok = wait_bar(smem_u32(&bars->pv_done[g]), (ns - 1) & 1, abort, kErrPagedSoftmax + 3);
             row_max[g * NR + row] = kWideLog2W - nmax;
             row_sum[g * NR + row] = l;
@@ -552,22 +591,25 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             const bool both = w.end - w.begin > 1;                          // warpgroup 1 had a tile
             const long long slot = (long long)blockIdx.x * 2 + (w.begin > 0 ? 0 : 1);
             const long long head = (long long)w.h * p.group + (it.r0 + row) % p.group;
+            const int i = (it.r0 + row) / p.group;
             const bool live = row < it.rows;
             if (live && g == 0) {
                 const float lse2 = sum == 0.f ? -INFINITY : m + (log2f(sum) - kWideLog2W);
                 if (!whole)
                     p.part_lse[slot * NR + row] = lse2;
                 else if (p.lse)
-                    p.lse[((long long)it.b * p.Hq + head) * p.Sq + q_row] = lse2 * kLn2;
+                    p.lse[((long long)it.b * p.Hq + head) * p.Sq + i] = lse2 * kLn2;
             }
             const bool nans = *any_nan != 0;
-            uint16_t* out = reinterpret_cast<uint16_t*>(p.O) + (long long)it.b * p.o_sb + (long long)q_row * p.o_ss + head * p.o_sh;
+            const long long last_at = p.causal ? it.start + i : it.start + it.count - 1;
+            const int last_key = last_at < it.keys ? (int)last_at : it.keys - 1;    // (a negative one is below any)
+            uint16_t* out = reinterpret_cast<uint16_t*>(p.O) + (long long)it.b * p.o_sb + (long long)i * p.o_ss + head * p.o_sh;
 #pragma unroll 1
             for (int c = g * (D / 2); c < (g + 1) * (D / 2); c += 32) {
                 uint32_t a[32], b[32];
-                tmem_ld32_wait(tmem + lanes + 128 + c, a);
+                tmem_ld32_wait(t_s + 256 + c, a);
                 if (both)
-                    tmem_ld32_wait(tmem + lanes + 256 + 128 + c, b);
+                    tmem_ld32_wait(t_s + 384 + c, b);
                 float o[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
@@ -579,7 +621,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (nans) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        if (last >= nan_at[c + e])
+                        if (last_key >= nan_at[c + e])
                             o[e] = NAN;
                 }
                 if (live && !whole) {
