@@ -309,7 +309,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     if (n >= L::kPageBufs)
                         ok = wait_bar(smem_u32(&bars->pages_free[pb]), (n / L::kPageBufs - 1) & 1, abort, kErrPagedSoftmax + 6);
                     if (ok && tid < 8) {
-                        pages[pb * 8 + tid] = make_float4(ks * p.scale_log2, valid ? __log2f(vs) : -INFINITY, __fdividef(1.f, vs), 0.f);
+                        pages[pb * 8 + tid] = make_float4(ks * p.scale_log2, valid ? __log2f(vs) : -INFINITY, __fdividef(1.f, vs),
+                                                          valid_parts == 0xffu ? 0.f : 1.f);
                         mbar_arrive(smem_u32(&bars->pages_full[pb]));
                     }
                     if (n >= 2)
@@ -487,17 +488,14 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         r[e] = __float_as_uint(y0);
                         r[e + 1] = __float_as_uint(y1);
                     }
-                    if (pg.y == -INFINITY) {                                // a page that is none: whatever was there
-#pragma unroll
-                        for (int e = 16 * c; e < 16 * c + 16; ++e)
-                            r[e] = 0xff800000u;
-                    }
                 }
-                if (edge) {
+                // keys that the row does not see, or whose page is none (.w: the
+                // tile has such a page), whatever was there
+                if (__builtin_expect(edge || pages[buf * 8].w != 0.f, 0)) {
                     const int seen_keys = seen_end - j * kTileKeys;             // of the tile, less one
 #pragma unroll
                     for (int e = 0; e < 128; ++e)
-                        if (e > seen_keys)
+                        if (e > seen_keys || pages[buf * 8 + e / 16].y == -INFINITY)
                             r[e] = 0xff800000u;
                 }
                 float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
@@ -519,7 +517,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     shift = mx;
                     factor = ex2_approx(-shift);
                 }
-                if (__any_sync(0xffffffffu, shift != 0.f)) {
+                if (__builtin_expect(__any_sync(0xffffffffu, shift != 0.f), 0)) {
                     nmax -= shift;
                     l *= factor;
                     const uint64_t s2 = f32x2(-shift, -shift);
@@ -553,7 +551,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (!ok)
                     break;
                 tc_fence_after_sync();
-                if (j > g && __any_sync(0xffffffffu, factor != 1.f)) {
+                if (__builtin_expect(j > g && __any_sync(0xffffffffu, factor != 1.f), 0)) {
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         uint32_t o[32];
