@@ -107,7 +107,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         for (int i = 0; i < L::kPageBufs; ++i) {
             mbar_init(smem_u32(&bars->pages_full[i]), 8);
-            mbar_init(smem_u32(&bars->pages_free[i]), 128);
+            mbar_init(smem_u32(&bars->pages_free[i]), 128 + 64);
         }
         mbar_init(smem_u32(&bars->q_full), 256);
         mbar_init(smem_u32(&bars->o_free), 256);
@@ -137,7 +137,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         regs_release<104>();
         if (warp == 8) {
             // ========================= TMA producer =========================
-            // as in paged_attn_kernel: lane i brings page i of a tile
+            // as in paged_attn_kernel: lane i brings page i of a tile; and lane
+            // i < 8 lays out the scales of the tile's keys 16 i .. 16 i + 15
             if (lane == 0 && blockIdx.x > 0)
                 p.joins[blockIdx.x] = more ? join_of(p, bars->total, w) : make_int4(0, 0, 0, 0);
             const int ppt = kTileKeys >> p.page_shift;
@@ -152,7 +153,33 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                                : -1;
                 };
                 int ahead0 = entry_of(w.begin), ahead1 = entry_of(w.begin + 1);
+                // a part's table entry two tiles ahead, its scales one ahead
+                auto part_of = [&](int tile) -> int {
+                    const int pos = tile * kTileKeys + lane * 16;
+                    return lane < 8 && tile < w.end && pos < it.keys ? p.table[(long long)it.b * p.max_pages + (pos >> p.page_shift)]
+                                                                     : INT_MIN;
+                };
+                auto scales_of = [&](int entry, float& a, float& b) -> bool {
+                    a = b = 1.f;
+                    const bool in = (unsigned)entry < (unsigned)p.n_pages;
+                    if (in) {
+                        a = p.k.scale[(long long)entry * p.Hkv + w.h];
+                        b = p.v.scale[(long long)entry * p.Hkv + w.h];
+                    } else if (entry != INT_MIN) {
+                        atomicCAS(&g_sdpa_error, 0u, (unsigned)cache::kErrPage);
+                    }
+                    return in;
+                };
+                int entry = part_of(w.begin), entry_next = part_of(w.begin + 1);
+                float k_scale, v_scale;
+                bool valid_next = scales_of(entry, k_scale, v_scale);
                 for (int j = w.begin; ok && j < w.end; ++j, ++n) {
+                    const bool valid = valid_next;
+                    const float k_now = k_scale;
+                    const float v_now = fminf(fmaxf(v_scale, 8.673617379884035e-19f), 1.152921504606847e18f);   // 2^-60 .. 2^60
+                    entry = entry_next;
+                    entry_next = part_of(j + 2);
+                    valid_next = scales_of(entry, k_scale, v_scale);
                     const int id = (unsigned)ahead0 < (unsigned)p.n_pages ? ahead0 : -1;
                     ahead0 = ahead1;
                     ahead1 = entry_of(j + 2);
@@ -168,8 +195,17 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     __syncwarp();
                     if (id >= 0)
                         tma_load_4d(sK + ks * L::kTileBytes + lane * p.page * D, &tm_k, smem_u32(&bars->k_full[ks]), 0, w.h, 0, id);
+                    const uint32_t pb = n % L::kPageBufs;
+                    if (n >= L::kPageBufs)
+                        ok = wait_bar(smem_u32(&bars->pages_free[pb]), (n / L::kPageBufs - 1) & 1, abort, kErrPagedLoad + 2);
+                    const bool some = __any_sync(0xffffffffu, lane < 8 && !valid);
+                    if (ok && lane < 8) {
+                        pages[pb * 8 + lane] = make_float4(k_now * p.scale_log2, valid ? __log2f(v_now) : -INFINITY,
+                                                           __fdividef(1.f, v_now), some ? 1.f : 0.f);
+                        mbar_arrive(smem_u32(&bars->pages_full[pb]));
+                    }
                     if (n >= NV)
-                        ok = wait_bar(smem_u32(&bars->v_empty[vs]), (n / NV - 1) & 1, abort, kErrPagedLoad + 1);
+                        ok = ok && wait_bar(smem_u32(&bars->v_empty[vs]), (n / NV - 1) & 1, abort, kErrPagedLoad + 1);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok)
                         break;
@@ -266,7 +302,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             // V's codes to f16, 16 at a time, into the layout of a 16-bit tile
             // (64 channels a chunk, 128-byte rows); rows that no row of the item
             // sees are zero, a NaN that only some see is taken out and kept in
-            // mind.  Thread i < 8 also lays out the scales of keys 16 i .. 16 i + 15.
+            // mind
             const int tid = threadIdx.x - 320;                              // 0 .. 63
             uint32_t n = 0, pieces = 0;
             bool ok = true;
@@ -276,42 +312,14 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->q_full), pieces & 1, abort, kErrPagedSoftmax + 8));
                 const long long row0 = p.causal ? it.start + it.r0 / p.group : it.start + it.count - 1;
                 const int full = row0 < 0 ? 0 : (int)(row0 + 1 < it.keys ? row0 + 1 : it.keys);
-                const int* table = p.table + (long long)it.b * p.max_pages;
-                const int part = lane & 7;                                  // every 8 lanes look after the tile's 8 parts
-                auto entry_of = [&](int tile) -> int {
-                    const int pos = tile * kTileKeys + part * 16;
-                    return tile < w.end && pos < it.keys ? table[pos >> p.page_shift] : INT_MIN;
-                };
-                auto scales_of = [&](int entry, float& a, float& b) -> bool {
-                    a = b = 1.f;
-                    const bool in = (unsigned)entry < (unsigned)p.n_pages;
-                    if (in) {
-                        a = p.k.scale[(long long)entry * p.Hkv + w.h];
-                        b = p.v.scale[(long long)entry * p.Hkv + w.h];
-                    } else if (entry != INT_MIN) {
-                        atomicCAS(&g_sdpa_error, 0u, (unsigned)cache::kErrPage);
-                    }
-                    return in;
-                };
-                int entry = entry_of(w.begin), entry_next = entry_of(w.begin + 1);
-                float k_scale, v_scale;
-                bool valid_next = scales_of(entry, k_scale, v_scale);
                 for (int j = w.begin; ok && j < w.end; ++j, ++n) {
-                    const bool valid = valid_next;
-                    const float ks = k_scale;
-                    const float vs = fminf(fmaxf(v_scale, 8.673617379884035e-19f), 1.152921504606847e18f);   // 2^-60 .. 2^60
-                    entry = entry_next;
-                    entry_next = entry_of(j + 2);
-                    valid_next = scales_of(entry, k_scale, v_scale);
                     const uint32_t b = n & 1, ring = n % NV, pb = n % L::kPageBufs;
-                    const uint32_t valid_parts = __ballot_sync(0xffffffffu, valid) & 0xffu;
-                    // the scales go ahead of the tile
-                    if (n >= L::kPageBufs)
-                        ok = wait_bar(smem_u32(&bars->pages_free[pb]), (n / L::kPageBufs - 1) & 1, abort, kErrPagedSoftmax + 6);
-                    if (ok && tid < 8) {
-                        pages[pb * 8 + tid] = make_float4(ks * p.scale_log2, valid ? __log2f(vs) : -INFINITY, __fdividef(1.f, vs),
-                                                          valid_parts == 0xffu ? 0.f : 1.f);
-                        mbar_arrive(smem_u32(&bars->pages_full[pb]));
+                    ok = wait_bar(smem_u32(&bars->pages_full[pb]), (n / L::kPageBufs) & 1, abort, kErrPagedSoftmax + 6);
+                    uint32_t valid_parts = 0xffu;
+                    if (pages[pb * 8].w != 0.f) {
+                        valid_parts = 0;
+                        for (int i = 0; i < 8; ++i)
+                            valid_parts |= pages[pb * 8 + i].y == -INFINITY ? 0u : 1u << i;
                     }
                     if (n >= 2)
                         ok = ok && wait_bar(smem_u32(&bars->v16_empty[b]), (n / 2 - 1) & 1, abort, kErrPagedSoftmax + 5);
@@ -366,6 +374,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         }
                     }
                     fence_proxy_async_smem();
+                    mbar_arrive(smem_u32(&bars->pages_free[pb]));
                     mbar_arrive(smem_u32(&bars->v_empty[ring]));
                     mbar_arrive(smem_u32(&bars->v16_full[b]));
                 }
