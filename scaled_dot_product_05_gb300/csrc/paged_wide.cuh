@@ -29,7 +29,7 @@ constexpr float kWideLog2W = 7.0f;         // weight 1 is held as 2^7: 2^15 at m
 template <int D, bool kBF16>
 struct WideLayout {
     static constexpr int kParts = kBF16 ? 2 : 3;
-    static constexpr int kThreads = 384;   // 8 softmax warps; TMA producer, MMA issuer, 2 converters
+    static constexpr int kThreads = 384;   // 8 softmax warps; TMA producer, S issuer, 2 converters
     static constexpr int kTileBytes = kTileKeys * D;            // 8-bit K or V tile, a part of Q
     static constexpr int kV16Bytes = kTileKeys * D * 2;
     static constexpr int kStagesK = D == 64 ? 4 : 3;
@@ -54,7 +54,7 @@ struct WideBarriers {
     uint64_t v16_full[2], v16_empty[2];    // converted V tile written / multiplied
     uint64_t pages_full[4], pages_free[4]; // a tile's scales written / read
     uint64_t s_full[2], s_free[2], w_full[2], pv_done[2];
-    uint64_t q_full, o_free, drain;
+    uint64_t q_full, o_free, drain[2];     // drain: one for each issuing thread
     uint32_t tmem_base;
     int abort;
     long long total, x, x_first;
@@ -111,7 +111,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         mbar_init(smem_u32(&bars->q_full), 256);
         mbar_init(smem_u32(&bars->o_free), 256);
-        mbar_init(smem_u32(&bars->drain), 1);
+        mbar_init(smem_u32(&bars->drain[0]), 1);
+        mbar_init(smem_u32(&bars->drain[1]), 1);
         bars->abort = 0;
         fence_mbar_init();
     }
@@ -226,30 +227,25 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             }
             __syncwarp();
         } else if (warp == 9) {
-            // ========================== MMA issuer ==========================
-            // S(0), S(1), then for each tile j S(j + 2) and W V of tile j: a
-            // warpgroup finds its next scores when it has written its weights
+            // =========================== S issuer ===========================
+            // S of tile j + 1 as soon as the scores of tile j have been read
             if (lane == 0) {
                 constexpr uint32_t kSwzCode = D == 128 ? 2u : 4u;
                 constexpr uint32_t idesc_s = idesc_make(0u, NR, kTileKeys, false);
-                constexpr uint32_t idesc_o = idesc_make(0u, NR, D, true);
                 const uint32_t hi = (uint32_t)(smem_desc(0, 16, 8 * D, kSwzCode) >> 32);
-                const uint32_t hi_v = (uint32_t)(smem_desc(0, 16, 1024, 2u) >> 32);
-                constexpr uint32_t kLboV = (uint32_t)((kTileKeys * 128) >> 4) << 16;    // next 64 channels
-                uint32_t ns = 0, nv = 0, pieces = 0, w0 = 0, w1 = 0;
-                uint32_t f0 = 0, f1 = 0;                   // S issued for each warpgroup
-                int prev = -1;                             // warpgroup of the last S
+                uint32_t ns = 0, pieces = 0, f0 = 0, f1 = 0;       // S issued: all, for each warpgroup
+                int prev = -1;                                     // warpgroup of the last S
                 bool ok = true;
                 for (; ok && more; more = next_piece<NR>(p, w), ++pieces) {
-                    const int n = w.end - w.begin;
-                    auto issue_s = [&](int g) -> bool {
+                    ok = wait_bar(smem_u32(&bars->q_full), pieces & 1, abort, kErrPagedMma + 2);
+                    for (int j = 0; ok && j < w.end - w.begin; ++j, ++ns) {
+                        const int g = j & 1;
                         const uint32_t ks = ns % NK;
-                        if (!wait_bar(smem_u32(&bars->k_full[ks]), (ns / NK) & 1, abort, kErrPagedMma))
-                            return false;
-                        // the S before has been read out of the region
-                        if (prev >= 0 &&
-                            !wait_bar(smem_u32(&bars->s_free[prev]), ((prev ? f1 : f0) - 1) & 1, abort, kErrPagedMma + 1))
-                            return false;
+                        ok = wait_bar(smem_u32(&bars->k_full[ks]), (ns / NK) & 1, abort, kErrPagedMma) &&
+                             (prev < 0 ||
+                              wait_bar(smem_u32(&bars->s_free[prev]), ((prev ? f1 : f0) - 1) & 1, abort, kErrPagedMma + 1));
+                        if (!ok)
+                            break;
                         tc_fence_after_sync();
                         const uint32_t k_lo = ((sK + ks * L::kTileBytes) >> 4) | (1u << 16);
 #pragma unroll
@@ -262,25 +258,38 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         }
                         mma_commit(smem_u32(&bars->s_full[g]));
                         mma_commit(smem_u32(&bars->k_empty[ks]));
-                        ++ns;
                         f0 += g ? 0 : 1;
                         f1 += g ? 1 : 0;
                         prev = g;
-                        return true;
-                    };
-                    ok = wait_bar(smem_u32(&bars->q_full), pieces & 1, abort, kErrPagedMma + 2) && issue_s(0) &&
-                         (n == 1 || issue_s(1));
-                    for (int j = 0; ok && j < n; ++j, ++nv) {
-                        const int g = j & 1;
-                        if (j + 2 < n && !(ok = issue_s(g)))
-                            break;
-                        if (j == 0 && pieces > 0 &&
-                            !(ok = wait_bar(smem_u32(&bars->o_free), (pieces - 1) & 1, abort, kErrPagedMma + 5)))
-                            break;
-                        ok = wait_bar(smem_u32(&bars->v16_full[nv & 1]), (nv / 2) & 1, abort, kErrPagedMma + 3) &&
-                             wait_bar(smem_u32(&bars->w_full[g]), (g ? w1 : w0) & 1, abort, kErrPagedMma + 4);
-                        if (!ok)
-                            break;
+                    }
+                }
+                mma_commit(smem_u32(&bars->drain[0]));
+                drain_wait(smem_u32(&bars->drain[0]), 0);
+            }
+            __syncwarp();
+        } else {
+            // ========================== converters ==========================
+            // V's codes to f16, 16 at a time, into the layout of a 16-bit tile
+            // (64 channels a chunk, 128-byte rows); rows that no row of the item
+            // sees are zero, a NaN that only some see is taken out and kept in
+            // mind.  Thread 0 also issues W V, of tile j when it has converted
+            // tile j + 1.
+            const int tid = threadIdx.x - 320;                              // 0 .. 63
+            constexpr uint32_t idesc_o = idesc_make(0u, NR, D, true);
+            const uint32_t hi_v = (uint32_t)(smem_desc(0, 16, 1024, 2u) >> 32);
+            constexpr uint32_t kLboV = (uint32_t)((kTileKeys * 128) >> 4) << 16;        // next 64 channels
+            uint32_t n = 0, pieces = 0, w0 = 0, w1 = 0;
+            bool ok = true;
+            // O (+)= W V of the piece's tile j, the CTA's tile nv
+            auto multiply = [&](int j, uint32_t nv) -> bool {
+                bool good = true;
+                if (tid == 0) {
+                    const int g = j & 1;
+                    good = wait_bar(smem_u32(&bars->v16_full[nv & 1]), (nv / 2) & 1, abort, kErrPagedMma + 3) &&
+                           wait_bar(smem_u32(&bars->w_full[g]), (g ? w1 : w0) & 1, abort, kErrPagedMma + 4) &&
+                           (j > 0 || pieces == 0 ||
+                            wait_bar(smem_u32(&bars->o_free), (pieces - 1) & 1, abort, kErrPagedMma + 5));
+                    if (good) {
                         tc_fence_after_sync();
                         const uint32_t v_lo = ((sV16 + (nv & 1) * L::kV16Bytes) >> 4) | kLboV;
 #pragma unroll
@@ -293,19 +302,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         w1 += g ? 1 : 0;
                     }
                 }
-                mma_commit(smem_u32(&bars->drain));
-                drain_wait(smem_u32(&bars->drain), 0);
-            }
-            __syncwarp();
-        } else {
-            // ========================== converters ==========================
-            // V's codes to f16, 16 at a time, into the layout of a 16-bit tile
-            // (64 channels a chunk, 128-byte rows); rows that no row of the item
-            // sees are zero, a NaN that only some see is taken out and kept in
-            // mind
-            const int tid = threadIdx.x - 320;                              // 0 .. 63
-            uint32_t n = 0, pieces = 0;
-            bool ok = true;
+                return __all_sync(0xffffffffu, good);
+            };
             for (; ok && more; more = next_piece<NR>(p, w), ++pieces) {
                 const Item it = item_of<NR>(p, w);
                 // the piece before has been read out and its NaN forgotten
@@ -336,24 +334,24 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     const uint32_t row = sV16 + b * L::kV16Bytes + (c / 4) * (kTileKeys * 128) + key0 * 128;
                     const uint32_t dst0 = row + (((c % 4) * 2) ^ (key0 & 7)) * 16, dst1 = row + (((c % 4) * 2 + 1) ^ (key0 & 7)) * 16;
                     if ((j + 1) * kTileKeys > full || valid_parts != 0xffu) {
-#pragma unroll 1
+#pragma unroll 4
                         for (int i = 0; i < kTurns; ++i) {
                             const int key = key0 + i * kStep, pos = j * kTileKeys + key;
-                            uint32_t* u = reinterpret_cast<uint32_t*>(src + i * kStep * D);
+                            uint4* u = reinterpret_cast<uint4*>(src + i * kStep * D);
                             if (pos >= it.keys || !(valid_parts >> (key / 16) & 1)) {
-                                for (int e = 0; e < 4; ++e)
-                                    u[e] = 0;
+                                *u = make_uint4(0, 0, 0, 0);
                             } else if (pos >= full) {
-                                for (int e = 0; e < 4; ++e) {
-                                    const uint32_t hit = ((u[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;    // 0x7F, 0xFF
-                                    if (!hit)
-                                        continue;
+                                const uint4 q = *u;
+                                auto nans = [](uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };    // 0x7F, 0xFF
+                                if (nans(q.x) | nans(q.y) | nans(q.z) | nans(q.w)) {
                                     *any_nan = 1;
-                                    for (int f = 0; f < 4; ++f)
-                                        if (hit >> (8 * f + 7) & 1) {
-                                            atomicMin(&nan_at[16 * c + 4 * e + f], pos);
-                                            u[e] &= ~(0xffu << (8 * f));
+                                    for (int e = 0; e < 16; ++e) {
+                                        uint8_t* byte = src + i * kStep * D + e;
+                                        if ((*byte & 0x7f) == 0x7f) {
+                                            atomicMin(&nan_at[16 * c + e], pos);
+                                            *byte = 0;
                                         }
+                                    }
                                 }
                             }
                         }
@@ -377,8 +375,16 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     mbar_arrive(smem_u32(&bars->pages_free[pb]));
                     mbar_arrive(smem_u32(&bars->v_empty[ring]));
                     mbar_arrive(smem_u32(&bars->v16_full[b]));
+                    if (j > w.begin)
+                        ok = multiply(j - 1 - w.begin, n - 1);
                 }
+                ok = ok && multiply(w.end - 1 - w.begin, n - 1);
             }
+            if (tid == 0) {
+                mma_commit(smem_u32(&bars->drain[1]));
+                drain_wait(smem_u32(&bars->drain[1]), 0);
+            }
+            __syncwarp();
         }
     } else {
         regs_acquire<192>();
@@ -401,27 +407,27 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 const uint4* q = reinterpret_cast<const uint4*>(
                     reinterpret_cast<const uint16_t*>(p.Q) + (long long)it.b * p.q_sb + (long long)i * p.q_ss +
                     (long long)(w.h * p.group + hh) * p.q_sh + half * (D / 2));
-                uint4 u[D / 16];
                 uint32_t top = 0;
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
-                    u[s] = live ? q[s] : make_uint4(0, 0, 0, 0);
+                    const uint4 u = live ? q[s] : make_uint4(0, 0, 0, 0);
                     float v[8];
-                    rope::unpack4<kBF16>(make_uint2(u[s].x, u[s].y), v);
-                    rope::unpack4<kBF16>(make_uint2(u[s].z, u[s].w), v + 4);
+                    rope::unpack4<kBF16>(make_uint2(u.x, u.y), v);
+                    rope::unpack4<kBF16>(make_uint2(u.z, u.w), v + 4);
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
                 }
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 const float qs = cache::pow2_scale(__uint_as_float(top)), inv = 1.f / qs;
-#pragma unroll
-                for (int s = 0; s < D / 32; ++s) {
+#pragma unroll 1
+                for (int s = 0; s < D / 32; ++s) {         // (rolled: code that runs once an item is fetched anew each time)
                     float v[16];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        rope::unpack4<kBF16>(make_uint2(u[2 * s + c].x, u[2 * s + c].y), &v[8 * c]);
-                        rope::unpack4<kBF16>(make_uint2(u[2 * s + c].z, u[2 * s + c].w), &v[8 * c + 4]);
+                        const uint4 u = live ? q[2 * s + c] : make_uint4(0, 0, 0, 0);
+                        rope::unpack4<kBF16>(make_uint2(u.x, u.y), &v[8 * c]);
+                        rope::unpack4<kBF16>(make_uint2(u.z, u.w), &v[8 * c + 4]);
                     }
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
@@ -503,9 +509,12 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (__builtin_expect(edge || pages[buf * 8].w != 0.f, 0)) {
                     const int seen_keys = seen_end - j * kTileKeys;             // of the tile, less one
 #pragma unroll
-                    for (int e = 0; e < 128; ++e)
-                        if (e > seen_keys || pages[buf * 8 + e / 16].y == -INFINITY)
-                            r[e] = 0xff800000u;
+                    for (int c = 0; c < 8; ++c) {
+                        const int end = pages[buf * 8 + c].y == -INFINITY ? -1 : seen_keys;
+#pragma unroll
+                        for (int e = 16 * c; e < 16 * c + 16; ++e)
+                            r[e] = e > end ? 0xff800000u : r[e];
+                    }
                 }
                 float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
