@@ -10,7 +10,8 @@
 // smallest step 2^-31 of that) and stay in tensor memory, and V's codes are
 // turned into f16, which holds them exactly, by two warps of their own.  The
 // two softmax warpgroups take alternate key tiles of the same rows, each with
-// its own maxima, sums and accumulator, joined when the item is done; the
+// its own maxima, sums and accumulator, joined when the item is done, and
+// issue their own W V; the
 // scores of both go through one region of tensor memory, which is free for
 // the next tile's as soon as they are read.  Bound by the tensor cores (128 x
 // 128 x D FP8 products for each part of q and the f16 product: 1056 cycles a
@@ -54,7 +55,7 @@ struct WideBarriers {
     uint64_t v16_full[2], v16_empty[2];    // converted V tile written / multiplied
     uint64_t pages_full[4], pages_free[4]; // a tile's scales written / read
     uint64_t s_full[2], s_free[2], w_full[2], pv_done[2];
-    uint64_t q_full, o_free, drain[2];     // drain: one for each issuing thread
+    uint64_t q_full, drain[3];             // drain: one for each issuing thread
     uint32_t tmem_base;
     int abort;
     long long total, x, x_first;
@@ -110,9 +111,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             mbar_init(smem_u32(&bars->pages_free[i]), 128 + 64);
         }
         mbar_init(smem_u32(&bars->q_full), 256);
-        mbar_init(smem_u32(&bars->o_free), 256);
-        mbar_init(smem_u32(&bars->drain[0]), 1);
-        mbar_init(smem_u32(&bars->drain[1]), 1);
+        for (int i = 0; i < 3; ++i)
+            mbar_init(smem_u32(&bars->drain[i]), 1);
         bars->abort = 0;
         fence_mbar_init();
     }
@@ -272,38 +272,10 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             // V's codes to f16, 16 at a time, into the layout of a 16-bit tile
             // (64 channels a chunk, 128-byte rows); rows that no row of the item
             // sees are zero, a NaN that only some see is taken out and kept in
-            // mind.  Thread 0 also issues W V, of tile j when it has converted
-            // tile j + 1.
+            // mind
             const int tid = threadIdx.x - 320;                              // 0 .. 63
-            constexpr uint32_t idesc_o = idesc_make(0u, NR, D, true);
-            const uint32_t hi_v = (uint32_t)(smem_desc(0, 16, 1024, 2u) >> 32);
-            constexpr uint32_t kLboV = (uint32_t)((kTileKeys * 128) >> 4) << 16;        // next 64 channels
-            uint32_t n = 0, pieces = 0, w0 = 0, w1 = 0;
+            uint32_t n = 0, pieces = 0;
             bool ok = true;
-            // O (+)= W V of the piece's tile j, the CTA's tile nv
-            auto multiply = [&](int j, uint32_t nv) -> bool {
-                bool good = true;
-                if (tid == 0) {
-                    const int g = j & 1;
-                    good = wait_bar(smem_u32(&bars->v16_full[nv & 1]), (nv / 2) & 1, abort, kErrPagedMma + 3) &&
-                           wait_bar(smem_u32(&bars->w_full[g]), (g ? w1 : w0) & 1, abort, kErrPagedMma + 4) &&
-                           (j > 0 || pieces == 0 ||
-                            wait_bar(smem_u32(&bars->o_free), (pieces - 1) & 1, abort, kErrPagedMma + 5));
-                    if (good) {
-                        tc_fence_after_sync();
-                        const uint32_t v_lo = ((sV16 + (nv & 1) * L::kV16Bytes) >> 4) | kLboV;
-#pragma unroll
-                        for (int kk = 0; kk < kTileKeys / 16; ++kk)
-                            mma_f16_ts(tmem + 256 + 128 * g, tmem + 128 + 64 * g + kk * 8,
-                                       desc_join(hi_v, v_lo + (uint32_t)((kk * 16 * 128) >> 4)), idesc_o, j >= 2 || kk > 0);
-                        mma_commit(smem_u32(&bars->pv_done[g]));
-                        mma_commit(smem_u32(&bars->v16_empty[nv & 1]));
-                        w0 += g ? 0 : 1;
-                        w1 += g ? 1 : 0;
-                    }
-                }
-                return __all_sync(0xffffffffu, good);
-            };
             for (; ok && more; more = next_piece<NR>(p, w), ++pieces) {
                 const Item it = item_of<NR>(p, w);
                 // the piece before has been read out and its NaN forgotten
@@ -375,16 +347,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     mbar_arrive(smem_u32(&bars->pages_free[pb]));
                     mbar_arrive(smem_u32(&bars->v_empty[ring]));
                     mbar_arrive(smem_u32(&bars->v16_full[b]));
-                    if (j > w.begin)
-                        ok = multiply(j - 1 - w.begin, n - 1);
                 }
-                ok = ok && multiply(w.end - 1 - w.begin, n - 1);
             }
-            if (tid == 0) {
-                mma_commit(smem_u32(&bars->drain[1]));
-                drain_wait(smem_u32(&bars->drain[1]), 0);
-            }
-            __syncwarp();
         }
     } else {
         regs_acquire<192>();
@@ -392,6 +356,9 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const int g = warp >> 2;
         const int row = threadIdx.x & 127;                                  // of the tile; TMEM lane
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        constexpr uint32_t idesc_o = idesc_make(0u, NR, D, true);
+        const uint32_t hi_v = (uint32_t)(smem_desc(0, 16, 1024, 2u) >> 32);
+        constexpr uint32_t kLboV = (uint32_t)((kTileKeys * 128) >> 4) << 16;            // next 64 channels
         const uint32_t t_s = tmem + lanes, t_w = t_s + 128 + 64 * g, t_o = t_s + 256 + 128 * g;
         uint32_t ns = 0;                                                    // tiles of this warpgroup so far
         uint32_t nv = 0;                                                    // tiles of the CTA before this piece
@@ -585,6 +552,24 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 tmem_st_wait();
                 tc_fence_before_sync();
                 mbar_arrive(smem_u32(&bars->w_full[g]));
+                // O (+)= W V: the warpgroup's first thread issues it when all
+                // weights and the tile's V are there
+                if (row == 0) {
+                    const uint32_t vb = vn & 1;
+                    ok = wait_bar(smem_u32(&bars->w_full[g]), ns & 1, abort, kErrPagedMma + 4) &&
+                         wait_bar(smem_u32(&bars->v16_full[vb]), (vn / 2) & 1, abort, kErrPagedMma + 3);
+                    if (ok) {
+                        tc_fence_after_sync();
+                        const uint32_t v_lo = ((sV16 + vb * L::kV16Bytes) >> 4) | kLboV;
+#pragma unroll
+                        for (int kk = 0; kk < kTileKeys / 16; ++kk)
+                            mma_f16_ts(tmem + 256 + 128 * g, tmem + 128 + 64 * g + kk * 8,
+                                       desc_join(hi_v, v_lo + (uint32_t)((kk * 16 * 128) >> 4)), idesc_o, j > g || kk > 0);
+                        mma_commit(smem_u32(&bars->pv_done[g]));
+                        mma_commit(smem_u32(&bars->v16_empty[vb]));
+                    }
+                }
+                __syncwarp();
             }
             // ---- the piece's result: both warpgroups' accumulators, a half of the channels each
             w = bars->piece;
@@ -654,9 +639,14 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 }
             }
             tc_fence_before_sync();
-            mbar_arrive(smem_u32(&bars->o_free));
-            named_bar_sync(kBarSoftmax, 256);                  // the rows' numbers are read
+            named_bar_sync(kBarSoftmax, 256);                  // the rows' numbers and O are read
+            tc_fence_after_sync();
         }
+        if (row == 0) {                                        // every product that this thread issued has completed
+            mma_commit(smem_u32(&bars->drain[1 + g]));
+            drain_wait(smem_u32(&bars->drain[1 + g]), 0);
+        }
+        __syncwarp();
     }
     tc_fence_before_sync();
     __syncthreads();
