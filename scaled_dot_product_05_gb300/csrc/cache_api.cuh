@@ -118,7 +118,7 @@ struct NormRopeArgs {
 // side's items, at most one block for each group-sized set of items.
 void bwd_blocks(long long tokens, const int* H, int D, int* blocks)
 {
-    const long long groups = sdpa::rope::kNormThreads / (D / 8);
+    const long long groups = sdpa::rope::kBwdThreads / (D / 8);
     long long items[2], total = 0;
     for (int k = 0; k < 2; ++k) {
         items[k] = tokens * ((H[k] + sdpa::rope::kBwdHeads - 1) / sdpa::rope::kBwdHeads);
@@ -146,12 +146,12 @@ cudaError_t launch_norm_rope(const sdpa::rope::NormRopeParams& p, bool backward,
     using namespace sdpa::rope;
     constexpr int kGroups = kNormThreads / (D / 8);
     if (!backward) {
-        const long long items = p.tokens * (p.side[0].chunks + p.side[1].chunks);
+        const long long items = static_cast<long long>(p.tokens) * (p.side[0].chunks + p.side[1].chunks);
         return launch_pdl(true, norm_rope_kernel<D, kBF16, kInter>, dim3(static_cast<unsigned>((items + kGroups - 1) / kGroups)),
                           dim3(kNormThreads), 0, stream, p);
     }
     cudaError_t e = launch_pdl(true, norm_rope_bwd_kernel<D, kBF16, kInter>, dim3(p.blocks[0] + p.blocks[1]),
-                               dim3(kNormThreads), 0, stream, p);
+                               dim3(kBwdThreads), 0, stream, p);
     if (e == cudaSuccess && p.part)
         e = launch_pdl(true, norm_dw_kernel, dim3(D / kDwCols, p.side[1].H ? 2 : 1), dim3(kDwThreads), 0, stream, p, D);
     return e;
@@ -270,7 +270,7 @@ sdpa_status_t run_norm_rope(NormRopeArgs& a, void* stream)
     }
     p.positions = a.positions;
     p.S = a.S;
-    p.tokens = tokens;
+    p.tokens = static_cast<uint32_t>(tokens);
     p.norm = a.norm != 0;
     p.w16 = a.w_dtype != SDPA_DTYPE_F32;
     p.eps = a.eps;
@@ -324,8 +324,19 @@ cudaError_t launch_append(const sdpa::cache::AppendParams& p, cudaStream_t strea
     if (p.S <= 4 * (256 / D))
         return launch_pdl(true, append_kernel<D, kBF16, kInter, 1, 4>, dim3(static_cast<unsigned>((units + 7) / 8)),
                           dim3(kAppendThreads), 0, stream, p);
-    return launch_pdl(true, append_kernel<D, kBF16, kInter, 8, D / 16>, dim3(static_cast<unsigned>(units)),
-                      dim3(kAppendThreads), 0, stream, p);
+    // eight warps a unit: 2048 / D rows a pass, as many passes as a page has
+    auto go = [&](auto passes) {
+        return launch_pdl(true, append_kernel<D, kBF16, kInter, 8, decltype(passes)::value>, dim3(static_cast<unsigned>(units)),
+                          dim3(kAppendThreads), 0, stream, p);
+    };
+    const int passes = (p.page * D + 2047) / 2048;
+    if (passes <= 1)
+        return go(std::integral_constant<int, 1>{});
+    if (passes <= 2)
+        return go(std::integral_constant<int, 2>{});
+    if (passes <= 4)
+        return go(std::integral_constant<int, 4>{});
+    return go(std::integral_constant<int, 8>{});
 }
 
 template <int D>

@@ -103,12 +103,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
             atomicCAS(&g_sdpa_error, 0u, (unsigned)kErrTable);
         return;
     }
-    const int id = p.table[(long long)b * p.max_pages + ord_page];
-    if ((unsigned)id >= (unsigned)p.n_pages) {
-        if (tid == 0)
-            atomicCAS(&g_sdpa_error, 0u, (unsigned)kErrPage);
-        return;
-    }
+    const int id = p.table[(long long)b * p.max_pages + ord_page];     // (looked at when the rows are on their way)
     const int rot = kv ? 0 : p.rot;                    // only the keys are rotated
     int a, c;
     rope::lane_channels<kInter>(lane, rot, a, c);
@@ -128,6 +123,14 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
             ok |= 1u << n;
         }
     }
+    if ((unsigned)id >= (unsigned)p.n_pages) {         // the whole unit
+        if (tid == 0)
+            atomicCAS(&g_sdpa_error, 0u, (unsigned)kErrPage);
+        return;
+    }
+    const Pool pool = p.pool[kv];
+    float* scale_at = pool.scale + (long long)id * p.Hkv + h;
+    const float old = *scale_at;                       // before the barrier: written after it
     float amax = 0.f;
 #pragma unroll
     for (int n = 0; n < kPasses; ++n) {
@@ -156,9 +159,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-    const Pool pool = p.pool[kv];
-    float* scale_at = pool.scale + (long long)id * p.Hkv + h;
-    const float old = *scale_at;                       // before the barrier: written after it
     if constexpr (kWarps > 1) {
         if ((threadIdx.x & 31) == 0)
             warp_max[threadIdx.x >> 5] = amax;

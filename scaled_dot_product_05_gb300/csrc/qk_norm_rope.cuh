@@ -36,7 +36,7 @@ struct NormRopeParams {
     const float* table;          // [n_pos][rot / 2][2]: cos, sin
     const int* positions;        // [B][S], or null: position s
     int S, n_pos, rot;
-    long long tokens;            // B * S
+    uint32_t tokens;             // B * S
     int norm, w16;               // w16: weights are 16-bit like x, else fp32
     float eps;
     float* part;                 // backward: dw partial sums [blocks][D]
@@ -44,7 +44,9 @@ struct NormRopeParams {
     float* dw[2];
 };
 
-constexpr int kNormThreads = 256;
+// Measured (B = 2, S = 4096, 40 heads of 128): 128 threads a block 30.6 us, 256
+// 33.2 us.
+constexpr int kNormThreads = 128;
 
 template <bool kBF16>
 __device__ __forceinline__ float weight_at(const void* w, int w16, int c)
@@ -60,6 +62,9 @@ __device__ __forceinline__ float weight_at(const void* w, int w16, int c)
 }
 
 // One item: kHeads consecutive heads of one token, by a group of D / 8 lanes.
+// More heads share a token's angles and have more loads in flight, but leave a
+// decoding step with fewer groups (measured at 2, 4 and 8 heads: 39, 31 and 29
+// us for the training batch, 2.2, 2.3 and 3.1 us for 64 tokens).
 constexpr int kHeads = 4;
 
 template <int D, bool kBF16, bool kInter>
@@ -69,16 +74,17 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormRopeP
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x % kLanes;
-    const int per_token = p.side[0].chunks + p.side[1].chunks;
-    const long long item = (long long)blockIdx.x * (kNormThreads / kLanes) + threadIdx.x / kLanes;
-    const long long token = item / per_token;
+    // (items fit into 31 bits: the host refuses more)
+    const uint32_t per_token = p.side[0].chunks + p.side[1].chunks;
+    const uint32_t item = blockIdx.x * (kNormThreads / kLanes) + threadIdx.x / kLanes;
+    const uint32_t token = item / per_token;
     const bool live = token < p.tokens;
     int chunk = (int)(item - token * per_token);
     const int k = chunk >= p.side[0].chunks;
     const Side& sd = p.side[k];
     chunk -= k ? p.side[0].chunks : 0;
-    const int b = live ? (int)(token / p.S) : 0;
-    const int s = live ? (int)(token - (long long)b * p.S) : 0;
+    const int b = live ? (int)(token / (uint32_t)p.S) : 0;
+    const int s = live ? (int)token - b * p.S : 0;
     int n_heads = live ? min(kHeads, sd.H - chunk * kHeads) : 0;
     int a, c;
     lane_channels<kInter>(lane, p.rot, a, c);
@@ -137,15 +143,23 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormRopeP
 
 // Blocks of the backward pass (both sides together at most): each walks many
 // items, so that dw is summed in registers and leaves as one row of partial
-// sums a block.
-constexpr int kBwdBlocks = 608;
-constexpr int kBwdHeads = 2;
+// sums a block.  All blocks are resident at once, five on each of 152 SMs
+// (measured, training batch of 8192 tokens x 40 heads of 128 / 3996 x 32 of 64,
+// the sum kernel included: 52 / 13.2 us; 4 blocks of 256 threads and 2 heads an
+// item 53 / 14.3 us; a second item's loads ahead of the first's arithmetic cost
+// more in occupancy than they hid, 62 us).
+constexpr int kBwdThreads = 128;
+constexpr int kBwdBlocks = 760;
+constexpr int kBwdHeads = 4;
 
+// Instructions count here as much as bytes (some 110 a lane and row): all
+// arithmetic is on packed pairs, of a run's neighbouring channels with the
+// halves order, of a rotated pair's two channels with the interleaved one.
 template <int D, bool kBF16, bool kInter>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_bwd_kernel(const NormRopeParams p)
+__global__ void __launch_bounds__(kBwdThreads, 5) norm_rope_bwd_kernel(const NormRopeParams p)
 {
     constexpr int kLanes = D / 8;
-    constexpr int kGroups = kNormThreads / kLanes;
+    constexpr int kGroups = kBwdThreads / kLanes;
     __shared__ float sums[kGroups][D];
     grid_dependency_wait();
     grid_launch_dependents();
@@ -156,25 +170,24 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_bwd_kernel(const NormR
     const int block = blockIdx.x - (k ? p.blocks[0] : 0);
     int a, c;
     lane_channels<kInter>(lane, p.rot, a, c);
-    float w[8], dw[8];
+    uint64_t w[4], dw[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        w[i] = p.norm ? weight_at<kBF16>(sd.w, p.w16, a + i) : 1.f;
-        w[4 + i] = p.norm ? weight_at<kBF16>(sd.w, p.w16, c + i) : 1.f;
+        const int at = i < 2 ? a + 2 * i : c + 2 * (i - 2);
+        w[i] = p.norm ? f32x2(weight_at<kBF16>(sd.w, p.w16, at), weight_at<kBF16>(sd.w, p.w16, at + 1)) : f32x2(1.f, 1.f);
+        dw[i] = 0;
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        dw[i] = 0.f;
-    const long long items = p.tokens * sd.chunks;
-    const long long stride = (long long)p.blocks[k] * kGroups;
+    // (items fit into 31 bits: the host refuses more)
+    const uint32_t items = p.tokens * sd.chunks;
+    const uint32_t stride = p.blocks[k] * kGroups;
     // every group of a warp runs the same number of turns: the sums shuffle
-    for (long long first = (long long)block * kGroups; first < items; first += stride) {
-        const long long item = first + group;
+    for (uint32_t first = block * kGroups; first < items; first += stride) {
+        const uint32_t item = first + group;
         const bool live = item < items;
-        const long long token = live ? item / sd.chunks : 0;
+        const uint32_t token = live ? item / (uint32_t)sd.chunks : 0;
         const int chunk = live ? (int)(item - token * sd.chunks) : 0;
-        const int b = (int)(token / p.S);
-        const int s = (int)(token - (long long)b * p.S);
+        const int b = (int)(token / (uint32_t)p.S);
+        const int s = (int)token - b * p.S;
         int n_heads = live ? min(kBwdHeads, sd.H - chunk * kBwdHeads) : 0;
         int pos = 0;
         if (p.rot) {
@@ -204,42 +217,54 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_bwd_kernel(const NormR
         }
         float cs[4], sn[4];
         lane_angles(p.table, pos, p.rot, lane, cs, sn);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            sn[i] = -sn[i];                        // the inverse rotation
         uint16_t* y = reinterpret_cast<uint16_t*>(sd.y) + b * sd.y_sb + s * sd.y_ss + h0 * sd.y_sh;
 #pragma unroll
         for (int h = 0; h < kBwdHeads; ++h) {
-            float u[8];
-            unpack4<kBF16>(ga[h], u);
-            unpack4<kBF16>(gb[h], u + 4);
-            rotate<kInter>(u, cs, sn);
-            if (p.norm) {
-                float v[8];
-                unpack4<kBF16>(xa[h], v);
-                unpack4<kBF16>(xb[h], v + 4);
-                float ss = 0.f;
+            uint64_t u[4];
+            unpack_pairs<kBF16>(ga[h], u);
+            unpack_pairs<kBF16>(gb[h], u + 2);
+            // the inverse rotation
+            if constexpr (kInter) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    ss = fmaf(v[i], v[i], ss);
-                const float r = rsqrtf(group_sum<kLanes>(ss) * (1.f / D) + p.eps);
-                float along = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    v[i] *= r;
-                    if (h < n_heads)
-                        dw[i] = fmaf(u[i], v[i], dw[i]);
-                    u[i] *= w[i];
-                    along = fmaf(u[i], v[i], along);
+                for (int i = 0; i < 4; ++i) {                  // (x cos + y sin, y cos - x sin)
+                    float e, f;
+                    f32x2_split(u[i], e, f);
+                    u[i] = fma_f32x2(f32x2(f, e), f32x2(sn[i], -sn[i]), mul_f32x2(u[i], f32x2(cs[i], cs[i])));
                 }
-                along = group_sum<kLanes>(along) * (1.f / D);
+            } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    u[i] = r * (u[i] - v[i] * along);
+                for (int i = 0; i < 2; ++i) {
+                    const uint64_t co = f32x2(cs[2 * i], cs[2 * i + 1]);
+                    const uint64_t si = f32x2(sn[2 * i], sn[2 * i + 1]), ni = f32x2(-sn[2 * i], -sn[2 * i + 1]);
+                    const uint64_t e = u[i], f = u[2 + i];
+                    u[i] = fma_f32x2(f, si, mul_f32x2(e, co));
+                    u[2 + i] = fma_f32x2(e, ni, mul_f32x2(f, co));
+                }
+            }
+            if (p.norm) {
+                uint64_t v[4];
+                unpack_pairs<kBF16>(xa[h], v);
+                unpack_pairs<kBF16>(xb[h], v + 2);
+                const float ss = sum_pairs(fma_f32x2(v[0], v[0], mul_f32x2(v[1], v[1])), fma_f32x2(v[2], v[2], mul_f32x2(v[3], v[3])));
+                const float r = rsqrtf(group_sum<kLanes>(ss) * (1.f / D) + p.eps);
+                const uint64_t r2 = f32x2(r, r);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i] = mul_f32x2(v[i], r2);
+                    if (h < n_heads)
+                        dw[i] = fma_f32x2(u[i], v[i], dw[i]);
+                    u[i] = mul_f32x2(u[i], w[i]);
+                }
+                float along = sum_pairs(fma_f32x2(u[0], v[0], mul_f32x2(u[1], v[1])), fma_f32x2(u[2], v[2], mul_f32x2(u[3], v[3])));
+                along = group_sum<kLanes>(along) * (-1.f / D);
+                const uint64_t al = f32x2(along, along);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    u[i] = mul_f32x2(r2, fma_f32x2(v[i], al, u[i]));
             }
             if (h < n_heads) {
-                *reinterpret_cast<uint2*>(y + h * sd.y_sh + a) = pack4<kBF16>(u);
-                *reinterpret_cast<uint2*>(y + h * sd.y_sh + c) = pack4<kBF16>(u + 4);
+                *reinterpret_cast<uint2*>(y + h * sd.y_sh + a) = pack_pairs<kBF16>(u);
+                *reinterpret_cast<uint2*>(y + h * sd.y_sh + c) = pack_pairs<kBF16>(u + 2);
             }
         }
     }
@@ -247,11 +272,14 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_bwd_kernel(const NormR
         return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        sums[group][a + i] = dw[i];
-        sums[group][c + i] = dw[4 + i];
+        float e, f;
+        f32x2_split(dw[i], e, f);
+        const int at = i < 2 ? a + 2 * i : c + 2 * (i - 2);
+        sums[group][at] = e;
+        sums[group][at + 1] = f;
     }
     __syncthreads();
-    for (int d = threadIdx.x; d < D; d += kNormThreads) {
+    for (int d = threadIdx.x; d < D; d += kBwdThreads) {
         float t = 0.f;
 #pragma unroll
         for (int g = 0; g < kGroups; ++g)

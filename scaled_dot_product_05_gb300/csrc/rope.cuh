@@ -62,6 +62,32 @@ __device__ __forceinline__ uint2 pack4(const float* x)
     return make_uint2(pack2<kBF16>(x[0], x[1]), pack2<kBF16>(x[2], x[3]));
 }
 
+// The same as packed pairs of neighbours.
+template <bool kBF16>
+__device__ __forceinline__ void unpack_pairs(uint2 v, uint64_t* x)
+{
+    float f[4];
+    unpack4<kBF16>(v, f);
+    x[0] = f32x2(f[0], f[1]);
+    x[1] = f32x2(f[2], f[3]);
+}
+
+template <bool kBF16>
+__device__ __forceinline__ uint2 pack_pairs(const uint64_t* x)
+{
+    float f[4];
+    f32x2_split(x[0], f[0], f[1]);
+    f32x2_split(x[1], f[2], f[3]);
+    return pack4<kBF16>(f);
+}
+
+__device__ __forceinline__ float sum_pairs(uint64_t a, uint64_t b)
+{
+    float e, f;
+    f32x2_split(add_f32x2(a, b), e, f);
+    return e + f;
+}
+
 // cos and sin of a lane's four pairs (1 and 0 for lanes behind `rot`).
 __device__ __forceinline__ void lane_angles(const float* table, int pos, int rot, int lane, float* cs, float* sn)
 {

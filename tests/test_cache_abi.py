@@ -98,7 +98,7 @@ def test_norm_rope_bwd(fake, kw, status):
 def test_norm_rope_bwd_workspace(fake):
     f = fake.sdpa_qk_norm_rope_bwd_workspace_bytes
     assert f(1, 1, 1, 1, 128) == 2 * 128 * 4 and f(1, 1, 1, 0, 64) == 64 * 4
-    assert f(8, 100000, 32, 8, 128) <= 608 * 128 * 4
+    assert f(8, 100000, 32, 8, 128) <= 760 * 128 * 4
     assert f(0, 1, 1, 1, 128) == f(1, 1, 1, 1, 96) == f(1, 1, 1, -1, 64) == 0
 
 
