@@ -506,6 +506,7 @@ sdpa_status_t sdpa_cache_append(const void* K, const void* V, const sdpa_cache_t
     p.S = S;
     p.Hkv = Hkv;
     p.page = page;
+    p.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
     p.n_pages = cache->n_pages;
     p.max_pages = max_pages;
     p.n_ord = n_ord;

@@ -43,7 +43,7 @@ struct AppendParams {
     const int* start;            // [B]
     const int* count;            // [B], or null: S
     const float* rope;           // [n_pos][rot / 2][2]
-    int B, S, Hkv, page, n_pages, max_pages;
+    int B, S, Hkv, page, page_shift, n_pages, max_pages;
     int n_pos, rot;
     int n_ord;                   // pages that S tokens can touch
 };
@@ -61,7 +61,7 @@ __device__ __forceinline__ float pow2_scale(float amax)
 
 // kWarps warps a unit (1 or 8), kPasses rows at most for each lane group.
 template <int D, bool kBF16, bool kInter, int kWarps, int kPasses>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p)
+__global__ void __launch_bounds__(kAppendThreads, kPasses <= 4 ? 4 : 2) append_kernel(const AppendParams p)
 {
     constexpr int kLanes = D / 8;
     constexpr int kUnitThreads = 32 * kWarps;
@@ -70,20 +70,19 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     grid_dependency_wait();
     grid_launch_dependents();
     const int tid = threadIdx.x % kUnitThreads;
-    const long long unit = (long long)blockIdx.x * (kAppendThreads / kUnitThreads) + threadIdx.x / kUnitThreads;
+    const uint32_t unit = blockIdx.x * (kAppendThreads / kUnitThreads) + threadIdx.x / kUnitThreads;
     const int lane = tid % kLanes;
     const int group = tid / kLanes;
-    // unit -> (KV head fastest, K or V, page of the sequence's new tokens, sequence)
-    long long rest = unit;
-    const int h = (int)(rest % p.Hkv);
-    rest /= p.Hkv;
+    // unit -> (KV head fastest, K or V, page of the sequence's new tokens,
+    // sequence); units fit into 31 bits, the host refuses more
+    uint32_t rest = unit / (uint32_t)p.Hkv;
+    const int h = (int)(unit - rest * p.Hkv);
     const int kv = (int)(rest & 1);
     rest >>= 1;
-    const int ord = (int)(rest % p.n_ord);
-    const long long bl = rest / p.n_ord;
-    if (bl >= p.B)
+    const int b = (int)(rest / (uint32_t)p.n_ord);
+    const int ord = (int)(rest - b * p.n_ord);
+    if (b >= p.B)
         return;                                        // whole units: their warps leave together
-    const int b = (int)bl;
     const long long start = p.start[b];
     const int count = p.count ? max(0, min(p.S, p.count[b])) : p.S;
     if (start < 0) {
@@ -91,7 +90,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
             atomicCAS(&g_sdpa_error, 0u, (unsigned)kErrTable);
         return;
     }
-    const long long ord_page = start / p.page + ord;   // ordinal of the page in its sequence
+    const long long ord_page = (start >> p.page_shift) + ord;      // ordinal of the page in its sequence
     const long long p0 = ord_page * p.page;            // position of its first slot
     const int lo = (int)(start > p0 ? start - p0 : 0);
     const long long end = start + count - p0;
@@ -111,6 +110,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     const uint16_t* x = reinterpret_cast<const uint16_t*>(p.x[kv]) + b * p.x_sb[kv] + h * p.x_sh[kv];
     float v[kPasses][8];
     uint2 ra[kPasses], rb[kPasses];
+    float cs[kPasses][4], sn[kPasses][4];
     uint32_t ok = 0;                                   // rows that are written
 #pragma unroll
     for (int n = 0; n < kPasses; ++n) {
@@ -121,6 +121,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
             ra[n] = *reinterpret_cast<const uint2*>(row + a);
             rb[n] = *reinterpret_cast<const uint2*>(row + c);
             ok |= 1u << n;
+            const long long pos = p0 + lo + r;
+            if (rot && pos >= p.n_pos) {
+                atomicCAS(&g_sdpa_error, 0u, (unsigned)rope::kErrPosition);
+                ok &= ~(1u << n);
+            } else if (rot) {
+                rope::lane_angles(p.rope, (int)pos, rot, lane, cs[n], sn[n]);
+            }
         }
     }
     if ((unsigned)id >= (unsigned)p.n_pages) {         // the whole unit
@@ -138,17 +145,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
             continue;
         rope::unpack4<kBF16>(ra[n], v[n]);
         rope::unpack4<kBF16>(rb[n], v[n] + 4);
-        if (rot) {
-            const long long pos = p0 + lo + n * kRows + group;
-            if (pos >= p.n_pos) {
-                atomicCAS(&g_sdpa_error, 0u, (unsigned)rope::kErrPosition);
-                ok &= ~(1u << n);
-                continue;
-            }
-            float cs[4], sn[4];
-            rope::lane_angles(p.rope, (int)pos, rot, lane, cs, sn);
-            rope::rotate<kInter>(v[n], cs, sn);
-        }
+        if (rot)
+            rope::rotate<kInter>(v[n], cs[n], sn[n]);
         // infinities (they saturate) and NaN stay out of the scale
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -190,21 +188,28 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     }
     if (tid == 0)
         *scale_at = scale;
+    auto write = [&](auto quotient) {
+#pragma unroll
+        for (int n = 0; n < kPasses; ++n) {
+            if (!(ok >> n & 1))
+                continue;
+            uint8_t* row = page + (long long)(lo + n * kRows + group) * pool.ss;
+            float q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                q[i] = quotient(v[n][i]);
+            *reinterpret_cast<uint32_t*>(row + a) =
+                (uint32_t)f32x2_to_e4m3x2(q[0], q[1]) | ((uint32_t)f32x2_to_e4m3x2(q[2], q[3]) << 16);
+            *reinterpret_cast<uint32_t*>(row + c) =
+                (uint32_t)f32x2_to_e4m3x2(q[4], q[5]) | ((uint32_t)f32x2_to_e4m3x2(q[6], q[7]) << 16);
+        }
+    };
+    // the product with the reciprocal is the quotient for a power of two
     const float inv = 1.f / scale;
-#pragma unroll
-    for (int n = 0; n < kPasses; ++n) {
-        if (!(ok >> n & 1))
-            continue;
-        uint8_t* row = page + (long long)(lo + n * kRows + group) * pool.ss;
-        float q[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            q[i] = exact ? v[n][i] * inv : v[n][i] / scale;
-        *reinterpret_cast<uint32_t*>(row + a) =
-            (uint32_t)f32x2_to_e4m3x2(q[0], q[1]) | ((uint32_t)f32x2_to_e4m3x2(q[2], q[3]) << 16);
-        *reinterpret_cast<uint32_t*>(row + c) =
-            (uint32_t)f32x2_to_e4m3x2(q[4], q[5]) | ((uint32_t)f32x2_to_e4m3x2(q[6], q[7]) << 16);
-    }
+    if (exact)
+        write([&](float x) { return x * inv; });
+    else
+        write([&](float x) { return x / scale; });
 }
 
 }  // namespace cache
