@@ -600,6 +600,7 @@ sdpa_status_t sdpa_fwd_paged(const void* Q, const sdpa_cache_t* cache, const int
     p.ctas = per_sm * sm_count < paged_ctas(nr) ? per_sm * sm_count : paged_ctas(nr);
     p.ctas = most < p.ctas ? static_cast<int>(most) : p.ctas;
     p.part_o = static_cast<float*>(workspace);
+    p.ctas_inverse = ~0ull / p.ctas + 1;
     p.part_lse = p.part_o + static_cast<long long>(p.ctas) * 2 * nr * D;
     p.joins = reinterpret_cast<int4*>(p.part_lse + static_cast<long long>(p.ctas) * 2 * nr);
     // L2 fetches no more than a slot's bytes where the slots of a head lie

@@ -51,9 +51,10 @@ struct Params {
     int page_shift;                  // log2(page)
     int row_tiles;                   // tiles of NR rows that Sq * group rows need
     int ctas;                        // CTAs that share the key tiles
+    unsigned long long ctas_inverse; // 2^64 / ctas, rounded up
     float* part_o;                   // [ctas][2][NR][D]: normalised results of pieces
     float* part_lse;                 // [ctas][2][NR]: their LSE in log2 units
-    int4* joins;                     // [ctas]: x (low, high half), KV head and pieces of an item to join, see Join
+    int4* joins;                     // [ctas]: entry, KV head, -, pieces of an item to join (join_of)
 };
 
 enum : unsigned int { kErrPagedLoad = 0x801, kErrPagedMma = 0x811, kErrPagedSoftmax = 0x821 };
@@ -118,7 +119,7 @@ struct PagedBarriers {
 };
 
 // Number of key tiles of entry x = (sequence, row tile): 0 without rows, else
-// at least 1.
+// at least 1.  (In 32 bits the kernel of many rows comes out 12% slower.)
 template <int NR>
 __device__ __forceinline__ int entry_tiles(const Params& p, long long x)
 {
@@ -135,14 +136,15 @@ __device__ __forceinline__ int entry_tiles(const Params& p, long long x)
     return len < 1 ? 1 : (int)((len + kTileKeys - 1) / kTileKeys);
 }
 
-// First tile of CTA c's share of `total` tiles.  With fewer tiles than CTAs
-// the first `total` CTAs have one each, so no share between two others is
-// empty.
-__device__ __forceinline__ long long share_begin(long long total, int c, int ctas)
+// First tile of CTA c's share of `total` tiles, c * total / ctas: the product
+// with ctas' reciprocal is exact for totals below 2^64 / ctas^2.  With fewer
+// tiles than CTAs the first `total` CTAs have one each, so no share between
+// two others is empty.
+__device__ __forceinline__ long long share_begin(const Params& p, long long total, int c)
 {
-    if (total < ctas)
-        return c < total ? c : total;
-    return total / ctas * c + total % ctas * c / ctas;
+    if (c >= p.ctas || total < p.ctas)
+        return c < total && c < p.ctas ? c : total;
+    return (long long)__umul64hi((unsigned long long)total, p.ctas_inverse * (unsigned)c);
 }
 
 // Whole-block: counts the tiles of all entries (times Hkv each) and finds the
@@ -175,7 +177,7 @@ __device__ __forceinline__ void find_share(const Params& p, int c, Bars* bars)
         total += s;
     }
     long long first = before + incl - sum;
-    const long long target = share_begin(total, c, p.ctas);
+    const long long target = share_begin(p, total, c);
     if (threadIdx.x == 0)
         bars->total = total;
     if (target >= first && target < first + sum) {
@@ -205,14 +207,14 @@ template <int NR, typename Bars>
 __device__ __forceinline__ bool first_piece(const Params& p, const Bars* bars, Piece& w)
 {
     const int c = blockIdx.x;
-    const long long t0 = share_begin(bars->total, c, p.ctas);
-    w.left = share_begin(bars->total, c + 1, p.ctas) - t0;
+    const long long t0 = share_begin(p, bars->total, c);
+    w.left = share_begin(p, bars->total, c + 1) - t0;
     if (w.left <= 0)
         return false;
     w.x = bars->x;
     w.n = entry_tiles<NR>(p, w.x);
     const long long off = t0 - bars->x_first;
-    w.h = (int)(off / w.n);
+    w.h = off >> 32 ? (int)(off / w.n) : (int)((uint32_t)off / (uint32_t)w.n);
     w.begin = (int)(off - (long long)w.h * w.n);
     w.end = (int)(w.n - w.begin < w.left ? w.n : w.begin + w.left);
     return true;
@@ -253,7 +255,7 @@ __device__ __forceinline__ Item item_of(const Params& p, const Piece& w)
     t.count = p.count ? max(0, min(p.Sq, p.count[t.b])) : p.Sq;
     t.rows = min(NR, t.count * p.group - t.r0);
     t.start = p.start[t.b];
-    const long long cap = (long long)p.max_pages * p.page;
+    const long long cap = (long long)p.max_pages << p.page_shift;
     long long len = t.start + (p.causal ? (t.r0 + t.rows - 1) / p.group + 1 : t.count);
     len = len < 0 ? 0 : len;
     t.keys = (int)(len < cap ? len : cap);
@@ -288,18 +290,18 @@ __device__ __forceinline__ float warp_sums(float (&s)[N], int lane)
 __device__ __forceinline__ int4 join_of(const Params& p, long long total, const Piece& w)
 {
     const int c = blockIdx.x;
-    const long long first = share_begin(total, c, p.ctas) - w.begin;          // the item's first tile
-    if (w.begin == 0 || first < share_begin(total, c - 1, p.ctas))
+    const long long first = share_begin(p, total, c) - w.begin;          // the item's first tile
+    if (w.begin == 0 || first < share_begin(p, total, c - 1))
         return make_int4(0, 0, 0, 0);
     int last = c, hi = p.ctas - 1;                     // the CTA that has the item's last tile: bisection
     while (last < hi) {
         const int mid = (last + hi + 1) >> 1;
-        if (share_begin(total, mid, p.ctas) <= first + w.n - 1)
+        if (share_begin(p, total, mid) <= first + w.n - 1)
             last = mid;
         else
             hi = mid - 1;
     }
-    return make_int4((int)(unsigned)w.x, (int)(w.x >> 32), w.h, last - c + 2);
+    return make_int4((int)w.x, w.h, 0, last - c + 2);
 }
 
 template <int D, bool kBF16, int NR>
@@ -899,7 +901,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 //     O = sum_k exp2(lse_k - LSE) O_k,   LSE = log2 sum_k exp2(lse_k).
 // Few rows have a block each, whose threads share the pieces out (there may be
 // hundreds); many rows go eight to a block, a warp each where the pieces are
-// few (measured on 1024 rows of 3 pieces: 25 us by blocks, %JOIN% by warps).
+// few (measured on 1024 rows of 3 pieces: 25 us by blocks, 13.5 by warps).
 constexpr int kJoinThreads = 256;
 
 template <int D, bool kBF16, int NR>
@@ -916,8 +918,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const Params p
     if (n == 0)
         return;
     Piece w;
-    w.x = (long long)(((unsigned long long)(unsigned)join.y << 32) | (unsigned)join.x);
-    w.h = join.z;
+    w.x = (uint32_t)join.x;
+    w.h = join.y;
     const Item it = item_of<NR>(p, w);
     auto slot_of = [&](int k) -> long long { return k == 0 ? (long long)(c - 1) * 2 + 1 : (long long)(c - 1 + k) * 2; };
     auto store = [&](int r, int d, float o) {
