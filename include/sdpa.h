@@ -316,7 +316,7 @@ typedef struct {
  *   *_layout  strides, NULL for contiguous, as for sdpa_fwd_ex.
  *   norm      0: rotation only (weights and eps are not read).
  *   q_weight, k_weight   device, [D], type weight_dtype (SDPA_DTYPE_F32 or
- *             dtype), or NULL for ones.
+ *             dtype), 4-byte aligned, or NULL for ones.
  *   rope      host pointer, see sdpa_rope_t.
  *   positions device, int32 [B][S] contiguous, or NULL: token s stands at
  *             position s.  A row whose position is outside the table is not
@@ -398,7 +398,7 @@ typedef struct {
  * that begins inside a page keeps at least the page's scale, and rounds the
  * page's earlier tokens to a scale that grows.  Larger values and infinities
  * saturate at 448 s, NaN stays NaN.  Pages that a call writes belong to one
- * sequence each.  Slots behind the last token are not written.
+ * sequence each and stand in its row of the table once.  Slots behind the last token are not written.
  * A page index outside the pool, a position outside the block table and a
  * position outside the rotation table are not followed: what would go there
  * is not written and the device error word becomes 0x601, 0x602 or 0x701.

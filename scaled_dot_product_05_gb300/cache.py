@@ -55,6 +55,19 @@ def _call(device: int, fn, *args) -> None:
         _run(device, fn, *args)
 
 
+def _alloc(stream, dev, make, /, *args, **kwargs):
+    """make(...) in the memory pool of the stream that the call runs on: what
+    the call leaves behind (a workspace) or takes over from earlier work is
+    then ordered by that stream."""
+    if stream is None:
+        return make(*args, **kwargs)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle, dev) if handle else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):
+        return make(*args, **kwargs)
+
+
 @functools.lru_cache(maxsize=1024)
 def _layout_ref(strides):
     """sdpa_layout_t of a 4-D tensor's strides, by value."""
@@ -138,12 +151,12 @@ def sdpa_qk_norm_rope(q, k=None, q_out=None, k_out=None, *, norm: bool = True, q
     dev, B, S, Hq, Hkv, D, lq, lk = _pair_shapes(q, k)
     lqo = lko = kp = kop = None
     if q_out is None:
-        q_out = torch.empty_like(q, memory_format=_DENSE)
+        q_out = _alloc(stream, dev, torch.empty_like, q, memory_format=_DENSE)
     else:
         lqo = _like(q_out, q, dev, "q_out")
     if k is not None:
         if k_out is None:
-            k_out = torch.empty_like(k, memory_format=_DENSE)
+            k_out = _alloc(stream, dev, torch.empty_like, k, memory_format=_DENSE)
         else:
             lko = _like(k_out, k, dev, "k_out")
         kp, kop = k.data_ptr(), k_out.data_ptr()
@@ -190,26 +203,27 @@ def sdpa_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq=None, dk=None, *, norm: bool 
     ldq = ldk = lgk = kp = gkp = dkp = dwq = dwk = ws = None
     ws_bytes = 0
     if dq is None:
-        dq = torch.empty_like(q, memory_format=_DENSE)
+        dq = _alloc(stream, dev, torch.empty_like, q, memory_format=_DENSE)
     else:
         ldq = _like(dq, q, dev, "dq")
     if k is not None:
         lgk = _like(dk_out, k, dev, "dk_out")
         if dk is None:
-            dk = torch.empty_like(k, memory_format=_DENSE)
+            dk = _alloc(stream, dev, torch.empty_like, k, memory_format=_DENSE)
         else:
             ldk = _like(dk, k, dev, "dk")
         kp, gkp, dkp = k.data_ptr(), dk_out.data_ptr(), dk.data_ptr()
     if norm:
         if dq_weight is None:
-            dq_weight = torch.empty(D, dtype=torch.float32, device=dev)
+            dq_weight = _alloc(stream, dev, torch.empty, D, dtype=torch.float32, device=dev)
         dwq = _weight_grad(dq_weight, D, dev)
         if k is not None:
             if dk_weight is None:
-                dk_weight = torch.empty(D, dtype=torch.float32, device=dev)
+                dk_weight = _alloc(stream, dev, torch.empty, D, dtype=torch.float32, device=dev)
             dwk = _weight_grad(dk_weight, D, dev)
         if workspace is None:
-            workspace = q.new_empty((qk_norm_rope_bwd_workspace_bytes(B, S, Hq, Hkv, D),), dtype=torch.uint8)
+            workspace = _alloc(stream, dev, q.new_empty, (qk_norm_rope_bwd_workspace_bytes(B, S, Hq, Hkv, D),),
+                               dtype=torch.uint8)
         ws, ws_bytes = _workspace(workspace, dev)
     else:
         dq_weight = dk_weight = None
@@ -302,7 +316,8 @@ def sdpa_fwd_paged(q, cache: PagedCache, block_table, start, count=None, o=None,
     :func:`sdpa_cache_append`, and sees positions 0 .. start[b] + i (causal) or
     all 0 .. start[b] + count[b] - 1.  Rows behind count[b] of ``o`` and
     ``lse`` ([B, Hq, Sq] float32) are left as they are.  ``o`` (like q) and
-    the workspace are allocated when not given.  Returns ``o``."""
+    the workspace are allocated when not given, from ``stream``'s memory.
+    Returns ``o``."""
     dev = cache._device
     shape = q.shape
     if len(shape) != 4 or shape[3] != cache.head_dim:
@@ -313,13 +328,13 @@ def sdpa_fwd_paged(q, cache: PagedCache, block_table, start, count=None, o=None,
     Hkv = cache.n_heads
     lo = None
     if o is None:
-        o = torch.empty_like(q, memory_format=_DENSE)
+        o = _alloc(stream, dev, torch.empty_like, q, memory_format=_DENSE)
     else:
         lo = _like(o, q, dev, "o")
     if lse is not None and lse.get_device() != dev:
         raise ValueError("lse must be on the cache's device")
     if workspace is None:
-        workspace = q.new_empty((paged_workspace_bytes(B, Hq, Hkv, Sq, D),), dtype=torch.uint8)
+        workspace = _alloc(stream, dev, q.new_empty, (paged_workspace_bytes(B, Hq, Hkv, Sq, D),), dtype=torch.uint8)
     ws, ws_bytes = _workspace(workspace, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(D)

@@ -531,6 +531,50 @@ def test_streams_graphs_and_chained_calls(gpu):
 
 
 @pytest.mark.gpu
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("raw", [False, True])
+def test_memory_of_a_call_on_another_stream(gpu, raw, monkeypatch):
+    """What a call allocates comes from its stream's memory: the workspace that it drops must not go to an allocation
+    of the current stream, whose kernels would not wait for the call's."""
+    import scaled_dot_product_05_gb300 as lib
+    from scaled_dot_product_05_gb300 import cache as module
+    n_pages, page, B, Hkv, Hq, D = 12, 16, 1, 2, 8, 64
+    c = lib.PagedCache.empty(n_pages, page, Hkv, D, device=DEV)
+    g = torch.Generator(DEV).manual_seed(5)
+    q = torch.randn((B, 1, Hq, D), generator=g, device=DEV).to(torch.bfloat16)
+    k = torch.randn((B, 150, Hkv, D), generator=g, device=DEV).to(torch.bfloat16)
+    table = torch.arange(n_pages, dtype=torch.int32, device=DEV)[None]
+    zero = torch.zeros(B, dtype=torch.int32, device=DEV)
+    lib.sdpa_cache_append(k, k, c, table, zero)
+    start = zero + 149
+    want = lib.sdpa_fwd_paged(q, c, table, start)
+    w = torch.ones(D, device=DEV)
+    grads = lib.sdpa_qk_norm_rope_bwd(k, None, k, None, q_weight=w)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    spans = []
+    orig = module._workspace
+
+    def spy(t, device):
+        spans.append((t.data_ptr(), t.data_ptr() + t.numel()))
+        return orig(t, device)
+    monkeypatch.setattr(module, "_workspace", spy)
+    stream = side.cuda_stream if raw else side
+    got = lib.sdpa_fwd_paged(q, c, table, start, stream=stream)
+    gots = lib.sdpa_qk_norm_rope_bwd(k, None, k, None, q_weight=w, stream=stream)
+    assert len(spans) == 2
+    kept = [torch.empty(b - a, dtype=torch.uint8, device=DEV) for a, b in spans for _ in range(4)]
+    for t in kept:
+        for a, b in spans:
+            assert t.data_ptr() >= b or t.data_ptr() + t.numel() <= a
+    side.synchronize()
+    assert torch.equal(got, want)
+    for x, y in zip(gots, grads):
+        assert (x is None and y is None) or torch.equal(x, y)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
 def test_serving_loop(gpu, dt):
     """Prompts of unlike lengths, then single tokens: norm and rotation of q and k, append, attention, against the
