@@ -54,7 +54,7 @@ struct Params {
     unsigned long long ctas_inverse; // 2^64 / ctas, rounded up
     float* part_o;                   // [ctas][2][NR][D]: normalised results of pieces
     float* part_lse;                 // [ctas][2][NR]: their LSE in log2 units
-    int4* joins;                     // [ctas]: entry, KV head, -, pieces of an item to join (join_of)
+    int4* joins;                     // [ctas]: entry, KV head, rows, pieces of an item to join (join_of)
 };
 
 enum : unsigned int { kErrPagedLoad = 0x801, kErrPagedMma = 0x811, kErrPagedSoftmax = 0x821 };
@@ -123,6 +123,12 @@ struct PagedBarriers {
 template <int NR>
 __device__ __forceinline__ int entry_tiles(const Params& p, long long x)
 {
+    if constexpr (NR <= 16) {                          // one row tile holds a sequence's rows
+        const int b = (int)x;
+        const int count = p.count ? max(0, min(p.Sq, p.count[b])) : p.Sq;
+        const long long len = min((long long)p.start[b] + count, (long long)p.max_pages << p.page_shift);
+        return count == 0 ? 0 : len < 1 ? 1 : (int)((len + kTileKeys - 1) / kTileKeys);
+    }
     const int b = (int)(x / p.row_tiles);
     const long long r0 = (x - (long long)b * p.row_tiles) * NR;
     const int count = p.count ? max(0, min(p.Sq, p.count[b])) : p.Sq;
@@ -250,13 +256,13 @@ template <int NR>
 __device__ __forceinline__ Item item_of(const Params& p, const Piece& w)
 {
     Item t;
-    t.b = (int)(w.x / p.row_tiles);
-    t.r0 = (int)(w.x - (long long)t.b * p.row_tiles) * NR;
+    t.b = NR <= 16 ? (int)w.x : (int)(w.x / p.row_tiles);
+    t.r0 = NR <= 16 ? 0 : (int)(w.x - (long long)t.b * p.row_tiles) * NR;
     t.count = p.count ? max(0, min(p.Sq, p.count[t.b])) : p.Sq;
     t.rows = min(NR, t.count * p.group - t.r0);
     t.start = p.start[t.b];
     const long long cap = (long long)p.max_pages << p.page_shift;
-    long long len = t.start + (p.causal ? (t.r0 + t.rows - 1) / p.group + 1 : t.count);
+    long long len = t.start + (NR > 16 && p.causal ? (t.r0 + t.rows - 1) / p.group + 1 : t.count);
     len = len < 0 ? 0 : len;
     t.keys = (int)(len < cap ? len : cap);
     return t;
@@ -287,6 +293,7 @@ __device__ __forceinline__ float warp_sums(float (&s)[N], int lane)
 
 // An item whose pieces several CTAs have is joined by the block of the second
 // of them, c: joins[c].w is the number of pieces (0: nothing to join there).
+template <int NR>
 __device__ __forceinline__ int4 join_of(const Params& p, long long total, const Piece& w)
 {
     const int c = blockIdx.x;
@@ -301,7 +308,7 @@ __device__ __forceinline__ int4 join_of(const Params& p, long long total, const 
         else
             hi = mid - 1;
     }
-    return make_int4((int)w.x, w.h, 0, last - c + 2);
+    return make_int4((int)w.x, w.h, item_of<NR>(p, w).rows, last - c + 2);
 }
 
 template <int D, bool kBF16, int NR>
@@ -366,8 +373,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         // =========================== TMA producer ===========================
         // lane i brings page i of a tile; pages that no row sees, or whose
         // index is outside the pool, are not loaded (their keys are masked)
-        if (lane == 0 && blockIdx.x > 0)
-            p.joins[blockIdx.x] = more ? join_of(p, bars->total, w) : make_int4(0, 0, 0, 0);
         const int ppt = kTileKeys >> p.page_shift;
         uint32_t n = 0;                                    // tiles issued (ring position)
         bool ok = true;
@@ -410,6 +415,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (id >= 0)
                     tma_load_4d(sV + vs * L::kTileBytes + lane * p.page * D, &tm_v, smem_u32(&bars->v_full[vs]), 0, w.h, 0, id);
             }
+        }
+        if (lane == 0 && blockIdx.x > 0) {                 // (after the loads, which nothing should keep waiting)
+            Piece first;
+            p.joins[blockIdx.x] = first_piece<NR>(p, bars, first) ? join_of<NR>(p, bars->total, first) : make_int4(0, 0, 0, 0);
         }
         // never leave with copies in flight (after an abort the last K tile
         // may or may not have been issued: at worst its wait runs out)
@@ -909,7 +918,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const Params p
 {
     constexpr int kSlices = kJoinThreads / D;
     constexpr int kRows = NR <= 16 ? 1 : 8;
-    __shared__ float sh_o[kJoinThreads], sh_w[kJoinThreads];
+    __shared__ float sh_o[kJoinThreads], sh_w[kJoinThreads], sh_m[kJoinThreads];
     grid_dependency_wait();
     grid_launch_dependents();
     const int c = blockIdx.x + 1;
@@ -917,20 +926,19 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const Params p
     const int n = join.w;
     if (n == 0)
         return;
-    Piece w;
-    w.x = (uint32_t)join.x;
-    w.h = join.y;
-    const Item it = item_of<NR>(p, w);
+    struct { int b, r0, rows; } it = {NR <= 16 ? join.x : join.x / p.row_tiles, 0, join.z};
+    it.r0 = NR <= 16 ? 0 : (join.x - it.b * p.row_tiles) * NR;
+    const int kv_head = join.y;
     auto slot_of = [&](int k) -> long long { return k == 0 ? (long long)(c - 1) * 2 + 1 : (long long)(c - 1 + k) * 2; };
     auto store = [&](int r, int d, float o) {
         const int i = (it.r0 + r) / p.group;
-        const long long head = (long long)w.h * p.group + (it.r0 + r) % p.group;
+        const long long head = (long long)kv_head * p.group + (it.r0 + r) % p.group;
         reinterpret_cast<uint16_t*>(p.O)[(long long)it.b * p.o_sb + (long long)i * p.o_ss + head * p.o_sh + d] =
             (uint16_t)(pack2<kBF16>(o, 0.f) & 0xffffu);
     };
     auto store_lse = [&](int r, float m, float den) {
         const int i = (it.r0 + r) / p.group;
-        const long long head = (long long)w.h * p.group + (it.r0 + r) % p.group;
+        const long long head = (long long)kv_head * p.group + (it.r0 + r) % p.group;
         if (p.lse)
             p.lse[((long long)it.b * p.Hq + head) * p.Sq + i] = den == 0.f ? -INFINITY : (m + log2f(den)) * kLn2;
     };
@@ -967,42 +975,55 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const Params p
             store_lse(r, m, den);
         return;
     }
+    // one pass, eight pieces of a slice at a time, each batch under the largest LSE so far
     for (int r = blockIdx.y * kRows; r < min(it.rows, (int)(blockIdx.y + 1) * kRows); ++r) {
-        float m = -INFINITY;
-        for (int k = threadIdx.x; k < n; k += kJoinThreads)
-            m = fmaxf(m, p.part_lse[slot_of(k) * NR + r]);
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1)
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-        if ((threadIdx.x & 31) == 0)
-            sh_w[threadIdx.x >> 5] = m;
-        __syncthreads();
-#pragma unroll
-        for (int s = 0; s < kJoinThreads / 32; ++s)
-            m = fmaxf(m, sh_w[s]);
-        __syncthreads();
         const int d = threadIdx.x % D, slice = threadIdx.x / D;
-        float o = 0.f, den = 0.f;
-#pragma unroll 8
-        for (int k = slice; k < n; k += kSlices) {
-            const long long slot = slot_of(k) * NR + r;
-            const float z = p.part_lse[slot];
-            const float f = z == -INFINITY ? 0.f : exp2f(z - m);   // a NaN stays one
-            den += f;
-            o = fmaf(f, p.part_o[slot * D + d], o);
+        float m = -INFINITY, o = 0.f, den = 0.f;
+        auto scaled = [](float z, float top) { return z == -INFINITY ? 0.f : exp2f(z - top); };   // a NaN stays one
+        for (int k0 = slice; k0 < n; k0 += 8 * kSlices) {
+            float z[8], v[8], top = m;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int k = k0 + i * kSlices;
+                const long long slot = slot_of(k) * NR + r;
+                z[i] = k < n ? p.part_lse[slot] : -INFINITY;
+                v[i] = k < n ? p.part_o[slot * D + d] : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                top = fmaxf(top, z[i]);
+            const float c = scaled(m, top);
+            o *= c;
+            den *= c;
+            m = top;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float f = scaled(z[i], m);
+                den += f;
+                o = fmaf(f, v[i], o);
+            }
         }
         sh_o[threadIdx.x] = o;
         sh_w[threadIdx.x] = den;
+        sh_m[threadIdx.x] = m;
         __syncthreads();
         if (slice == 0) {
+            float top = m;
+#pragma unroll
+            for (int s = 1; s < kSlices; ++s)
+                top = fmaxf(top, sh_m[s * D + d]);
+            const float c = scaled(m, top);
+            o *= c;
+            den *= c;
 #pragma unroll
             for (int s = 1; s < kSlices; ++s) {
-                o += sh_o[s * D + d];
-                den += sh_w[s * D + d];
+                const float f = scaled(sh_m[s * D + d], top);
+                o = fmaf(f, sh_o[s * D + d], o);
+                den = fmaf(f, sh_w[s * D + d], den);
             }
             store(r, d, den == 0.f ? 0.f : o / den);
             if (d == 0)
-                store_lse(r, m, den);
+                store_lse(r, top, den);
         }
         __syncthreads();
     }

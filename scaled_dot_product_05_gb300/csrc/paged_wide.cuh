@@ -141,7 +141,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             // as in paged_attn_kernel: lane i brings page i of a tile; and lane
             // i < 8 lays out the scales of the tile's keys 16 i .. 16 i + 15
             if (lane == 0 && blockIdx.x > 0)
-                p.joins[blockIdx.x] = more ? join_of(p, bars->total, w) : make_int4(0, 0, 0, 0);
+                p.joins[blockIdx.x] = more ? join_of<NR>(p, bars->total, w) : make_int4(0, 0, 0, 0);
             const int ppt = kTileKeys >> p.page_shift;
             uint32_t n = 0;
             bool ok = true;

@@ -531,9 +531,6 @@ def test_streams_graphs_and_chained_calls(gpu):
 
 
 @pytest.mark.gpu
-
-
-@pytest.mark.gpu
 @pytest.mark.parametrize("raw", [False, True])
 def test_memory_of_a_call_on_another_stream(gpu, raw, monkeypatch):
     """What a call allocates comes from its stream's memory: the workspace that it drops must not go to an allocation
@@ -575,6 +572,7 @@ def test_memory_of_a_call_on_another_stream(gpu, raw, monkeypatch):
         assert (x is None and y is None) or torch.equal(x, y)
 
 
+@pytest.mark.gpu
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
 def test_serving_loop(gpu, dt):
     """Prompts of unlike lengths, then single tokens: norm and rotation of q and k, append, attention, against the
