@@ -398,7 +398,9 @@ typedef struct {
  * that begins inside a page keeps at least the page's scale, and rounds the
  * page's earlier tokens to a scale that grows.  Larger values and infinities
  * saturate at 448 s, NaN stays NaN.  Pages that a call writes belong to one
- * sequence each and stand in its row of the table once.  Slots behind the last token are not written.
+ * sequence each and stand in its row of the table once.  Codes are the nearest
+ * ones (ties to even) to the exact rotated values, but where the two terms of a
+ * rotated value cancel to less than a sixteenth: there fp32's roundings count.  Slots behind the last token are not written.
  * A page index outside the pool, a position outside the block table and a
  * position outside the rotation table are not followed: what would go there
  * is not written and the device error word becomes 0x601, 0x602 or 0x701.

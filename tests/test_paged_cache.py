@@ -190,6 +190,41 @@ def test_append(gpu, case):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotated_keys_get_the_codes_of_the_exact_product(gpu, inter):
+    """A rotation in fp32 is off by an ulp or so, which would send some of a few million keys to the code on the other
+    side of a border: codes have to be those of the exact product, wherever it is not the rest of terms more than
+    eight times as large, and not subnormal."""
+    import scaled_dot_product_05_gb300 as lib
+    page, H, D, S = 128, 16, 128, 4000
+    cache = make_cache(S // page + 1, page, H, D, "heads", filled=False)
+    k = torch.randn((1, S, H, D), generator=torch.Generator().manual_seed(11)).bfloat16()
+    rope = lib.rope_table(S, D, device=DEV)
+    table = torch.arange(S // page + 1, dtype=torch.int32, device=DEV)[None]
+    lib.sdpa_cache_append(k.to(DEV), k.to(DEV), cache, table, i32([0]), rope=rope, interleaved=inter)
+    x = rotate64(k[0].double(), rope.cpu().double(), torch.arange(S), inter)
+    # the sum of the magnitudes of the two terms
+    terms = rotate64(k[0].double().abs(), torch.stack((rope[..., 0].abs(), -rope[..., 1].abs()), -1).cpu().double(),
+                     torch.arange(S), inter)
+    if inter:
+        other = rotate64(k[0].double().abs(), rope.abs().cpu().double(), torch.arange(S), inter)
+        terms[..., 1::2] = other[..., 1::2]
+    else:
+        other = rotate64(k[0].double().abs(), rope.abs().cpu().double(), torch.arange(S), inter)
+        terms[..., D // 2:] = other[..., D // 2:]
+    got = PlainCache(cache)
+    pages = table[0].cpu().long()
+    codes = got.codes[0][pages].reshape(-1, H, D)[:S]
+    scale = got.scale[0][pages].repeat_interleave(page, 0)[:S, :, None]
+    y = x / scale
+    step = torch.exp2(torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6))) - 3)      # (to 32 bits first would round twice)
+    want = torch.round(y / step) * step
+    sure = (x.abs() * 8 >= terms) & (y.abs() >= 2.0 ** -6)
+    assert sure.double().mean() > 0.7
+    assert torch.equal(codes[sure], want[sure])
+
+
+@pytest.mark.gpu
 def test_append_special_values(gpu):
     import scaled_dot_product_05_gb300 as lib
     cache = make_cache(4, 16, 1, 64, "heads", filled=False)
