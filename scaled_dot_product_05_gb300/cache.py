@@ -59,13 +59,19 @@ def _alloc(stream, dev, make, /, *args, **kwargs):
     """make(...) in the memory pool of the stream that the call runs on: what
     the call leaves behind (a workspace) or takes over from earlier work is
     then ordered by that stream."""
-    if stream is None:
+    if stream is None:                                 # the current one
         return make(*args, **kwargs)
     if not isinstance(stream, torch.cuda.Stream):
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
         stream = torch.cuda.ExternalStream(handle, dev) if handle else torch.cuda.default_stream(dev)
     with torch.cuda.stream(stream):
         return make(*args, **kwargs)
+
+
+def _empty_like(t, stream, dev):
+    if stream is None:
+        return torch.empty_like(t, memory_format=_DENSE)
+    return _alloc(stream, dev, torch.empty_like, t, memory_format=_DENSE)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -151,12 +157,12 @@ def sdpa_qk_norm_rope(q, k=None, q_out=None, k_out=None, *, norm: bool = True, q
     dev, B, S, Hq, Hkv, D, lq, lk = _pair_shapes(q, k)
     lqo = lko = kp = kop = None
     if q_out is None:
-        q_out = _alloc(stream, dev, torch.empty_like, q, memory_format=_DENSE)
+        q_out = _empty_like(q, stream, dev)
     else:
         lqo = _like(q_out, q, dev, "q_out")
     if k is not None:
         if k_out is None:
-            k_out = _alloc(stream, dev, torch.empty_like, k, memory_format=_DENSE)
+            k_out = _empty_like(k, stream, dev)
         else:
             lko = _like(k_out, k, dev, "k_out")
         kp, kop = k.data_ptr(), k_out.data_ptr()
@@ -203,13 +209,13 @@ def sdpa_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq=None, dk=None, *, norm: bool 
     ldq = ldk = lgk = kp = gkp = dkp = dwq = dwk = ws = None
     ws_bytes = 0
     if dq is None:
-        dq = _alloc(stream, dev, torch.empty_like, q, memory_format=_DENSE)
+        dq = _empty_like(q, stream, dev)
     else:
         ldq = _like(dq, q, dev, "dq")
     if k is not None:
         lgk = _like(dk_out, k, dev, "dk_out")
         if dk is None:
-            dk = _alloc(stream, dev, torch.empty_like, k, memory_format=_DENSE)
+            dk = _empty_like(k, stream, dev)
         else:
             ldk = _like(dk, k, dev, "dk")
         kp, gkp, dkp = k.data_ptr(), dk_out.data_ptr(), dk.data_ptr()
@@ -328,7 +334,7 @@ def sdpa_fwd_paged(q, cache: PagedCache, block_table, start, count=None, o=None,
     Hkv = cache.n_heads
     lo = None
     if o is None:
-        o = _alloc(stream, dev, torch.empty_like, q, memory_format=_DENSE)
+        o = _empty_like(q, stream, dev)
     else:
         lo = _like(o, q, dev, "o")
     if lse is not None and lse.get_device() != dev:

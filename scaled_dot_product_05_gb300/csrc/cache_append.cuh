@@ -15,8 +15,9 @@
 // a unit for prompts, one warp a unit (eight units a block) for the few tokens
 // of a decoding step.  The rows wait in registers between the maximum and the
 // rounding, so each is read once.  Measured (4 prompts of up to 2000 tokens, 8
-// KV heads of 128, rotated): 13.6 us for 37 MB, two thirds of the issue slots
-// taken, 25% more than HBM's time and the launch; 128 single tokens: 2.8 us,
+// KV heads of 128, rotated): 13.6 us for 37 MB, bound by its latencies (table,
+// page, rows, scale one after the other in one and a half waves of blocks) and
+// by issue slots, of which two thirds are taken; 128 single tokens: 2.8 us,
 // latency.
 //
 // A rotated key is off by an ulp or two of fp32, enough to send one key in a

