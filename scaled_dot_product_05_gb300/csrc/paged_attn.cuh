@@ -12,12 +12,20 @@
 // word; no address is formed from such an index.
 //
 // The codes go to the FP8 tensor cores as they lie in the cache, and the
-// 16-bit operands are split instead: q, scaled by a power of two, and the
-// weights w_j = exp(s_j - m) v_scale_j, into E4M3 parts that add up to them:
-// two hold the 8 bits of bf16, three the 11 of fp16.  A weight's second part is
-// held 16 times as large as it counts, its third 256 times, each in columns of
-// its own, so that small weights keep their bits.  Products of E4M3 values
-// are exact in the fp32 accumulator.  Nothing is dequantised, and K and V are
+// 16-bit operands are split instead into 8-bit parts that add up to them; the
+// products of 8-bit values are exact in the fp32 accumulator.  q, scaled by a
+// power of two, becomes E4M3 parts: two hold the 8 bits of bf16, three the 11
+// of fp16.  A weight w_j = exp(s_j - m) v_scale_j is rounded to f16, the only
+// rounding that it sees (attention over fp16 keys and values rounds its
+// weights so), and cut into four E5M2 parts: each is the upper byte of what
+// the parts before it have left (3 bits of it), held 8 times as large as the
+// one before, in columns of its own.  The parts are the f16 number exactly,
+// subnormal ones included.  A row's largest weight is held as 2^11 to 2^15:
+// weights down to e^-17 of it have 11 bits, and the smallest step is 2^-35 of
+// it (the many small weights of a long cache are the whole output where a token
+// with most of the weight has a value near zero).  Cutting costs no more than
+// rounding into two E4M3 parts did, which lost what was below e^-14 (8
+// sequences of 32768 keys 91.3 us against 91.0).  Nothing is dequantised, and K and V are
 // read once as bytes.
 //
 // The rows (token, query head) of one KV head are the N side of the products,
@@ -69,28 +77,31 @@ struct Params {
 enum : unsigned int { kErrPagedLoad = 0x801, kErrPagedMma = 0x811, kErrPagedSoftmax = 0x821 };
 
 constexpr int kTileKeys = 128;
-// The running maximum is let behind by up to 2^2 before everything is rescaled
-// to a new one, so weights reach 4; times 112 they reach 448, the largest
-// E4M3 value.
-constexpr float kLag = 2.0f;
-constexpr float kLog2W = 6.807354922057604f;   // log2(112)
+// The running maximum is let behind by up to 2^4 before everything is rescaled
+// to a new one, and weight 1 is held as 2^11: no weight passes 2^15, which the
+// parts need (with 2^2 and 2^13: 64 sequences, 16 rows of 64, 73.6 us against 71.8).
+constexpr float kLag = 4.0f;
+constexpr float kLog2W = 11.0f;
 
-// Shared memory and TMEM of one CTA: NR rows, in kParts E4M3 parts.
+// Shared memory and TMEM of one CTA: NR rows, q in kParts E4M3 parts, weights
+// in kWParts E5M2 parts.
 template <int D, bool kBF16, int NR>
 struct PagedLayout {
     static_assert(D == 64 || D == 128, "head dimension");
     static_assert(NR == 8 || NR == 16, "rows of a tile");
     static constexpr int kParts = kBF16 ? 2 : 3;
+    static constexpr int kWParts = 4;
     static constexpr int kGroups = 2;                           // softmax warpgroups
     static constexpr int kSoftmax = 128 * kGroups;              // warps 0 ..
     static constexpr int kThreads = kSoftmax + 64;              // then TMA producer, MMA issuer
     static constexpr int kTileBytes = kTileKeys * D;            // a K or V tile
     // depth of the rings: what two CTAs fit into an SM
-    static constexpr int kStagesK = D == 64 ? 5 : 3;
-    static constexpr int kStagesV = D == 64 ? 5 : NR == 16 && !kBF16 ? 2 : 3;
+    // (16 rows of 128: 155 us with 2 + 3, 196 us with 3 + 2, as V waits longer; one weight tile for both warpgroups and 3 + 3: 157 us)
+    static constexpr int kStagesK = D == 64 ? 5 : NR == 16 ? 2 : 3;
+    static constexpr int kStagesV = D == 64 ? 5 : 3;
     static constexpr int kQRows = 16;                           // columns of S^T: 16 at least
     static constexpr int kQPartBytes = kQRows * D;
-    static constexpr int kWRow = kParts * NR <= 32 ? 32 : 64;   // bytes of a key's weights
+    static constexpr int kWRow = kWParts * NR;                  // bytes of a key's weights: 32 or 64
     static constexpr int kWBytes = kTileKeys * kWRow;
     static constexpr int kOffK = 0;
     static constexpr int kOffV = kOffK + kStagesK * kTileBytes;
@@ -106,10 +117,10 @@ struct PagedLayout {
     static_assert(D == 128 || kGroups * kWBytes + kParts * kQPartBytes >= kTileBytes, "operand of the unused half");
     static_assert(2 * (kSmemBytes + 1024) <= 233472, "two CTAs per SM");
     // a warpgroup's columns: S^T, then the parts of O^T
-    static constexpr int kOCols = (kParts * NR + 15) / 16 * 16;
+    static constexpr int kOCols = kWParts * NR;
     static constexpr int kGroupCols = kQRows + kOCols;
-    static constexpr uint32_t kTmemCols = kGroups * kGroupCols <= 64 ? 64 : 128;
-    static_assert(kGroups * kGroupCols <= 128, "two CTAs per SM");
+    static constexpr uint32_t kTmemCols = kGroups * kGroupCols <= 128 ? 128 : 256;
+    static_assert(kGroups * kGroupCols <= 256, "two CTAs per SM");
 };
 
 template <int NK, int NV, int kGroups>
@@ -325,7 +336,7 @@ __global__ void __launch_bounds__(PagedLayout<D, kBF16, NR>::kThreads, 2)
 paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p)
 {
     using L = PagedLayout<D, kBF16, NR>;
-    constexpr int NK = L::kStagesK, NV = L::kStagesV, G = L::kGroups, QP = L::kParts;
+    constexpr int NK = L::kStagesK, NV = L::kStagesV, G = L::kGroups, QP = L::kParts, WP = L::kWParts;
     constexpr int kProducer = L::kSoftmax / 32, kIssuer = kProducer + 1;      // warps
     constexpr uint32_t kBarAll = 1;                    // named barriers: all softmax threads, 2 + g one warpgroup
     using Bars = PagedBarriers<NK, NV, G>;
@@ -448,8 +459,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             constexpr uint32_t kWCode = L::kWRow == 32 ? 6u : 4u;
             constexpr uint32_t idesc_s = idesc_make(0u, kTileKeys, L::kQRows, false);
             // V^T: 128 rows of which D are the tile's; at D = 64 the others are
-            // whatever lies behind the tile, and their results are not read
-            constexpr uint32_t idesc_o = idesc_make_amn(0u, 128, L::kOCols, true);
+            // whatever lies behind the tile, and their results are not read.  Weights (B) are E5M2.
+            constexpr uint32_t idesc_o = idesc_make_amn(0u, 128, L::kOCols, true) | (1u << 10);
             const uint32_t hi = (uint32_t)(smem_desc(0, 16, 8 * kSwz, kSwzCode) >> 32);
             const uint32_t hi_w = (uint32_t)(smem_desc(0, 16, 8 * L::kWRow, kWCode) >> 32);
             const uint32_t lbo_v = (uint32_t)(L::kTileBytes >> 4) << 16;
@@ -519,7 +530,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         float* row_scale = reinterpret_cast<float*>(smem + L::kOffRows);    // q's power of two * scale * log2 e
         int* row_last = reinterpret_cast<int*>(row_scale + NR);             // last key that a row sees
         float* group_rows = row_scale + 2 * NR;                             // 7 NR numbers of each warpgroup
-        float* row_nmax = group_rows + 7 * NR * g;                          // log2(112) - maximum
+        float* row_nmax = group_rows + 7 * NR * g;                          // kLog2W - maximum
         float* row_shift = row_nmax + NR;                                   // by how much the maximum grows
         float* row_factor = row_nmax + 2 * NR;                              // rescale; in the end the weight of O^T
         float* exch = row_nmax + 3 * NR;                                    // [4][NR]
@@ -644,7 +655,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 const bool edge = (j + 1) * kTileKeys > full || __any_sync(0xffffffffu, !valid);
                 ok = ok && wait_bar(smem_u32(&bars->s_full[g]), ns & 1, abort, kErrPagedSoftmax);
                 tc_fence_after_sync();
-                // s + log2(v_scale): the logarithm of a weight but for the maximum, which comes off with log2(112) on top
+                // s + log2(v_scale): the logarithm of a weight but for the maximum, which comes off with kLog2W on top
                 const uint64_t ks2 = f32x2(ks, ks), lvs2 = f32x2(lvs, lvs);
                 uint64_t x[NR / 2];
                 float top;
@@ -725,7 +736,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     }
                     if (j > first) {
 #pragma unroll 1
-                        for (int part = 0; part < QP; ++part) {
+                        for (int part = 0; part < WP; ++part) {
                             uint32_t o[NR];
                             if constexpr (NR == 8)
                                 tmem_ld8_wait(t_o + part * NR, o);
@@ -771,37 +782,38 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         }
                     }
                 }
-                // ---- weights into E4M3 parts: first to 11 bits, whose differences are exact
+                // ---- weights to f16 (11 bits) and into E5M2 parts
                 if (ok && ns > 0)
                     ok = wait_bar(smem_u32(&bars->pv_done[g]), (ns - 1) & 1, abort, kErrPagedSoftmax + 3);
                 const uint32_t w_row = sW + g * L::kWBytes + tid * L::kWRow;
                 const int swz = L::kWRow == 32 ? (tid >> 2) & 1 : (tid >> 1) & 3;
                 const uint64_t rvs2 = f32x2(rvs, rvs);
                 constexpr int kWords = NR / 4;                              // 32-bit words of a part
-                uint32_t words[(QP * kWords + 3) / 4 * 4];
+                uint32_t words[WP * kWords];
 #pragma unroll
-                for (int r = 0; r < NR / 2; ++r) {
-                    float a, b;
-                    f32x2_split(x[r], a, b);
-                    a = ex2_approx(a);
-                    b = ex2_approx(b);
-                    l[r] = fma_f32x2(f32x2(a, b), rvs2, l[r]);
-                    uint32_t rest = f32x2_to_f16x2(a, b);
+                for (int r = 0; r < NR / 2; r += 2) {
+                    uint32_t rest[2];                                       // four rows
 #pragma unroll
-                    for (int k = 0; k < QP; ++k) {
-                        const uint32_t e = f16x2_to_e4m3x2(rest);
-                        uint32_t& at = words[k * kWords + r / 2];
-                        at = r & 1 ? at | (e << 16) : e;
-                        if (k + 1 < QP)                                     // 16 (rest - part)
-                            rest = mul_f16x2(add_f16x2(rest, e4m3x2_to_f16x2((uint16_t)e) ^ 0x80008000u), 0x4c004c00u);
+                    for (int i = 0; i < 2; ++i) {
+                        float a, b;
+                        f32x2_split(x[r + i], a, b);
+                        a = ex2_approx(a);
+                        b = ex2_approx(b);
+                        l[r + i] = fma_f32x2(f32x2(a, b), rvs2, l[r + i]);
+                        rest[i] = f32x2_to_f16x2(a, b);
+                    }
+#pragma unroll
+                    for (int k = 0; k < WP; ++k) {
+                        words[k * kWords + r / 2] = __byte_perm(rest[0], rest[1], 0x7531);      // the upper bytes
+                        if (k + 1 < WP)                                     // 8 (rest - part), both exact
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                rest[i] = mul_f16x2(add_f16x2(rest[i], (rest[i] & 0xff00ff00u) ^ 0x80008000u), 0x48004800u);
                     }
                 }
-#pragma unroll
-                for (int i = QP * kWords; i < (QP * kWords + 3) / 4 * 4; ++i)
-                    words[i] = 0;
                 if (ok) {
 #pragma unroll
-                    for (int i = 0; i < (QP * kWords + 3) / 4; ++i)
+                    for (int i = 0; i < WP * kWords / 4; ++i)
                         st_shared_v4(w_row + (uint32_t)((i ^ swz) * 16), words[4 * i], words[4 * i + 1], words[4 * i + 2],
                                      words[4 * i + 3]);
                 }
@@ -829,7 +841,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             const bool whole = w.begin == 0 && w.end == w.n;
             const long long slot = (long long)blockIdx.x * 2 + (w.begin > 0 ? 0 : 1);
             if (threadIdx.x < NR) {
-                // join the warpgroups: sums s_g of exp2(logit - max_g + log2 112), weights of their O^T
+                // join the warpgroups: sums s_g of exp2(logit - max_g + kLog2W), weights of their O^T
                 const int r = threadIdx.x;
                 float s[G], nm[G], m = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -870,7 +882,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 for (int k = 0; k < groups; ++k) {
                     float unit = 1.f;
 #pragma unroll 1
-                    for (int part = 0; part < QP; ++part, unit *= 1.f / 16.f) {
+                    for (int part = 0; part < WP; ++part, unit *= 1.f / 8.f) {
                         uint32_t a[NR];
                         const uint32_t at = tmem + lanes + k * L::kGroupCols + L::kQRows + part * NR;
                         if constexpr (NR == 8)
