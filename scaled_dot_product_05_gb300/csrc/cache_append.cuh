@@ -58,12 +58,12 @@ struct AppendParams {
 
 constexpr int kAppendThreads = 256;
 
-// Smallest e in [-60, 60] with amax <= 448 * 2^e (448 = 1.75 * 2^8), as 2^e.
-__device__ __forceinline__ float pow2_scale(float amax)
+// Smallest e in [lo, hi] with amax <= 448 * 2^e (448 = 1.75 * 2^8), as 2^e.
+__device__ __forceinline__ float pow2_scale(float amax, int lo = -60, int hi = 60)
 {
     const uint32_t bits = __float_as_uint(amax);
     int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-    e = max(-60, min(60, e));
+    e = max(lo, min(hi, e));
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 

@@ -77,6 +77,15 @@ struct Params {
 enum : unsigned int { kErrPagedLoad = 0x801, kErrPagedMma = 0x811, kErrPagedSoftmax = 0x821 };
 
 constexpr int kTileKeys = 128;
+
+// The power of two that a row of q is divided by: all of bf16's range, but that
+// it stops at 2^-118, for its inverse to be finite (a row whose largest is
+// below 2^-110 keeps fewer bits).
+__device__ __forceinline__ float query_scale(uint32_t top_bits)
+{
+    return cache::pow2_scale(__uint_as_float(top_bits), -118, 120);
+}
+
 // The running maximum is let behind by up to 2^4 before everything is rescaled
 // to a new one, and weight 1 is held as 2^11: no weight passes 2^15, which the
 // parts need (with 2^2 and 2^13: 64 sequences, 16 rows of 64, 73.6 us against 71.8).
@@ -571,7 +580,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 for (int m = 1; m < kPer; m <<= 1)
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
                 const bool finite = top < 0x7f800000u;
-                const float qs = cache::pow2_scale(__uint_as_float(top)), inv = 1.f / qs;
+                const float qs = query_scale(top), inv = 1.f / qs;
                 const int chunk = D == 128 ? seg ^ (r & 7) : seg ^ ((r >> 1) & 3);
 #pragma unroll
                 for (int e = 0; e < 16; ++e)

@@ -390,7 +390,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
                 }
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                const float qs = cache::pow2_scale(__uint_as_float(top)), inv = 1.f / qs;
+                const float qs = query_scale(top), inv = 1.f / qs;
 #pragma unroll 1
                 for (int s = 0; s < D / 32; ++s) {         // (rolled: code that runs once an item is fetched anew each time)
                     float v[16];

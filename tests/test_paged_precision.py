@@ -117,3 +117,20 @@ def test_weights_of_eleven_bits(gpu, case):
             assert (err <= tol).all(), (b, (err / tol).max().item())
             assert ((lse[b, :, :n].cpu().double() - z).abs() <= ds + 2.0 ** -22 * z.abs()).all(), b
         assert (o[b, n:] == 7).all() and (lse[b, :, n:] == 7).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Sq", [1, 4, 40])
+@pytest.mark.parametrize("shift", [70, 100, -70, -90])
+def test_large_and_small_queries(gpu, Sq, shift):
+    """bf16 reaches to 2^127: queries times a power of two and the scale by its inverse is the same attention, bit for
+    bit."""
+    case = (16, 8, 2, 128, Sq, "bf16", "heads", True, [0, 100, 700], None, 0.1)
+    cache = make_cache(150, 16, 2, 128, "heads", 3)
+    table = tables(150, 3, 50, 2)
+    q = torch.randn((3, Sq, 8, 128), generator=torch.Generator().manual_seed(5)).bfloat16()
+    ref = launch(case, cache, table, q)
+    far = q * 2.0 ** shift
+    assert torch.equal(far * 2.0 ** -shift, q)
+    o, lse = launch(case[:10] + (0.1 * 2.0 ** -shift,), cache, table, far)
+    assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
