@@ -425,14 +425,17 @@ sdpa_status_t sdpa_cache_append(const void *K, const void *V, const sdpa_cache_t
  *   O         device, written, [B][Sq][Hq][D], type `dtype`; rows i >=
  *             count[b] are not written.  A row that sees no key is 0.
  *   LSE       device, fp32 [B][Hq][Sq], or NULL; -infinity for such a row.
- * A softmax weight, the page's v_scale included, is rounded to f16 before it
- * meets V: 2^-11 of itself at most, and where it is below e^-17 of its row's
- * largest (e^-14 with more than 16 rows, Sq * Hq / Hkv) 2^-36 (2^-32) of that.
  *   workspace device scratch of sdpa_paged_workspace_bytes(...) bytes,
  *             16-byte aligned, needing no initialisation, not used by a
  *             concurrent call.
  * Keys in pages outside the pool or positions outside the block table are
  * left out, and the device error word becomes 0x601 or 0x602.
+ *
+ * Numbers.  Scores and sums are fp32.  Elements of Q below 2^-13 (fp16: 2^-10)
+ * of their row's largest are taken within 2^-21 of that largest, the others
+ * exactly.  A softmax weight, the page's v_scale included, is rounded to f16
+ * before it meets V: by 2^-11 of itself, or, below e^-17 of its row's largest
+ * (e^-14 where Sq * Hq / Hkv > 16), by 2^-36 (2^-32) of that.  O rounds once.
  */
 sdpa_status_t sdpa_fwd_paged(const void *Q, const sdpa_cache_t *cache,
                              const int *block_table, const int *start, const int *count,

@@ -13,19 +13,25 @@
 //
 // The codes go to the FP8 tensor cores as they lie in the cache, and the
 // 16-bit operands are split instead into 8-bit parts that add up to them; the
-// products of 8-bit values are exact in the fp32 accumulator.  q, scaled by a
-// power of two, becomes E4M3 parts: two hold the 8 bits of bf16, three the 11
-// of fp16.  A weight w_j = exp(s_j - m) v_scale_j is rounded to f16, the only
-// rounding that it sees (attention over fp16 keys and values rounds its
-// weights so), and cut into four E5M2 parts: each is the upper byte of what
-// the parts before it have left (3 bits of it), held 8 times as large as the
-// one before, in columns of its own.  The parts are the f16 number exactly,
-// subnormal ones included.  A row's largest weight is held as 2^11 to 2^15:
-// weights down to e^-17 of it have 11 bits, and the smallest step is 2^-35 of
-// it (the many small weights of a long cache are the whole output where a token
-// with most of the weight has a value near zero).  Cutting costs no more than
-// rounding into two E4M3 parts did, which lost what was below e^-14 (8
-// sequences of 32768 keys 91.3 us against 91.0).  Nothing is dequantised, and K and V are
+// products of 8-bit values are exact in the fp32 accumulator.  q, divided by a
+// power of two that puts its row's largest element into (224, 448], becomes one
+// (bf16) or two (fp16) E4M3 parts and a last one in E5M2: what rounding to
+// E4M3 leaves of 8 bits, or of 11 the second time, are three bits and a sign, and
+// E5M2 has the finer steps.  Elements down to 2^-13 (bf16) or 2^-10 (fp16) of
+// the row's largest are held exactly, smaller ones within 2^-21 of it (2^-17,
+// from 2^-9 and 2^-6 on, with E4M3 alone, in the same time).
+//
+// A weight w_j = exp(s_j - m) v_scale_j is rounded to f16, the only rounding
+// that it sees (attention over fp16 keys and values rounds its weights so),
+// and cut into four E5M2 parts: each is the upper byte of what the parts
+// before it have left (3 bits of it), held 8 times as large as the one before,
+// in columns of its own.  The parts are the f16 number exactly, subnormal ones
+// included.  A row's largest weight is held as 2^11 to 2^15: weights down to
+// e^-17 of it have 11 bits, and the smallest step is 2^-35 of it (the many
+// small weights of a long cache are the whole output where a token with most
+// of the weight has a value near zero).  Cutting costs no more than rounding
+// into two E4M3 parts did, which lost what was below e^-14 (8 sequences of
+// 32768 keys 91.3 us against 91.0).  Nothing is dequantised, and K and V are
 // read once as bytes.
 //
 // The rows (token, query head) of one KV head are the N side of the products,
@@ -86,13 +92,28 @@ __device__ __forceinline__ float query_scale(uint32_t top_bits)
     return cache::pow2_scale(__uint_as_float(top_bits), -118, 120);
 }
 
+// The next 8-bit part of four elements of a divided row, which it takes off them
+// (exactly); `last`: what is left, as E5M2.
+__device__ __forceinline__ uint32_t query_part(float* v, bool last)
+{
+    if (last)
+        return (uint32_t)f32x2_to_e5m2x2(v[0], v[1]) | ((uint32_t)f32x2_to_e5m2x2(v[2], v[3]) << 16);
+    const uint16_t lo = f32x2_to_e4m3x2(v[0], v[1]), up = f32x2_to_e4m3x2(v[2], v[3]);
+    const float2 a = f16x2_to_f32x2(e4m3x2_to_f16x2(lo)), b = f16x2_to_f32x2(e4m3x2_to_f16x2(up));
+    v[0] -= a.x;
+    v[1] -= a.y;
+    v[2] -= b.x;
+    v[3] -= b.y;
+    return (uint32_t)lo | ((uint32_t)up << 16);
+}
+
 // The running maximum is let behind by up to 2^4 before everything is rescaled
 // to a new one, and weight 1 is held as 2^11: no weight passes 2^15, which the
 // parts need (with 2^2 and 2^13: 64 sequences, 16 rows of 64, 73.6 us against 71.8).
 constexpr float kLag = 4.0f;
 constexpr float kLog2W = 11.0f;
 
-// Shared memory and TMEM of one CTA: NR rows, q in kParts E4M3 parts, weights
+// Shared memory and TMEM of one CTA: NR rows, q in kParts 8-bit parts, weights
 // in kWParts E5M2 parts.
 template <int D, bool kBF16, int NR>
 struct PagedLayout {
@@ -488,10 +509,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
                     for (int q = 0; q < QP; ++q) {
                         const uint32_t q_lo = ((sQ + q * L::kQPartBytes) >> 4) | (1u << 16);
+                        const uint32_t idesc = idesc_s | (q + 1 == QP ? 1u << 10 : 0u);         // q (B): E5M2 in the end
 #pragma unroll
                         for (int kk = 0; kk < D / 32; ++kk)
                             mma_f8_ss(tmem + g * L::kGroupCols, desc_join(hi, k_lo + 2 * kk), desc_join(hi, q_lo + 2 * kk),
-                                      idesc_s, q > 0 || kk > 0);
+                                      idesc, q > 0 || kk > 0);
                     }
                     mma_commit(smem_u32(&bars->s_full[g]));
                     mma_commit(smem_u32(&bars->k_empty[ks]));
@@ -551,7 +573,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         bool ok = true;
         for (; more; nv += w.end - w.begin, more = next_piece<NR>(p, w)) {
             const Item it = item_of<NR>(p, w);
-            // ---- q into E4M3 parts, and each row's numbers
+            // ---- q into 8-bit parts, and each row's numbers
             {
                 constexpr int kPer = L::kSoftmax / L::kQRows;               // threads of a row
                 static_assert(kPer >= D / 16, "a 16-element run a thread");
@@ -590,16 +612,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     for (int part = 0; part < QP; ++part) {
                         uint32_t o[4];
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const uint16_t lo = f32x2_to_e4m3x2(v[e], v[e + 1]);
-                            const uint16_t up = f32x2_to_e4m3x2(v[e + 2], v[e + 3]);
-                            const float2 a = f16x2_to_f32x2(e4m3x2_to_f16x2(lo)), b = f16x2_to_f32x2(e4m3x2_to_f16x2(up));
-                            v[e] -= a.x;
-                            v[e + 1] -= a.y;
-                            v[e + 2] -= b.x;
-                            v[e + 3] -= b.y;
-                            o[e / 4] = (uint32_t)lo | ((uint32_t)up << 16);
-                        }
+                        for (int e = 0; e < 16; e += 4)
+                            o[e / 4] = query_part(&v[e], part + 1 == QP);
                         st_shared_v4(sQ + part * L::kQPartBytes + r * D + chunk * 16, o[0], o[1], o[2], o[3]);
                     }
                 }

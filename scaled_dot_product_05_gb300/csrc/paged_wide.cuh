@@ -4,7 +4,7 @@
 //
 // Here the rows (token, query head) of one KV head are the M side, 128 at a
 // time, and a softmax thread has one row:
-//     S[128 rows][128 keys] = Q K8^T          FP8, q in two or three E4M3 parts
+//     S[128 rows][128 keys] = Q K8^T          FP8, q in two or three 8-bit parts
 //     O[128 rows][D] += W V                   f16, W = exp(s - m) v_scale
 // The weights keep 11 bits: they are rounded to f16 (weight 1 as 2^7, the
 // smallest step 2^-31 of that) and stay in tensor memory, and V's codes are
@@ -255,9 +255,10 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
                         for (int q = 0; q < QP; ++q) {
                             const uint32_t q_lo = ((sQ + q * L::kTileBytes) >> 4) | (1u << 16);
+                            const uint32_t idesc = idesc_s | (q + 1 == QP ? 1u << 7 : 0u);      // q (A): E5M2 in the end
 #pragma unroll
                             for (int kk = 0; kk < D / 32; ++kk)
-                                mma_f8_ss(tmem, desc_join(hi, q_lo + 2 * kk), desc_join(hi, k_lo + 2 * kk), idesc_s,
+                                mma_f8_ss(tmem, desc_join(hi, q_lo + 2 * kk), desc_join(hi, k_lo + 2 * kk), idesc,
                                           q > 0 || kk > 0);
                         }
                         mma_commit(smem_u32(&bars->s_full[g]));
@@ -369,7 +370,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         bool ok = true;
         for (; more; nv += w.end - w.begin, more = next_piece<NR>(p, w)) {
             Item it = item_of<NR>(p, w);
-            // ---- q into E4M3 parts: two threads a row, half of its channels each
+            // ---- q into 8-bit parts: two threads a row, half of its channels each
             float scale;                                                    // of this thread's row in the loop below
             {
                 const int r = threadIdx.x >> 1, half = threadIdx.x & 1;
@@ -409,16 +410,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     for (int part = 0; part < QP; ++part) {
                         uint32_t o[4];
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const uint16_t lo = f32x2_to_e4m3x2(v[e], v[e + 1]);
-                            const uint16_t up = f32x2_to_e4m3x2(v[e + 2], v[e + 3]);
-                            const float2 a = f16x2_to_f32x2(e4m3x2_to_f16x2(lo)), b = f16x2_to_f32x2(e4m3x2_to_f16x2(up));
-                            v[e] -= a.x;
-                            v[e + 1] -= a.y;
-                            v[e + 2] -= b.x;
-                            v[e + 3] -= b.y;
-                            o[e / 4] = (uint32_t)lo | ((uint32_t)up << 16);
-                        }
+                        for (int e = 0; e < 16; e += 4)
+                            o[e / 4] = query_part(&v[e], part + 1 == QP);
                         st_shared_v4(sQ + part * L::kTileBytes + r * D + chunk * 16, o[0], o[1], o[2], o[3]);
                     }
                 }

@@ -542,6 +542,15 @@ __device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float lo, float hi)
     return h;
 }
 
+// Two floats -> two E5M2 bytes (round to nearest even, saturate to +-57344):
+// `lo` in the low byte.
+__device__ __forceinline__ uint16_t f32x2_to_e5m2x2(float lo, float hi)
+{
+    uint16_t h;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(h) : "f"(hi), "f"(lo));
+    return h;
+}
+
 // Two E4M3 bytes -> f16x2 (exact).
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v)
 {

@@ -134,3 +134,28 @@ def test_large_and_small_queries(gpu, Sq, shift):
     assert torch.equal(far * 2.0 ** -shift, q)
     o, lse = launch(case[:10] + (0.1 * 2.0 ** -shift,), cache, table, far)
     assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("Sq", [1, 4, 40])
+def test_queries_with_one_large_channel(gpu, dt, Sq):
+    """A channel 2^8 above the others, at which the keys are zero: the scores are the others' alone.  A query's element
+    is held exactly, or within 2^-14 where its row's largest is above 224: 2^-21 of the largest.  Non-causal and one key each, so
+    that the log-sum-exp is the score."""
+    B, Hq, Hkv, D, page = 48, 8, 2, 128, 16
+    cache = make_cache(B, page, Hkv, D, "heads", 3)
+    cache.k.view(torch.uint8)[..., 7] = 0
+    q = torch.randn((B, Sq, Hq, D), generator=torch.Generator().manual_seed(5))
+    q[..., 7] = 768
+    q = q.to(DT[dt])
+    table = torch.arange(B, dtype=torch.int32)[:, None]
+    # positions 1 - Sq .. 0: keys 0 .. 0
+    case = (page, Hq, Hkv, D, Sq, dt, "heads", False, [1 - Sq] * B, None, None)
+    o, lse = launch(case, cache, table, q)
+    k = PlainCache(cache).rows(0, torch.arange(B), B * page).reshape(B, page, Hkv, D)[:, 0].repeat_interleave(Hq // Hkv, 1)
+    s = torch.einsum("bihd,bhd->bhi", q.double(), k) / math.sqrt(D)
+    mag = torch.einsum("bihd,bhd->bhi", q.double().abs(), k.abs()) / math.sqrt(D)
+    tol = 2.0 ** -17 * mag + 2.0 ** -21.8 * 768 * k.abs().sum(-1)[..., None] / math.sqrt(D) + 1e-6
+    err = (lse.cpu().double() - s).abs()
+    assert (err <= tol).all(), (err / tol).max().item()
