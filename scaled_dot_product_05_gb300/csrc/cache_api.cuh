@@ -530,7 +530,7 @@ sdpa_status_t sdpa_fwd_paged(const void* Q, const sdpa_cache_t* cache, const int
 {
     if (dtype != SDPA_DTYPE_BF16 && dtype != SDPA_DTYPE_FP16)
         return SDPA_ERR_DTYPE;
-    if (!Q || !O || !workspace)
+    if (!Q || !O)
         return SDPA_ERR_NULL_PTR;
     if (!aligned16(Q) || !aligned16(O) || !aligned(LSE, 4))
         return SDPA_ERR_MISALIGNED;
@@ -550,6 +550,8 @@ sdpa_status_t sdpa_fwd_paged(const void* Q, const sdpa_cache_t* cache, const int
     if (!view_ok(q) || !view_ok(o) || !injective(o.st, B, Sq, Hq, D))
         return SDPA_ERR_LAYOUT;
     const size_t need = paged_workspace(Hq, Hkv, Sq, D);
+    if (!workspace)
+        return SDPA_ERR_NULL_PTR;
     if (!aligned16(workspace) || workspace_bytes < need)
         return SDPA_ERR_WORKSPACE;
     // O, LSE and the workspace lie apart from one another and from every input

@@ -194,3 +194,9 @@ def test_rope_table():
     assert t.shape == (70000, 32, 2) and t.dtype == torch.float32
     a = 69999 * 5e5 ** (-2 * 5 / 64)
     assert abs(t[69999, 5, 0].item() - torch.tensor(a, dtype=torch.float64).cos().item()) < 2.0 ** -24
+
+
+@pytest.mark.parametrize("kw,status", [(dict(Hq=9), 4), (dict(B=0), 3), (dict(S=0), 3), (dict(scale=-1.0), 7), ({}, 1)])
+def test_attention_names_the_fault_that_leaves_no_workspace_size(fake, kw, status):
+    """The workspace of sizes that are refused is of 0 bytes, which PyTorch allocates as a null pointer."""
+    assert read(fake, ws=None, n=0, **kw) == status
