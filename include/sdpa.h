@@ -422,6 +422,7 @@ sdpa_status_t sdpa_cache_append(const void *K, const void *V, const sdpa_cache_t
  *   causal    nonzero: it sees positions 0 .. start[b] + i; 0: all of
  *             0 .. start[b] + count[b] - 1.  (The alignment is that of the
  *             sequence's end, unlike sdpa_fwd's.)
+ *   scale     finite, > 0, and so that scale * log2(e) is finite.
  *   O         device, written, [B][Sq][Hq][D], type `dtype`; rows i >=
  *             count[b] are not written.  A row that sees no key is 0.
  *   LSE       device, fp32 [B][Hq][Sq], or NULL; -infinity for such a row.

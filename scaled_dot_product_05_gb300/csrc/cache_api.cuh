@@ -544,7 +544,9 @@ sdpa_status_t sdpa_fwd_paged(const void* Q, const sdpa_cache_t* cache, const int
         return SDPA_ERR_HEADS;
     if (static_cast<__int128>(B) * Sq * Hq > INT32_MAX)
         return SDPA_ERR_BAD_SHAPE;
-    if (!valid_scale(scale))
+    // (the kernels' factor, with log2(e), has to be finite as well)
+    const float scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+    if (!valid_scale(scale) || !std::isfinite(scale_log2))
         return SDPA_ERR_SCALE;
     const View q{Q, resolve(q_layout, Sq, Hq, D), B, Sq, Hq, D, 2}, o{O, resolve(o_layout, Sq, Hq, D), B, Sq, Hq, D, 2};
     if (!view_ok(q) || !view_ok(o) || !injective(o.st, B, Sq, Hq, D))
@@ -591,7 +593,7 @@ sdpa_status_t sdpa_fwd_paged(const void* Q, const sdpa_cache_t* cache, const int
     p.n_pages = cache->n_pages;
     p.max_pages = max_pages;
     p.causal = causal ? 1 : 0;
-    p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+    p.scale_log2 = scale_log2;
     p.page_shift = p.page == 16 ? 4 : p.page == 32 ? 5 : p.page == 64 ? 6 : 7;
     const int nr = paged_tile_rows(Sq, p.group);
     p.row_tiles = static_cast<int>((static_cast<long long>(Sq) * p.group + nr - 1) / nr);

@@ -200,3 +200,9 @@ def test_rope_table():
 def test_attention_names_the_fault_that_leaves_no_workspace_size(fake, kw, status):
     """The workspace of sizes that are refused is of 0 bytes, which PyTorch allocates as a null pointer."""
     assert read(fake, ws=None, n=0, **kw) == status
+
+
+@pytest.mark.parametrize("scale,status", [(2.3e38, OK), (2.4e38, 7), (3.4e38, 7), (1e-45, OK)])
+def test_attention_scale_stays_finite_in_base_two(fake, scale, status):
+    st = read(fake, scale=scale)
+    assert st in status if isinstance(status, tuple) else st == status
