@@ -1,5 +1,6 @@
 """How exactly sdpa_fwd_paged holds its weights and queries, and the kernel
-instances that tests/test_paged_cache.py does not reach.
+instances of the attention and of the append that tests/test_paged_cache.py
+does not reach.
 
 Tolerances.  A weight exp(s - m) v_scale is rounded to f16 once: half a step,
 2^-11 of itself, or half of the smallest step 2^-24 where it is subnormal, with the row's
@@ -14,6 +15,7 @@ import torch
 
 from tests.test_paged_cache import (DEV, DT, HALF, PlainCache, attention64, gpu, i32, launch, make_cache,  # noqa: F401
                                     tables)
+from tests.test_paged_cache import test_append as append_case
 
 WEIGHT = 2.0 ** -11
 
@@ -159,3 +161,18 @@ def test_queries_with_one_large_channel(gpu, dt, Sq):
     tol = 2.0 ** -17 * mag + 2.0 ** -21.8 * 768 * k.abs().sum(-1)[..., None] / math.sqrt(D) + 1e-6
     err = (lse.cpu().double() - s).abs()
     assert (err <= tol).all(), (err / tol).max().item()
+
+
+# page, Hkv, D, S, rot, interleaved, dtype, layout, starts, counts: four rows a lane group and unit
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [
+    (64, 2, 128, 200, 128, False, "bf16", "heads", [0, 5, 63, 64, 100], [200, 199, 65, 1, 0]),
+    (64, 2, 128, 200, 64, True, "fp16", "tokens", [0, 5, 63, 64, 100], [200, 199, 65, 1, 2]),
+    (64, 1, 128, 130, 128, False, "fp16", "pairs", [0, 1], None),
+    (64, 1, 128, 130, 128, True, "bf16", "heads", [3, 63], None),
+    (128, 2, 64, 300, 64, True, "bf16", "pairs", [0, 127, 129, 1], [300, 129, 127, 4]),
+    (128, 2, 64, 300, 64, False, "fp16", "heads", [0, 127, 129, 1], [300, 129, 127, 4]),
+    (32, 2, 128, 70, 0, False, "fp16", "heads", [0, 31, 17], None),
+], ids=lambda c: "-".join(map(str, c[:8])))
+def test_append_instances(gpu, case):
+    append_case(gpu, case)
