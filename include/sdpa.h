@@ -304,7 +304,7 @@ typedef struct {
  * front of the attention: for every row x of D channels (one head of one
  * token)
  *     y = R(position) (x * w / sqrt(mean(x^2) + eps)),
- * computed in fp32 and rounded once.
+ * computed in fp32 (the sum of x^2 has to be within its range) and rounded once.
  *   Q, K      device, read only, [B][S][Hq][D] and [B][S][Hkv][D], type
  *             `dtype` (bf16 or fp16), D 32, 64 or 128.  K is optional: NULL
  *             with Hkv = 0.
@@ -394,16 +394,26 @@ typedef struct {
  *             position that rotates its key.
  *   rope      see sdpa_rope_t.
  * The scale of a page is the smallest power of two s with max|x| <= 448 s over
- * its tokens (of finite values; 2^-60 at least, 2^60 at most), where a call
- * that begins inside a page keeps at least the page's scale, and rounds the
- * page's earlier tokens to a scale that grows.  Larger values and infinities
- * saturate at 448 s, NaN stays NaN.  Pages that a call writes belong to one
- * sequence each and stand in its row of the table once.  Codes are the nearest
- * ones (ties to even) to the exact rotated values, but where the two terms of a
- * rotated value cancel to less than a sixteenth: there fp32's roundings count.  Slots behind the last token are not written.
+ * its tokens (of finite values, as fp32 has them after the rotation; 2^-60 at
+ * least, 2^60 at most), where a call that begins inside a page keeps at least
+ * the page's scale, and rounds the page's earlier tokens to a scale that
+ * grows.  Larger values and infinities saturate at 448 s, NaN stays NaN.  Pages
+ * that a call writes belong to one sequence each and stand in its row of the
+ * table once.  Codes are the nearest ones (ties to even) to x / s; those of
+ * rotated keys to the exact rotated values, except where fp32's roundings (an
+ * ulp or two) may decide between two neighbouring codes: where the two terms of a
+ * rotated value cancel to less than an eighth, and for subnormal codes
+ * (|x| < 2^-6 s).  Under a scale that is no power of two, which only the
+ * caller can have put there, x / s is rounded to fp32 first.  Slots behind the
+ * last token are not written.
  * A page index outside the pool, a position outside the block table and a
  * position outside the rotation table are not followed: what would go there
  * is not written and the device error word becomes 0x601, 0x602 or 0x701.
+ * (A key whose position is outside the rotation table is not written; its value
+ * is.)  A sequence with start[b] < 0 is left out as a whole, also its tokens at
+ * positions from 0 on, with 0x602, though sdpa_fwd_paged takes such a start (rows
+ * at negative positions see no key): the same start and count then read slots
+ * that this call has not written.
  */
 sdpa_status_t sdpa_cache_append(const void *K, const void *V, const sdpa_cache_t *cache,
                                 const int *block_table, const int *start, const int *count,

@@ -294,7 +294,9 @@ def sdpa_cache_append(k, v, cache: PagedCache, block_table, start, count=None, *
     rotated by their positions on the way.  Token i < count[b] of sequence b
     goes to position start[b] + i: page block_table[b, position / page_size].
     block_table (int32 [B, max_pages]), start and count (int32 [B]; None: S
-    tokens each) are CUDA tensors; nothing is read back to the host."""
+    tokens each) are CUDA tensors; nothing is read back to the host.  A
+    sequence with a negative start is left out as a whole and reported by
+    :func:`sdpa_device_error`, as are indexes out of range."""
     dev = cache._device
     shape = k.shape
     if len(shape) != 4 or v.shape != shape or k.dtype != v.dtype:

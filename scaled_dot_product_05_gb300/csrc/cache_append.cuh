@@ -24,6 +24,8 @@
 // million to the code on the other side of a border.  Rows with an element
 // that close to one are computed again without rounding (7% of the time of a
 // prompt's append, most of it the test).
+// (The border test looks at normal codes under a power-of-two scale, before the
+// scale is known; the maximum behind the scale is fp32's.)
 #pragma once
 
 #include "rope.cuh"
@@ -104,8 +106,8 @@ __device__ __forceinline__ bool any_near(const float* x)
 }
 
 // Rotates a lane's 8 elements, those next to a border by the exact product, so
-// that they get its codes (but where its two terms cancel to less than about a
-// sixteenth, and for subnormal codes).
+// that they get its codes (but where its two terms cancel to less than an
+// eighth, and for subnormal codes).
 template <bool kInter>
 __device__ __forceinline__ void rotate_for_codes(float* x, const float* cs, const float* sn)
 {
