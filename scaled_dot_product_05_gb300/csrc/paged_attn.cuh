@@ -49,7 +49,7 @@
 //
 // Bound by HBM for long caches, by a chain of latencies below.  Measured (D =
 // 128, 32 query heads on 8, bf16): 8 sequences of 32768 keys 88 - 92 us (537 MB:
-// 5.8 - 6.1 TB/s), 64 of up to 8192 114 - 123 us (684 MB), one of 500 keys 8.5 us;
+// 5.8 - 6.1 TB/s), 64 of up to 8192 114 - 124 us (684 MB), one of 500 keys 8.6 us;
 // without any loads the first of these takes 63 us, one tile of a CTA 0.9 us.
 #pragma once
 
