@@ -126,7 +126,8 @@ struct PagedLayout {
     static constexpr int kThreads = kSoftmax + 64;              // then TMA producer, MMA issuer
     static constexpr int kTileBytes = kTileKeys * D;            // a K or V tile
     // depth of the rings: what two CTAs fit into an SM
-    // (16 rows of 128: 155 us with 2 + 3, 196 us with 3 + 2, as V waits longer; one weight tile for both warpgroups and 3 + 3: 157 us)
+    // (64 sequences of up to 8192 keys, 16 rows of 128: 154 us with 2 + 3 and 196 us with 3 + 2, as V waits longer;
+    // one weight tile for both warpgroups leaves room for 3 + 3: 157 us)
     static constexpr int kStagesK = D == 64 ? 5 : NR == 16 ? 2 : 3;
     static constexpr int kStagesV = D == 64 ? 5 : 3;
     static constexpr int kQRows = 16;                           // columns of S^T: 16 at least
@@ -489,7 +490,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             constexpr uint32_t kWCode = L::kWRow == 32 ? 6u : 4u;
             constexpr uint32_t idesc_s = idesc_make(0u, kTileKeys, L::kQRows, false);
             // V^T: 128 rows of which D are the tile's; at D = 64 the others are
-            // whatever lies behind the tile, and their results are not read.  Weights (B) are E5M2.
+            // whatever lies behind the tile, and their results are not read
+            // (B, the weights, is E5M2)
             constexpr uint32_t idesc_o = idesc_make_amn(0u, 128, L::kOCols, true) | (1u << 10);
             const uint32_t hi = (uint32_t)(smem_desc(0, 16, 8 * kSwz, kSwzCode) >> 32);
             const uint32_t hi_w = (uint32_t)(smem_desc(0, 16, 8 * L::kWRow, kWCode) >> 32);
