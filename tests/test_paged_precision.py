@@ -29,7 +29,8 @@ def floor_of(rows):
 @pytest.mark.gpu
 @pytest.mark.parametrize("spread", [0.0, 0.5])
 @pytest.mark.parametrize("depth", [9, 12, 14, 15, 17])
-@pytest.mark.parametrize("dt,D,Sq", [("bf16", 128, 1), ("bf16", 64, 4), ("fp16", 128, 1), ("fp16", 128, 4), ("bf16", 128, 8)])
+@pytest.mark.parametrize("dt,D,Sq", [("bf16", 128, 1), ("bf16", 64, 4), ("bf16", 128, 4), ("bf16", 128, 8),
+                                     ("fp16", 128, 1), ("fp16", 64, 1), ("fp16", 128, 4), ("fp16", 64, 8)])
 def test_small_weights_below_a_sink_without_a_value(gpu, dt, D, Sq, depth, spread):
     """One token far above the others whose value is zero: the output is the others' alone, however small their weights.
     All values are positive, so the bound is one relative to the output.  More items than CTAs, so that one CTA holds
