@@ -1,0 +1,612 @@
+"""Measured cases of the attention whose rows see part of the keys, and of
+what keeps a cache small: attention with a sliding window and a few first
+tokens that stay visible (its gradient, and its form over the paged 8-bit
+cache), attention of a tree of drafted tokens over that cache, the attention
+weight that each cached key has drawn, and the eviction of the keys with the
+least of it.
+
+A case is a dict of plain sizes.  `prepare` makes what a program has in hand
+before the call, `run` is one call, in elementary torch operations or, where
+`own` is set, through the library, and `exact` states the definition in 64
+bits."""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+E4M3_MAX = 448.0
+_TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+# ------------------------------------------------------------------- cases --
+
+def listed():
+    return [
+        # one training step's attention over long documents: grouped heads, a window of 1024, four first tokens
+        dict(name="window fwd 8192", op="window", B=2, S=8192, Hq=32, Hkv=8, D=128, dtype="bf16", window=1024, sinks=4),
+        # a small batch of odd length: 16 heads of 64, the first token stays
+        dict(name="window fwd mha 999", op="window", B=4, S=999, Hq=16, Hkv=16, D=64, dtype="fp16", window=256, sinks=1),
+        # the gradient of a training step at the causal GQA headline shape
+        dict(name="window bwd 4096", op="window_bwd", B=2, S=4096, Hq=32, Hkv=8, D=128, dtype="bf16", window=1024,
+             sinks=4),
+        # the gradient of the small batch, no token stays
+        dict(name="window bwd mha 999", op="window_bwd", B=4, S=999, Hq=16, Hkv=16, D=64, dtype="fp16", window=256,
+             sinks=0),
+        # one short chat, one token: the smallest call, where latency counts
+        dict(name="paged window b1", op="paged_window", B=1, S=1, Hq=32, Hkv=8, D=128, page=16, dtype="bf16", ctx=1500,
+             ragged=False, window=512, sinks=4),
+        # a served batch of long streams, one token each; pages behind the window have been given back
+        dict(name="paged window b64", op="paged_window", B=64, S=1, Hq=32, Hkv=8, D=128, page=64, dtype="bf16",
+             ctx=16384, ragged=True, window=4096, sinks=4),
+        # 16 drafted tokens for each of 8 requests
+        dict(name="tree b8 16 nodes", op="tree", B=8, S=16, Hq=32, Hkv=8, D=128, page=64, dtype="bf16", ctx=8192,
+             ragged=True),
+        # one request, a wide draft behind a long prompt
+        dict(name="tree b1 61 nodes", op="tree", B=1, S=61, Hq=32, Hkv=8, D=128, page=32, dtype="fp16", ctx=20001,
+             ragged=False),
+        # the weights of a decoding step of 8 sequences of 32768 keys, added to what the keys have drawn before
+        dict(name="weights b8 32k", op="weights", B=8, S=1, Hq=32, Hkv=8, D=128, page=64, dtype="bf16", ctx=32768,
+             ragged=False),
+        # those of a chunk of two long prompts
+        dict(name="weights chunk 512", op="weights", B=2, S=512, Hq=32, Hkv=8, D=128, page=64, dtype="bf16", ctx=8192,
+             ragged=True),
+        # a long batch is brought down to a quarter of its keys
+        dict(name="evict b8 32k", op="evict", B=8, Hkv=8, D=128, page=64, ctx=32768, ragged=False, budget=8192, sinks=4,
+             recent=1024),
+        # one chat is brought down to half
+        dict(name="evict b1 4001", op="evict", B=1, Hkv=16, D=64, page=16, ctx=4001, ragged=False, budget=2000, sinks=4,
+             recent=256),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["window", "window_bwd", "paged_window", "tree", "weights", "evict"])
+    D = rng.choice([64, 128])
+    Hkv = rng.choice([1, 2, 4, 8, 16])
+    Hq = Hkv * rng.choice([1, 2, 3, 4, 8])
+    dtype = rng.choice(["bf16", "bf16", "fp16"])
+    if op in ("window", "window_bwd"):
+        if op == "window":
+            D = rng.choice([32, 64, 128])
+        B = _log(rng, 1, 16)
+        window, sinks = _log(rng, 1, 4096), rng.choice([0, 1, 4, 4, 100, 200])
+        top = 2 * 4096 * 32 * 128 * 1024 // (B * Hq * D * min(4096, window + sinks))
+        return dict(op=op, B=B, S=max(1, min(_log(rng, 1, 8192), top)), Hq=Hq, Hkv=Hkv, D=D, dtype=dtype, window=window,
+                    sinks=sinks)
+    page = rng.choice([16, 32, 64, 128])
+    if op == "evict":
+        B = _log(rng, 1, 32)
+        ctx = max(8, min(_log(rng, 8, 40000), 8 * 32768 * 8 * 128 // (B * Hkv * D)))
+        sinks = rng.choice([0, 1, 4])
+        recent = rng.choice([0, 1, ctx // 8])
+        budget = max(1, sinks + recent, _log(rng, 4, ctx + 4))
+        return dict(op=op, B=B, Hkv=Hkv, D=D, page=page, ctx=ctx, ragged=rng.random() < 0.7, budget=budget, sinks=sinks,
+                    recent=recent)
+    B = _log(rng, 1, 64)
+    S = _log(rng, 1, 64) if op == "tree" else rng.choice([1, 1, _log(rng, 1, 16), _log(rng, 1, 300)])
+    ctx = S + min(_log(rng, 1, 32768), 8 * 32768 * 8 * 128 // (B * Hkv * D))
+    if S * B * ctx * Hq * D > 2 * 512 * 8192 * 32 * 128:
+        ctx = S + 2 * 512 * 8192 * 32 * 128 // (S * B * Hq * D)
+    case = dict(op=op, B=B, S=S, Hq=Hq, Hkv=Hkv, D=D, page=page, dtype=dtype, ctx=ctx, ragged=rng.random() < 0.7)
+    if op == "paged_window":
+        case.update(window=_log(rng, 1, 8192), sinks=rng.choice([0, 1, 4, 100, 200]))
+    return case
+
+
+# -------------------------------------------------------------- the inputs --
+
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(int(seed))
+    return g
+
+
+def _host_gen(seed, part):
+    g = torch.Generator()
+    g.manual_seed(1000 * part + int(seed))
+    return g
+
+
+def _lengths(case, seed):
+    """(tokens in the cache before the call, new tokens) of each sequence, on the host; of an eviction (its tokens, none)."""
+    B, S, ctx = case["B"], case.get("S", 0), case["ctx"]
+    top = max(0, ctx - S)
+    start = torch.full((B,), top, dtype=torch.int64)
+    if case["ragged"]:
+        start = torch.randint(top // 4, top + 1, (B,), generator=_host_gen(seed, 1))
+    return start, torch.full((B,), S, dtype=torch.int64)
+
+
+def _pow2_scale(amax):
+    """The smallest power of two s with amax <= 448 s (between 2^-60 and 2^60)."""
+    m, e = torch.frexp((amax / E4M3_MAX).clamp(min=2.0 ** -60))
+    e = torch.where(m == 0.5, e - 1, e).clamp(-60, 60)
+    return torch.ldexp(torch.ones_like(amax), e)
+
+
+def _cache(case, seed, g, more=0):
+    """A page pool and its page table, pages handed out in random order, `more` further pages for each sequence in a
+    second table."""
+    B, Hkv, D, page = case["B"], case["Hkv"], case["D"], case["page"]
+    width = -(-case["ctx"] // page)
+    n_pages = B * (width + more) + 7
+    ids = torch.randperm(n_pages, generator=_host_gen(seed, 2))[:B * (width + more)].to(torch.int32).to(DEV)
+    table, table2 = ids[:B * width].reshape(B, width), ids[B * width:].reshape(B, more)
+    out = []
+    for part in range(2):
+        codes = torch.empty((n_pages, page, Hkv, D), dtype=torch.float8_e4m3fn, device=DEV)
+        scale = torch.empty((n_pages, Hkv), dtype=torch.float32, device=DEV)
+        step = max(1, (1 << 26) // (page * Hkv * D))
+        for p in range(0, n_pages, step):
+            x = torch.randn((min(step, n_pages - p), page, Hkv, D), generator=g, device=DEV)
+            x *= 0.5 + torch.rand((x.shape[0], 1, Hkv, 1), generator=g, device=DEV)
+            s = _pow2_scale(x.abs().amax((1, 3)))
+            codes[p:p + step] = (x / s[:, None, :, None]).to(torch.float8_e4m3fn)
+            scale[p:p + step] = s
+        out += [codes, scale]
+    k, ks, v, vs = out
+    return k, v, ks, vs, table, table2
+
+
+def _tree(case, seed):
+    """Parents of the drafted tokens (each drafted behind its parent, -1: behind the text), and which of them each
+    sees: itself and those on its way to the text, a bit each in words of 32."""
+    B, S = case["B"], case["S"]
+    h = _host_gen(seed, 3)
+    parents = torch.full((B, S), -1, dtype=torch.int64)
+    sees = torch.zeros((B, S, S), dtype=torch.bool)
+    for i in range(S):
+        sees[:, i, i] = True
+        if i:
+            # near tokens more often: drafts are a few long branches and many short ones
+            up = (torch.rand((B,), generator=h) ** 2 * (i + 1)).long() + 1
+            parents[:, i] = (i - up).clamp(min=-1)
+            has = parents[:, i] >= 0
+            sees[has, i] |= sees[has, parents[has, i]]
+    bits = torch.zeros((B, S, -(-S // 32) * 32), dtype=torch.int64)
+    bits[:, :, :S] = sees
+    words = (bits.reshape(B, S, -1, 32) << torch.arange(32)).sum(-1)
+    words = torch.where(words >= 1 << 31, words - (1 << 32), words).to(torch.int32)
+    return words.to(DEV), sees.to(DEV)
+
+
+def prepare(case, seed):
+    g = _gen(seed)
+    op, Hkv, D = case["op"], case["Hkv"], case["D"]
+    B = case["B"]
+    st = dict(case)
+    if own:
+        import scaled_dot_product_05_gb300 as lib
+        st["lib"] = lib
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device=DEV)
+
+    if op in ("window", "window_bwd"):
+        dt, S, Hq = _TYPES[case["dtype"]], case["S"], case["Hq"]
+        st.update(q=normal(B, S, Hq, D).to(dt), k=normal(B, S, Hkv, D).to(dt), v=normal(B, S, Hkv, D).to(dt))
+        if op == "window_bwd":
+            st["o"], st["lse"] = _window_plain(st)
+            st["do"] = normal(B, S, Hq, D).to(dt)
+            if own:
+                st["ws"] = torch.empty(lib.bwd_workspace_bytes(B, Hq, S, D), dtype=torch.uint8, device=DEV)
+        return st
+
+    page = case["page"]
+    start, count = _lengths(case, seed)
+    st["start"], st["count"] = start.to(torch.int32).to(DEV), count.to(torch.int32).to(DEV)
+    more = -(-case["budget"] // page) if op == "evict" else 0
+    st["kc"], st["vc"], st["ks"], st["vs"], st["table"], st["table2"] = _cache(case, seed, g, more)
+    if own:
+        st["cache"] = lib.PagedCache(st["kc"], st["vc"], st["ks"], st["vs"])
+    if op == "evict":
+        # weights drawn so far: a few keys have most of them, keys of one text piece alike have none at all
+        x = normal(B, Hkv, case["ctx"])
+        st["score"] = torch.where(x > -1, (2 * x).exp() * 1e-3, torch.zeros_like(x))
+        st["kept"] = torch.zeros((B, Hkv, case["budget"]), dtype=torch.int32, device=DEV)
+        st["score2"] = torch.zeros((B, Hkv, case["budget"]), dtype=torch.float32, device=DEV)
+        return st
+    dt, S, Hq = _TYPES[case["dtype"]], case["S"], case["Hq"]
+    st["q"] = normal(B, S, Hq, D).to(dt)
+    if op == "paged_window":
+        # pages that no row sees any more have been given back
+        p0 = torch.arange(st["table"].shape[1], device=DEV) * page
+        gone = (p0 >= case["sinks"]) & (p0 + page <= (st["start"] - case["window"] + 1)[:, None])
+        st["table"] = torch.where(gone, torch.full_like(st["table"], -1), st["table"])
+    if op == "tree":
+        st["mask"], st["sees"] = _tree(case, seed)
+    if op == "weights":
+        st["score"] = torch.rand((B, Hkv, case["ctx"]), generator=g, device=DEV)
+        st["out"] = torch.zeros_like(st["score"])
+        st["lse"] = _paged_plain(st)[1]
+    elif own:
+        st["ws"] = torch.empty(lib.paged_workspace_bytes(B, Hq, Hkv, S, D), dtype=torch.uint8, device=DEV)
+    return st
+
+
+# --------------------------------------------------------- the plain forms --
+
+def _window_seen(i, j, window, sinks):
+    """Whether row i sees key j."""
+    return (j <= i) & ((j > i - window) | (j < sinks))
+
+
+def _window_blocks(s):
+    """Row blocks with the keys that some row of the block sees: (rows, keys, mask)."""
+    S, window, sinks = s["S"], s["window"], s["sinks"]
+    for r0 in range(0, S, 1024):
+        r1 = min(S, r0 + 1024)
+        k0 = max(0, r0 - window + 1)
+        keys = torch.arange(k0, r1, device=DEV)
+        if min(sinks, k0):
+            keys = torch.cat([torch.arange(min(sinks, k0), device=DEV), keys])
+        yield r0, r1, keys, _window_seen(torch.arange(r0, r1, device=DEV)[:, None], keys, window, sinks)
+
+
+def _heads(x, Hkv):
+    """[B, S, H, D] as [B, Hkv, H / Hkv, S, D] in 32 bits."""
+    B, S, H, D = x.shape
+    return x.float().reshape(B, S, Hkv, H // Hkv, D).permute(0, 2, 3, 1, 4)
+
+
+def _rows(x):
+    """The way back from `_heads`."""
+    B, Hkv, G, S, D = x.shape
+    return x.permute(0, 3, 1, 2, 4).reshape(B, S, Hkv * G, D)
+
+
+def _window_plain(s):
+    q, k, v = _heads(s["q"], s["Hkv"]), _heads(s["k"], s["Hkv"]), _heads(s["v"], s["Hkv"])
+    o = torch.empty_like(q)
+    lse = torch.empty(q.shape[:-1], device=DEV)
+    for r0, r1, keys, seen in _window_blocks(s):
+        a = torch.matmul(q[..., r0:r1, :], k[..., keys, :].transpose(-1, -2)) * (1 / math.sqrt(s["D"]))
+        a = a.masked_fill(~seen, float("-inf"))
+        m = a.amax(-1, keepdim=True)
+        p = (a - m).exp()
+        l = p.sum(-1, keepdim=True)
+        o[..., r0:r1, :] = torch.matmul(p, v[..., keys, :]) / l
+        lse[..., r0:r1] = (m + l.log())[..., 0]
+    return _rows(o).to(s["q"].dtype), lse.flatten(1, 2)
+
+
+def _window_bwd_plain(s):
+    """P = exp(S - LSE), dV = P^T dO, dS = P (dO V^T - dO . O), dQ = scale dS K, dK = scale dS^T Q."""
+    q, k, v, o, do = (_heads(s[n], s["Hkv"]) for n in ("q", "k", "v", "o", "do"))
+    scale = 1 / math.sqrt(s["D"])
+    lse = s["lse"].reshape(q.shape[:-1])[..., None]
+    delta = (do * o).sum(-1, keepdim=True)
+    dq, dk, dv = torch.empty_like(q), torch.zeros_like(k), torch.zeros_like(v)
+    for r0, r1, keys, seen in _window_blocks(s):
+        r = slice(r0, r1)
+        kk, vv = k[..., keys, :], v[..., keys, :]
+        p = (torch.matmul(q[..., r, :], kk.transpose(-1, -2)) * scale - lse[..., r, :]).exp()
+        p = p.masked_fill(~seen, 0.0)
+        ds = p * (torch.matmul(do[..., r, :], vv.transpose(-1, -2)) - delta[..., r, :]) * scale
+        dq[..., r, :] = torch.matmul(ds, kk)
+        dk.index_add_(3, keys, torch.matmul(ds.transpose(-1, -2), q[..., r, :]).sum(2, keepdim=True))
+        dv.index_add_(3, keys, torch.matmul(p.transpose(-1, -2), do[..., r, :]).sum(2, keepdim=True))
+    dt = s["q"].dtype
+    return _rows(dq).to(dt), _rows(dk).to(dt), _rows(dv).to(dt)
+
+
+def _gathered(s, codes, scale):
+    """The cache's values at each position, [B, Hkv, L, D]."""
+    t = s["table"].long().clamp(min=0)
+    x = codes[t].float() * scale[t][:, :, None, :, None]
+    return x.flatten(1, 2).permute(0, 2, 1, 3)
+
+
+def _paged_scores(s):
+    """Scores [B, Hkv, S * G, L] (-inf where a row does not see a key), row i * G + head of the group."""
+    q, B, S, Hq, Hkv, D = s["q"], s["B"], s["S"], s["Hq"], s["Hkv"], s["D"]
+    G = Hq // Hkv
+    k = _gathered(s, s["kc"], s["ks"])
+    L = k.shape[2]
+    qf = q.float().reshape(B, S, Hkv, G, D).permute(0, 2, 1, 3, 4).reshape(B, Hkv, S * G, D)
+    sc = torch.matmul(qf, k.transpose(2, 3)) * (1 / math.sqrt(D))
+    j = torch.arange(L, device=DEV)
+    start = s["start"][:, None, None]
+    pos = start + torch.arange(S, device=DEV)[:, None]
+    if s["op"] == "paged_window":
+        seen = _window_seen(pos, j, s["window"], s["sinks"])
+    elif s["op"] == "tree":
+        d = (j - start).clamp(0, S - 1).expand(B, S, L)                  # which drafted token a key is
+        word = s["mask"].long().gather(2, d >> 5)
+        seen = (j < start) | ((j < start + S) & ((word >> (d & 31)) & 1 == 1))
+    else:
+        seen = j <= pos
+    seen = seen[:, None, :, None].expand(B, 1, S, G, L).reshape(B, 1, S * G, L)
+    return sc.masked_fill(~seen, float("-inf"))
+
+
+def _paged_plain(s):
+    B, S, Hq, Hkv, D = s["B"], s["S"], s["Hq"], s["Hkv"], s["D"]
+    G = Hq // Hkv
+    sc = _paged_scores(s)
+    m = sc.amax(-1, keepdim=True)
+    p = (sc - m).exp()
+    l = p.sum(-1, keepdim=True)
+    lse = (m + l.log())[..., 0].reshape(B, Hkv, S, G).permute(0, 1, 3, 2).reshape(B, Hq, S)
+    o = torch.matmul(p, _gathered(s, s["vc"], s["vs"])) / l
+    o = o.reshape(B, Hkv, S, G, D).permute(0, 2, 1, 3, 4).reshape(B, S, Hq, D)
+    return o.to(s["q"].dtype), lse
+
+
+def _weights_plain(s):
+    """What a key has drawn before (nothing, if it is new), and its weights of this call's rows."""
+    B, S, Hq, Hkv, ctx = s["B"], s["S"], s["Hq"], s["Hkv"], s["ctx"]
+    G = Hq // Hkv
+    z = s["lse"].reshape(B, Hkv, G, S).permute(0, 1, 3, 2).reshape(B, Hkv, S * G, 1)
+    w = (_paged_scores(s) - z).exp().sum(2)[..., :ctx]
+    j = torch.arange(ctx, device=DEV)
+    start = s["start"][:, None, None]
+    total = w + torch.where(j < start, s["score"], torch.zeros_like(w))
+    s["out"].copy_(torch.where(j < start + S, total, s["out"]))
+    return s["out"]
+
+
+def _evict_plain(s):
+    B, Hkv, page, budget, ctx = s["B"], s["Hkv"], s["page"], s["budget"], s["ctx"]
+    n = s["start"][:, None, None].long()
+    j = torch.arange(ctx, device=DEV)
+    # first and last tokens stay, then those with the largest weight, the earlier one where two are equal
+    x = s["score"].double()
+    x = torch.where((j < s["sinks"]) | (j >= n - s["recent"]), torch.full_like(x, math.inf), x)
+    x = torch.where(j < n, x, torch.full_like(x, -math.inf))
+    kept = x.sort(dim=-1, descending=True, stable=True)[1][..., :budget].sort(-1)[0]
+    kept = torch.nn.functional.pad(kept, (0, budget - kept.shape[-1]))
+    i = torch.arange(budget, device=DEV)
+    live = i < n.clamp(max=budget)                                       # [B, 1, budget]
+    s["kept"].copy_(torch.where(live, kept, s["kept"].long()))
+    s["score2"].copy_(torch.where(live, s["score"].gather(2, kept), s["score2"]))
+    b = torch.arange(B, device=DEV)[:, None, None].expand(kept.shape)
+    h = torch.arange(Hkv, device=DEV)[None, :, None].expand(kept.shape)
+    src = s["table"].long()[b, kept // page]
+    dst = s["table2"].long()[b, (i // page).expand(kept.shape)]
+    use = live.expand(kept.shape)
+    for codes, scale in ((s["kc"], s["ks"]), (s["vc"], s["vs"])):
+        x = codes[src, kept % page, h].float() * scale[src, h][..., None]             # [B, Hkv, budget, D]
+        amax = torch.zeros_like(scale)
+        flat = (dst * Hkv + h)[use]
+        amax = amax.flatten().scatter_reduce(0, flat, x.abs().amax(-1)[use], "amax").reshape(scale.shape)
+        touched = torch.zeros(scale.numel(), dtype=torch.bool, device=DEV).index_fill_(0, flat, True).reshape(scale.shape)
+        scale.copy_(torch.where(touched, _pow2_scale(amax), scale))
+        y = (x / scale[dst, h][..., None]).to(torch.float8_e4m3fn)
+        codes[dst[use], (i % page).expand(kept.shape)[use], h[use]] = y[use]
+    return s["kept"], s["score2"], s["kc"], s["vc"], s["ks"], s["vs"]
+
+
+def run(s):
+    op = s["op"]
+    if not own:
+        return {"window": _window_plain, "window_bwd": _window_bwd_plain, "paged_window": _paged_plain,
+                "tree": _paged_plain, "weights": _weights_plain, "evict": _evict_plain}[op](s)
+    lib = s["lib"]
+    if op == "window":
+        lse = torch.empty((s["B"], s["Hq"], s["S"]), dtype=torch.float32, device=DEV)
+        return lib.sdpa_fwd_window(s["q"], s["k"], s["v"], lse=lse, window=s["window"], sinks=s["sinks"]), lse
+    if op == "window_bwd":
+        return lib.sdpa_bwd_window(s["q"], s["k"], s["v"], s["o"], s["do"], s["lse"], window=s["window"],
+                                   sinks=s["sinks"], workspace=s["ws"])
+    if op == "weights":
+        return lib.sdpa_cache_weights(s["q"], s["cache"], s["table"], s["start"], s["count"], s["lse"], s["score"],
+                                      s["out"])
+    if op == "evict":
+        lib.sdpa_cache_evict(s["cache"], s["table"], s["start"], s["score"], s["table2"], budget=s["budget"],
+                             sinks=s["sinks"], recent=s["recent"], kept=s["kept"], kept_score=s["score2"])
+        return s["kept"], s["score2"], s["kc"], s["vc"], s["ks"], s["vs"]
+    lse = torch.empty((s["B"], s["Hq"], s["S"]), dtype=torch.float32, device=DEV)
+    if op == "paged_window":
+        o = lib.sdpa_fwd_paged_window(s["q"], s["cache"], s["table"], s["start"], s["count"], lse=lse,
+                                      window=s["window"], sinks=s["sinks"], workspace=s["ws"])
+    else:
+        o = lib.sdpa_fwd_paged_tree(s["q"], s["cache"], s["table"], s["start"], s["mask"], s["count"], lse=lse,
+                                    workspace=s["ws"])
+    return o, lse
+
+
+# ------------------------------------------------- the definition, 64 bits --
+
+def _seen_keys(r0, r1, window, sinks):
+    """Key numbers that rows r0 .. r1 - 1 see, and for each row which of them."""
+    lo = max(0, r0 - window + 1)
+    keys = sorted(set(range(min(sinks, r1))) | set(range(lo, r1)))
+    keys = torch.tensor(keys, device=DEV)
+    i = torch.arange(r0, r1, device=DEV)[:, None]
+    hidden = (keys > i) | ((i - keys >= window) & (keys >= sinks))
+    return keys, hidden
+
+
+def _exact_window(s):
+    B, S, Hq, G, D = s["B"], s["S"], s["Hq"], s["Hq"] // s["Hkv"], s["D"]
+    o = torch.empty((B, S, Hq, D), dtype=torch.float64, device=DEV)
+    lse = torch.empty((B, Hq, S), dtype=torch.float64, device=DEV)
+    for r0 in range(0, S, 512):
+        r1 = min(S, r0 + 512)
+        keys, hidden = _seen_keys(r0, r1, s["window"], s["sinks"])
+        for h in range(Hq):
+            k, v = s["k"][:, keys, h // G].double(), s["v"][:, keys, h // G].double()
+            a = torch.einsum("bid,bjd->bij", s["q"][:, r0:r1, h].double(), k) / math.sqrt(D)
+            a[:, hidden] = -math.inf
+            z = torch.logsumexp(a, -1)
+            lse[:, h, r0:r1] = z
+            o[:, r0:r1, h] = torch.einsum("bij,bjd->bid", (a - z[..., None]).exp(), v)
+    return o, lse
+
+
+def _exact_window_bwd(s):
+    """From the rows' weights w_ij = exp(s_ij - LSE_i): d s_ij = w_ij (dO_i . v_j - dO_i . O_i)."""
+    B, S, Hq, Hkv, D = s["B"], s["S"], s["Hq"], s["Hkv"], s["D"]
+    G = Hq // Hkv
+    dq = torch.zeros((B, S, Hq, D), dtype=torch.float64, device=DEV)
+    dk = torch.zeros((B, S, Hkv, D), dtype=torch.float64, device=DEV)
+    dv = torch.zeros_like(dk)
+    for r0 in range(0, S, 512):
+        r1 = min(S, r0 + 512)
+        keys, hidden = _seen_keys(r0, r1, s["window"], s["sinks"])
+        for h in range(Hq):
+            q, g, o = (s[n][:, r0:r1, h].double() for n in ("q", "do", "o"))
+            k, v = s["k"][:, keys, h // G].double(), s["v"][:, keys, h // G].double()
+            w = (torch.einsum("bid,bjd->bij", q, k) / math.sqrt(D) - s["lse"][:, h, r0:r1, None].double()).exp()
+            w[:, hidden] = 0
+            d = w * torch.einsum("bid,bjd->bij", g, v) - w * torch.einsum("bid,bid->bi", g, o)[..., None]
+            d /= math.sqrt(D)
+            dq[:, r0:r1, h] = torch.einsum("bij,bjd->bid", d, k)
+            dk[:, keys, h // G] += torch.einsum("bij,bid->bjd", d, q)
+            dv[:, keys, h // G] += torch.einsum("bij,bid->bjd", w, g)
+    return dq, dk, dv
+
+
+def _cached(s, which, b, h, keys):
+    """Values of the given positions of a sequence, 64 bits."""
+    codes, scale = s[which + "c"], s[which + "s"]
+    p = s["table"][b].long()[keys // s["page"]]
+    return codes[p, keys % s["page"], h].double() * scale[p, h].double()[:, None]
+
+
+def _exact_rows(s, b):
+    """(keys that some row of sequence b sees, which of them each row does not)."""
+    st, S = int(s["start"][b]), s["S"]
+    i = torch.arange(st, st + S, device=DEV)[:, None]
+    if s["op"] == "paged_window":
+        keys = sorted(set(range(min(s["sinks"], st + S))) | set(range(max(0, st - s["window"] + 1), st + S)))
+        keys = torch.tensor(keys, device=DEV)
+        return keys, (keys > i) | ((keys >= s["sinks"]) & (keys <= i - s["window"]))
+    keys = torch.arange(st + S, device=DEV)
+    if s["op"] == "tree":
+        hidden = torch.zeros((S, st + S), dtype=torch.bool, device=DEV)
+        hidden[:, st:] = ~s["sees"][b]
+        return keys, hidden
+    return keys, keys > i
+
+
+def _exact_paged(s):
+    B, S, Hq, Hkv, D = (s[n] for n in ("B", "S", "Hq", "Hkv", "D"))
+    G = Hq // Hkv
+    o = torch.empty((B, S, Hq, D), dtype=torch.float64, device=DEV)
+    lse = torch.empty((B, Hq, S), dtype=torch.float64, device=DEV)
+    for b in range(B):
+        keys, hidden = _exact_rows(s, b)
+        for h in range(Hkv):
+            k, v = _cached(s, "k", b, h, keys), _cached(s, "v", b, h, keys)
+            a = torch.einsum("sgd,ld->gsl", s["q"][b, :, h * G:(h + 1) * G].double(), k) / math.sqrt(D)
+            a[:, hidden] = -math.inf
+            z = torch.logsumexp(a, -1)
+            o[b, :, h * G:(h + 1) * G] = torch.einsum("gsl,ld->sgd", (a - z[..., None]).exp(), v)
+            lse[b, h * G:(h + 1) * G] = z
+    return o, lse
+
+
+def _exact_weights(s):
+    G, D = s["Hq"] // s["Hkv"], s["D"]
+    out = s["out"].double()
+    for b in range(s["B"]):
+        keys, hidden = _exact_rows(s, b)
+        st = int(s["start"][b])
+        for h in range(s["Hkv"]):
+            a = torch.einsum("sgd,ld->gsl", s["q"][b, :, h * G:(h + 1) * G].double(), _cached(s, "k", b, h, keys))
+            a = (a / math.sqrt(D) - s["lse"][b, h * G:(h + 1) * G, :, None].double()).exp()
+            a[:, hidden] = 0
+            out[b, h, :len(keys)] = a.sum((0, 1))
+            out[b, h, :st] += s["score"][b, h, :st].double()
+    return out
+
+
+def _e4m3(x):
+    """The nearest E4M3 value, ties to the even code, |x| <= 448."""
+    _, e = torch.frexp(x)
+    unit = torch.ldexp(torch.ones_like(x), (e - 4).clamp(min=-9))
+    return torch.round(x / unit) * unit
+
+
+def _exact_evict(s):
+    page, budget = s["page"], s["budget"]
+    kept, score2 = s["kept"].clone(), s["score2"].double()
+    steps = torch.tensor([2.0 ** e for e in range(-60, 61)], dtype=torch.float64, device=DEV)
+    out = {n: s[n].double() for n in ("kc", "vc", "ks", "vs")}
+    for b, n in enumerate(s["start"].tolist()):
+        for h in range(s["Hkv"]):
+            if n <= budget:
+                pick = torch.arange(n, device=DEV)
+            else:
+                x = s["score"][b, h, s["sinks"]:n - s["recent"]].cpu()
+                room = budget - s["sinks"] - s["recent"]
+                order = sorted(range(len(x)), key=dict(enumerate((-x).tolist())).__getitem__)[:room]   # (stable)
+                middle = torch.tensor(sorted(order), dtype=torch.int64) + s["sinks"]
+                pick = torch.cat([torch.arange(s["sinks"]), middle, torch.arange(n - s["recent"], n)]).to(DEV)
+            m = len(pick)
+            kept[b, h, :m] = pick.to(torch.int32)
+            score2[b, h, :m] = s["score"][b, h, pick].double()
+            for which in ("k", "v"):
+                x = _cached(s, which, b, h, pick)
+                for p in range(-(-m // page)):
+                    rows = x[p * page:(p + 1) * page]
+                    to = int(s["table2"][b, p])
+                    # the first of 2^-60, 2^-59 .. whose largest code's value reaches the largest of the rows
+                    scale = steps[torch.searchsorted(E4M3_MAX * steps, rows.abs().amax()).clamp(max=120)]
+                    out[which + "s"][to, h] = scale
+                    out[which + "c"][to, :len(rows), h] = _e4m3(rows / scale)
+    return kept, score2, out["kc"], out["vc"], out["ks"], out["vs"]
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    return {"window": _exact_window, "window_bwd": _exact_window_bwd, "paged_window": _exact_paged, "tree": _exact_paged,
+            "weights": _exact_weights, "evict": _exact_evict}[case["op"]](s)
+
+
+# --------------------------------------------------------------------- work --
+
+def _window_pairs(first, n, window, sinks):
+    """Keys seen by rows first .. first + n - 1, summed, and how many different keys those are."""
+    total = 0
+    for i in range(first, first + n):
+        w = min(i + 1, window)
+        total += w + min(sinks, i + 1 - w)
+    w = min(first + n, window + n - 1)
+    return total, w + min(sinks, first + n - w)
+
+
+def work(case):
+    B, Hkv, D = case["B"], case["Hkv"], case["D"]
+    op = case["op"]
+    if op in ("window", "window_bwd"):
+        S, Hq = case["S"], case["Hq"]
+        pairs, _ = _window_pairs(0, S, case["window"], case["sinks"])
+        q, k = 2 * B * S * Hq * D, 2 * B * S * Hkv * D
+        if op == "window":
+            return {"bytes": 2 * q + 2 * k + 4 * B * Hq * S, "flops": 4 * B * Hq * pairs * D}
+        return {"bytes": 4 * q + 4 * k + 4 * B * Hq * S, "flops": 10 * B * Hq * pairs * D}
+    start, count = _lengths(case, 0)
+    page = case["page"]
+    if op == "evict":
+        keys = [min(n, case["budget"]) for n in start.tolist()]
+        pages = sum(-(-n // page) for n in keys)
+        cut = sum(n for n in start.tolist() if n > case["budget"])
+        # scores of the sequences that are cut, the kept ones' numbers and scores, their codes in and out, scales
+        return {"bytes": Hkv * (4 * cut + 12 * sum(keys) + 4 * sum(keys) * D + 32 * pages) + 8 * pages + 4 * B,
+                "flops": 4 * Hkv * sum(keys) * D}
+    S, Hq = case["S"], case["Hq"]
+    ends = (start + count).tolist()
+    pairs, keys = 0, 0
+    for a, n in zip(start.tolist(), ends):
+        if op == "paged_window":
+            p, u = _window_pairs(a, S, case["window"], case["sinks"])
+            pairs, keys = pairs + p, keys + u
+        else:
+            pairs += S * a + (S * (S + 1)) // 2
+            keys += n
+    pages = -(-keys // page)
+    if op == "weights":
+        return {"bytes": keys * Hkv * (D + 8) + pages * (4 + 4 * Hkv) + 2 * B * S * Hq * D + 4 * B * S * Hq,
+                "flops": 2 * pairs * Hq * D}
+    mask = 4 * B * S * -(-S // 32) if op == "tree" else 0
+    return {"bytes": 2 * keys * Hkv * D + pages * (4 + 8 * Hkv) + 4 * B * S * Hq * D + 4 * B * S * Hq + mask,
+            "flops": 4 * pairs * Hq * D}
