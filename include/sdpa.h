@@ -239,6 +239,32 @@ sdpa_status_t sdpa_bwd(const void *Q, const void *K, const void *V, const void *
 size_t sdpa_bwd_workspace_bytes(int B, int Hq, int Sq, int D);
 
 /*
+ * Attention with a sliding window and a few first keys that stay visible, and
+ * its gradient: row i sees the keys j <= i with j > i - window or j < sinks
+ * (top-left aligned like the causal mask; a window of Sq or more with any sinks
+ * is the causal mask).  The key tiles that no row of a query tile sees are not
+ * read.
+ *   window    >= 1.
+ *   sinks     >= 0.
+ * A row that sees no key (with Sq > Skv) has O = 0 and LSE = -infinity, and no
+ * part in the gradients.  Other arguments, numbers and statuses as for
+ * sdpa_fwd_ex and sdpa_bwd (whose workspace bytes they are).  As there, a key
+ * or value that is not finite reaches every row of the query tiles that meet
+ * its key tile (0 times infinity is NaN), rows that do not see it included.
+ */
+sdpa_status_t sdpa_fwd_window(const void *Q, const void *K, const void *V, void *O, float *LSE,
+                              int B, int Hq, int Hkv, int Sq, int Skv, int D,
+                              const sdpa_layout_t *q_layout, const sdpa_layout_t *k_layout,
+                              const sdpa_layout_t *v_layout, const sdpa_layout_t *o_layout,
+                              float scale, int window, int sinks, sdpa_dtype_t dtype, void *stream);
+
+sdpa_status_t sdpa_bwd_window(const void *Q, const void *K, const void *V, const void *O, const void *dO,
+                              const float *LSE, void *dQ, void *dK, void *dV,
+                              int B, int Hq, int Hkv, int Sq, int Skv, int D,
+                              float scale, int window, int sinks, sdpa_dtype_t dtype,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * FP8 backward pass (section 10 of the codelab, "FP8": E4M3 tensors in the
  * forward pass, E5M2 for the backward pass), contiguous BSHD, D 64 or 128:
  * the gradients of sum(dO * O) for O = sdpa_fwd_fp8(Q, K, V), every GEMM on
@@ -477,7 +503,8 @@ int sdpa_last_cuda_error(void);
 sdpa_status_t sdpa_device_error(unsigned int *code);
 
 /* Version of this ABI (bumped on any change; 2 added the *_ex entry points, 3 the decode pass,
- * 4 the backward pass, 5 the FP8 backward pass, 6 the norm and rotation, the paged cache and its attention). */
+ * 4 the backward pass, 5 the FP8 backward pass, 6 the norm and rotation, the paged cache and its attention,
+ * 7 windows and trees, key weights and eviction). */
 int sdpa_abi_version(void);
 
 #ifdef __cplusplus

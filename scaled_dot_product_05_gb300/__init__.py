@@ -19,7 +19,8 @@ __all__ = ["sdpa_fwd", "sdpa_fwd_fp8", "sdpa_fwd_ex", "sdpa_fwd_fp8_ex", "sdpa_f
            "sdpa_bwd", "bwd_workspace_bytes", "sdpa_bwd_fp8", "bwd_fp8_workspace_bytes",
            "decode_workspace_bytes", "sdpa_status_string", "sdpa_device_error", "SdpaError", "lib",
            "rope_table", "sdpa_qk_norm_rope", "sdpa_qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_bytes",
-           "PagedCache", "sdpa_cache_append", "sdpa_fwd_paged", "paged_workspace_bytes"]
+           "PagedCache", "sdpa_cache_append", "sdpa_fwd_paged", "paged_workspace_bytes",
+           "sdpa_fwd_window", "sdpa_bwd_window"]
 
 _DTYPE = {torch.bfloat16: _abi.SDPA_DTYPE_BF16, torch.float16: _abi.SDPA_DTYPE_FP16}
 
@@ -326,3 +327,4 @@ def sdpa_device_error() -> int:
 
 from .cache import (PagedCache, paged_workspace_bytes, qk_norm_rope_bwd_workspace_bytes, rope_table,  # noqa: E402
                     sdpa_cache_append, sdpa_fwd_paged, sdpa_qk_norm_rope, sdpa_qk_norm_rope_bwd)
+from .masked import sdpa_bwd_window, sdpa_fwd_window  # noqa: E402

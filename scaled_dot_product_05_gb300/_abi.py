@@ -17,7 +17,7 @@ EXPORTS = ("sdpa_fwd", "sdpa_fwd_fp8", "sdpa_fwd_ex", "sdpa_fwd_fp8_ex", "sdpa_f
            "sdpa_fwd_decode_noalloc", "sdpa_decode_workspace_bytes", "sdpa_bwd", "sdpa_bwd_workspace_bytes", "sdpa_bwd_fp8", "sdpa_bwd_fp8_workspace_bytes", "sdpa_status_string", "sdpa_last_cuda_error", "sdpa_device_error",
            "sdpa_abi_version",
            "sdpa_qk_norm_rope", "sdpa_qk_norm_rope_bwd", "sdpa_qk_norm_rope_bwd_workspace_bytes", "sdpa_cache_append",
-           "sdpa_fwd_paged", "sdpa_paged_workspace_bytes")
+           "sdpa_fwd_paged", "sdpa_paged_workspace_bytes", "sdpa_fwd_window", "sdpa_bwd_window")
 
 
 class Layout(ctypes.Structure):
@@ -66,6 +66,10 @@ def _bind(lib):
     lib.sdpa_fwd_decode_noalloc.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, lp, lp, lp, lp, f, i, vp]
     lib.sdpa_bwd.restype = i
     lib.sdpa_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, vp, ctypes.c_size_t, vp]
+    lib.sdpa_fwd_window.restype = i
+    lib.sdpa_fwd_window.argtypes = [vp] * 5 + [i] * 6 + [lp] * 4 + [f, i, i, i, vp]
+    lib.sdpa_bwd_window.restype = i
+    lib.sdpa_bwd_window.argtypes = [vp] * 9 + [i] * 6 + [f, i, i, i, vp, ctypes.c_size_t, vp]
     lib.sdpa_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.sdpa_bwd_workspace_bytes.argtypes = [i, i, i, i]
     lib.sdpa_bwd_fp8.restype = i

@@ -12,9 +12,9 @@ LIB_PATH = os.path.join(BUILD_DIR, "libsdpa_gb300.so")
 # the same sources built with -DSDPA_WAIT_TEST: a test-only library whose wait
 # limit and one withheld K copy are set from the host (bounded-wait tests)
 WAIT_TEST_LIB_PATH = os.path.join(BUILD_DIR, "libsdpa_gb300_waittest.so")
-SOURCES = ["sdpa_api.cu"]
+SOURCES = ["sdpa_api.cu", "sdpa_cache.cu"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
-              "-Xcompiler", "-fPIC", "-shared"]
+              "-Xcompiler", "-fPIC"]
 
 
 def headers():
@@ -43,10 +43,21 @@ def _compile(path: str, extra, verbose: bool) -> str:
     if not os.path.exists(nvcc):
         nvcc = "nvcc"
     tmp = path + f".tmp{os.getpid()}"
-    cmd = [nvcc, *NVCC_FLAGS, *extra, *(["-Xptxas", "-v"] if verbose else []), "-o", tmp,
-           *[os.path.join(CSRC, f) for f in SOURCES]]
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, path)
+    flags = [*NVCC_FLAGS, *extra, *(["-Xptxas", "-v"] if verbose else [])]
+    # the sources side by side, then one link
+    objs = [f"{tmp}.{i}.o" for i in range(len(SOURCES))]
+    try:
+        runs = [subprocess.Popen([nvcc, *flags, "-c", "-o", obj, os.path.join(CSRC, src)])
+                for obj, src in zip(objs, SOURCES)]
+        codes = [r.wait() for r in runs]
+        if any(codes):
+            raise subprocess.CalledProcessError(max(codes, key=abs), [nvcc, *flags])
+        subprocess.run([nvcc, *flags, "-shared", "-o", tmp, *objs], check=True)
+        os.replace(tmp, path)
+    finally:
+        for f in objs:
+            if os.path.exists(f):
+                os.remove(f)
     return path
 
 

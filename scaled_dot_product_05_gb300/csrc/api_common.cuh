@@ -1,0 +1,163 @@
+// api_common.cuh -- what the C entry points share: sizes, strides and their
+// checks, tensor maps, launches.  The library is compiled as two object files
+// (sdpa_api.cu: attention over tensors; sdpa_cache.cu: everything around the
+// paged cache); what has state is defined in the first.
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+#include <utility>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "../../include/sdpa.h"
+#include "sdpa_kernel.cuh"
+
+namespace sdpa_host {
+
+// Element strides of a [B][S][H][D] tensor (D contiguous).
+struct Strides {
+    long long b, s, h;
+};
+
+}  // namespace sdpa_host
+
+namespace {
+
+using sdpa_host::Strides;
+
+constexpr int kMaxDevices = 64;
+
+bool aligned16(const void* p)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+}
+
+bool overlaps(const void* a, long long na, const void* b, long long nb)
+{
+    const unsigned __int128 a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    return a0 < b0 + (unsigned long long)nb && b0 < a0 + (unsigned long long)na;
+}
+
+Strides contiguous_bshd(int S, int H, int D)
+{
+    return {static_cast<long long>(S) * H * D, static_cast<long long>(H) * D, D};
+}
+
+Strides resolve(const sdpa_layout_t* l, int S, int H, int D)
+{
+    return l ? Strides{l->batch, l->seq, l->head} : contiguous_bshd(S, H, D);
+}
+
+// Bytes from the first element to one past the last one of a B x S x H x D
+// tensor with strides st (all strides > 0), or -1 past 2^62 bytes.
+long long span_bytes(const Strides& st, int B, int S, int H, int D, int elem_bytes)
+{
+    const __int128 last = (__int128)(B - 1) * st.b + (__int128)(S - 1) * st.s + (__int128)(H - 1) * st.h + D;
+    const __int128 bytes = last * elem_bytes;
+    return bytes > ((__int128)1 << 62) ? -1 : static_cast<long long>(bytes);
+}
+
+// A stride the TMA engine and the 16-byte output stores accept: > 0, a
+// multiple of 16 bytes, below 2^40 bytes.
+bool stride_ok(long long st, int elem_bytes)
+{
+    if (st <= 0 || st > (1ll << 40) / elem_bytes)
+        return false;
+    return (st * elem_bytes) % 16 == 0;
+}
+
+bool strides_ok(const Strides& st, int elem_bytes)
+{
+    return stride_ok(st.b, elem_bytes) && stride_ok(st.s, elem_bytes) && stride_ok(st.h, elem_bytes);
+}
+
+// No two (b, s, h, d) of a B x S x H x D tensor share an address: with the
+// dimensions of size > 1 sorted by stride, each stride reaches past the span
+// of the smaller ones (D contiguous comes first).
+bool injective(const Strides& st, int B, int S, int H, int D)
+{
+    long long dims[3][2] = {{st.b, B}, {st.s, S}, {st.h, H}};
+    for (int i = 0; i < 3; ++i)                      // sort by stride
+        for (int j = i + 1; j < 3; ++j)
+            if (dims[j][0] < dims[i][0]) {
+                std::swap(dims[i][0], dims[j][0]);
+                std::swap(dims[i][1], dims[j][1]);
+            }
+    long long reach = D;                             // span of the dimensions so far
+    for (int i = 0; i < 3; ++i) {
+        if (dims[i][1] == 1)
+            continue;
+        if (dims[i][0] < reach)
+            return false;
+        reach = dims[i][0] * (dims[i][1] - 1) + reach;
+    }
+    return true;
+}
+
+bool aligned(const void* p, unsigned bytes)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+
+bool valid_scale(float x)
+{
+    return std::isfinite(x) && x > 0.f;
+}
+
+// Launches `kernel`, with programmatic stream serialization when `pdl`: it
+// may then start while the previous kernel in the stream finishes.  Every
+// kernel launched here executes griddepcontrol.wait before touching global
+// memory (a no-op in a plain launch), so it sees everything the previous
+// kernel wrote and does not overwrite what that kernel still reads.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(bool pdl, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                       Args&&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Reads and clears this object file's device error word.
+cudaError_t take_error_word(unsigned int* code)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(code, sdpa::g_sdpa_error, sizeof *code);
+    const unsigned int zero = 0;
+    return e != cudaSuccess ? e : cudaMemcpyToSymbol(sdpa::g_sdpa_error, &zero, sizeof zero);
+}
+
+}  // namespace
+
+namespace sdpa_host {
+
+// Keeps the error for sdpa_last_cuda_error.
+sdpa_status_t cuda_fail(cudaError_t e);
+
+// The current device and its SMs; on its first use there, the architecture
+// check and the attributes of the attention kernels.
+sdpa_status_t device_ready(int* dev_out, int* sm_count);
+
+// A tensor map of a [B][S][H][D] tensor, box_h x box_s (heads x rows) per
+// copy: 1 x 128, or G x 128 / G for packed query tiles.
+bool make_map(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int elem_bytes, int D, int H, int S, int B,
+              const Strides& st, int box_h = 1, int box_s = sdpa::kBlockM,
+              CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+
+cudaError_t take_cache_error(unsigned int* code);
+
+}  // namespace sdpa_host
+
+using sdpa_host::cuda_fail;
+using sdpa_host::device_ready;
+using sdpa_host::make_map;

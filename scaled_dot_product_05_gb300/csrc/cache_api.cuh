@@ -1,10 +1,11 @@
 // cache_api.cuh -- C ABI of the norm / rotation, cache append and cached
-// attention calls: argument checks and launches.  Included by sdpa_api.cu
-// after its helpers.
+// attention calls: argument checks and launches.
 #pragma once
 
+#include <mutex>
 #include <type_traits>
 
+#include "api_common.cuh"
 #include "cache_append.cuh"
 #include "paged_attn.cuh"
 #include "paged_wide.cuh"

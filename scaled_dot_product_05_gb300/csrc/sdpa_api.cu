@@ -3,10 +3,12 @@
 //
 // Every check runs before the first CUDA call, so a rejected call enqueues
 // nothing.  Nothing here allocates device memory.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 #include <vector>
 #include <utility>
 
@@ -14,14 +16,25 @@
 #include <cuda_runtime.h>
 
 #include "../../include/sdpa.h"
+#include "api_common.cuh"
 #include "sdpa_kernel.cuh"
 #include "sdpa_bwd.cuh"
 #include "sdpa_bwd_prep.cuh"
 #include "sdpa_bwd_fp8.cuh"
 
-namespace {
+namespace sdpa_host {
 
 thread_local int t_last_cuda_error = 0;
+
+sdpa_status_t cuda_fail(cudaError_t e)
+{
+    t_last_cuda_error = static_cast<int>(e);
+    return SDPA_ERR_CUDA;
+}
+
+}  // namespace sdpa_host
+
+namespace {
 
 // Scratch of sdpa_fwd_decode_noalloc: a file-scope device array (one instance
 // per device, allocated with the module, never by a call; every process that
@@ -34,14 +47,6 @@ thread_local int t_last_cuda_error = 0;
 // it must not overlap in time (same stream, or otherwise ordered).
 constexpr size_t kDecodeScratchBytes = size_t(32) << 20;
 static __device__ __align__(256) float g_decode_scratch[kDecodeScratchBytes / sizeof(float)];
-
-sdpa_status_t cuda_fail(cudaError_t e)
-{
-    t_last_cuda_error = static_cast<int>(e);
-    return SDPA_ERR_CUDA;
-}
-
-constexpr int kMaxDevices = 64;
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -75,17 +80,17 @@ struct DeviceState {
 };
 DeviceState g_dev[kMaxDevices];
 
-template <int D, int KIND, bool kPacked = false, int QT = 2>
+template <int D, int KIND, bool kPacked = false, int QT = 2, bool kWin = false>
 cudaError_t set_attrs()
 {
-    return cudaFuncSetAttribute(sdpa::sdpa_fwd_kernel<D, KIND, kPacked, QT>,
+    return cudaFuncSetAttribute(sdpa::sdpa_fwd_kernel<D, KIND, kPacked, QT, kWin>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, sdpa::Layout<D, KIND, QT>::kSmemBytes);
 }
 
-template <int D, int KIND>
+template <int D, int KIND, bool kWin = false>
 cudaError_t set_bwd_attrs()
 {
-    return cudaFuncSetAttribute(sdpa::bwd::sdpa_bwd_kernel<D, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(sdpa::bwd::sdpa_bwd_kernel<D, KIND, kWin>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 sdpa::bwd::BwdLayout<D>::kSmemBytes);
 }
 
@@ -95,6 +100,10 @@ cudaError_t set_bwd8_attrs()
     return cudaFuncSetAttribute(sdpa::bwd8::sdpa_bwd_fp8_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 sdpa::bwd8::Layout<D>::kSmemBytes);
 }
+
+}  // namespace
+
+namespace sdpa_host {
 
 sdpa_status_t device_ready(int* dev_out, int* sm_count)
 {
@@ -132,7 +141,14 @@ sdpa_status_t device_ready(int* dev_out, int* sm_count)
                             set_attrs<128, sdpa::kBF16, true>(), set_attrs<128, sdpa::kFP16, true>(),
                             set_bwd_attrs<64, sdpa::kBF16>(),    set_bwd_attrs<64, sdpa::kFP16>(),
                             set_bwd_attrs<128, sdpa::kBF16>(),   set_bwd_attrs<128, sdpa::kFP16>(),
-                            set_bwd8_attrs<64>(),                set_bwd8_attrs<128>()};
+                            set_bwd8_attrs<64>(),                set_bwd8_attrs<128>(),
+                            set_attrs<32, sdpa::kBF16, false, 1, true>(), set_attrs<32, sdpa::kFP16, false, 1, true>(),
+                            set_attrs<64, sdpa::kBF16, false, 1, true>(), set_attrs<64, sdpa::kFP16, false, 1, true>(),
+                            set_attrs<32, sdpa::kBF16, false, 2, true>(), set_attrs<32, sdpa::kFP16, false, 2, true>(),
+                            set_attrs<64, sdpa::kBF16, false, 2, true>(), set_attrs<64, sdpa::kFP16, false, 2, true>(),
+                            set_attrs<128, sdpa::kBF16, false, 2, true>(), set_attrs<128, sdpa::kFP16, false, 2, true>(),
+                            set_bwd_attrs<64, sdpa::kBF16, true>(), set_bwd_attrs<64, sdpa::kFP16, true>(),
+                            set_bwd_attrs<128, sdpa::kBF16, true>(), set_bwd_attrs<128, sdpa::kFP16, true>()};
         for (cudaError_t x : es)
             if (x != cudaSuccess && st.err == cudaSuccess)
                 st.err = x;
@@ -145,6 +161,10 @@ sdpa_status_t device_ready(int* dev_out, int* sm_count)
     *sm_count = st.sm_count;
     return SDPA_OK;
 }
+
+}  // namespace sdpa_host
+
+namespace {
 
 // Device address of the current device's g_decode_scratch.  In host code
 // the array's name is only a host-side stand-in, so the address is looked up
@@ -160,86 +180,9 @@ sdpa_status_t decode_scratch(int dev, void** out)
     return SDPA_OK;
 }
 
-bool aligned16(const void* p)
-{
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
-}
-
-bool overlaps(const void* a, long long na, const void* b, long long nb)
-{
-    const unsigned __int128 a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + (unsigned long long)nb && b0 < a0 + (unsigned long long)na;
-}
-
 struct Shape {
     int B, Hq, Hkv, Sq, Skv, D;
 };
-
-// Element strides of a [B][S][H][D] tensor (D contiguous).
-struct Strides {
-    long long b, s, h;
-};
-
-Strides contiguous_bshd(int S, int H, int D)
-{
-    return {static_cast<long long>(S) * H * D, static_cast<long long>(H) * D, D};
-}
-
-Strides resolve(const sdpa_layout_t* l, int S, int H, int D)
-{
-    return l ? Strides{l->batch, l->seq, l->head} : contiguous_bshd(S, H, D);
-}
-
-// Bytes from the first element to one past the last one of a B x S x H x D
-// tensor with strides st (all strides > 0), or -1 past 2^62 bytes.
-long long span_bytes(const Strides& st, int B, int S, int H, int D, int elem_bytes)
-{
-    const __int128 last = (__int128)(B - 1) * st.b + (__int128)(S - 1) * st.s + (__int128)(H - 1) * st.h + D;
-    const __int128 bytes = last * elem_bytes;
-    return bytes > ((__int128)1 << 62) ? -1 : static_cast<long long>(bytes);
-}
-
-// A stride the TMA engine and the 16-byte output stores accept: > 0, a
-// multiple of 16 bytes, below 2^40 bytes.
-bool stride_ok(long long st, int elem_bytes)
-{
-    if (st <= 0 || st > (1ll << 40) / elem_bytes)
-        return false;
-    return (st * elem_bytes) % 16 == 0;
-}
-
-bool strides_ok(const Strides& st, int elem_bytes)
-{
-    return stride_ok(st.b, elem_bytes) && stride_ok(st.s, elem_bytes) && stride_ok(st.h, elem_bytes);
-}
-
-// No two (b, s, h, d) of a B x S x H x D tensor share an address: with the
-// dimensions of size > 1 sorted by stride, each stride reaches past the span
-// of the smaller ones (D contiguous comes first).
-bool injective(const Strides& st, int B, int S, int H, int D)
-{
-    long long dims[3][2] = {{st.b, B}, {st.s, S}, {st.h, H}};
-    for (int i = 0; i < 3; ++i)                      // sort by stride
-        for (int j = i + 1; j < 3; ++j)
-            if (dims[j][0] < dims[i][0]) {
-                std::swap(dims[i][0], dims[j][0]);
-                std::swap(dims[i][1], dims[j][1]);
-            }
-    long long reach = D;                             // span of the dimensions so far
-    for (int i = 0; i < 3; ++i) {
-        if (dims[i][1] == 1)
-            continue;
-        if (dims[i][0] < reach)
-            return false;
-        reach = dims[i][0] * (dims[i][1] - 1) + reach;
-    }
-    return true;
-}
-
-bool aligned(const void* p, unsigned bytes)
-{
-    return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
-}
 
 struct Args {
     const void *Q, *K, *V;
@@ -288,11 +231,6 @@ sdpa_status_t check_common(const Args& a, int in_elem_bytes, int out_elem_bytes)
             return SDPA_ERR_ALIAS;
     }
     return SDPA_OK;
-}
-
-bool valid_scale(float x)
-{
-    return std::isfinite(x) && x > 0.f;
 }
 
 // 4-D tensor map over a [B][S][H][D] tensor with element strides st: dims
@@ -359,11 +297,12 @@ uint64_t map_key_hash(const MapKey& k)
     return h ^ (h >> 32);
 }
 
-// box_h x box_s (heads x rows) per copy: 1 x 128, or G x 128 / G for packed
-// query tiles.
+}  // namespace
+
+namespace sdpa_host {
+
 bool make_map(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int elem_bytes, int D, int H, int S, int B,
-              const Strides& st, int box_h = 1, int box_s = sdpa::kBlockM,
-              CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B)
+              const Strides& st, int box_h, int box_s, CUtensorMapL2promotion promotion)
 {
     MapKey k;
     std::memset(&k, 0, sizeof k);                    // padding bytes take part in the comparison
@@ -405,30 +344,11 @@ bool make_map(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int el
     return true;
 }
 
-// Launches `kernel`, with programmatic stream serialization when `pdl`: it
-// may then start while the previous kernel in the stream finishes.  Every
-// kernel launched here executes griddepcontrol.wait before touching global
-// memory (a no-op in a plain launch), so it sees everything the previous
-// kernel wrote and does not overwrite what that kernel still reads.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(bool pdl, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                       Args&&... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-    return e != cudaSuccess ? e : cudaGetLastError();
-}
+}  // namespace sdpa_host
 
-template <int D, int KIND, bool kPacked = false, int QT = 2>
+namespace {
+
+template <int D, int KIND, bool kPacked = false, int QT = 2, bool kWin = false>
 cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
                    const sdpa::Params& p, int sm_count, cudaStream_t stream)
 {
@@ -438,7 +358,7 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
     const long long slots = static_cast<long long>(sm_count) * R::kCtasPerSm;
     const unsigned grid = static_cast<unsigned>(p.n_units < slots ? p.n_units : slots);
     // the CTAs may start their prologue while the previous kernel finishes
-    cudaError_t e = launch_pdl(true, sdpa::sdpa_fwd_kernel<D, KIND, kPacked, QT>, dim3(grid), dim3(R::kThreads),
+    cudaError_t e = launch_pdl(true, sdpa::sdpa_fwd_kernel<D, KIND, kPacked, QT, kWin>, dim3(grid), dim3(R::kThreads),
                                sdpa::Layout<D, KIND, QT>::kSmemBytes, stream, tq, tk, tv, to, p);
     if constexpr (kPacked) {
         if (e == cudaSuccess && p.part_o) {
@@ -515,10 +435,28 @@ cudaError_t launch_kind(int D, int qt, const CUtensorMap& tq, const CUtensorMap&
                    : launch<128, KIND>(tq, tk, tv, to, p, sm_count, stream);
 }
 
+template <int KIND>
+cudaError_t launch_window(int D, int qt, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                          const CUtensorMap& to, const sdpa::Params& p, int sm_count, cudaStream_t stream)
+{
+    if (D == 128)
+        return launch<128, KIND, false, 2, true>(tq, tk, tv, to, p, sm_count, stream);
+    if (D == 64)
+        return qt == 1 ? launch<64, KIND, false, 1, true>(tq, tk, tv, to, p, sm_count, stream)
+                       : launch<64, KIND, false, 2, true>(tq, tk, tv, to, p, sm_count, stream);
+    return qt == 1 ? launch<32, KIND, false, 1, true>(tq, tk, tv, to, p, sm_count, stream)
+                   : launch<32, KIND, false, 2, true>(tq, tk, tv, to, p, sm_count, stream);
+}
+
+// A sliding window and first tokens that stay visible (window 0: no window).
+struct Window {
+    int window, sinks;
+};
+
 // The forward pass for already resolved arguments: checks, tensor maps,
 // launch.  `descales` is null for 16-bit kinds.
 sdpa_status_t run(const Args& a, float scale, const float* descales, int causal, sdpa_dtype_t dtype,
-                  void* stream)
+                  void* stream, Window win = {0, 0})
 {
     const bool fp8 = dtype == SDPA_DTYPE_E4M3;
     const int in_bytes = fp8 ? 1 : 2;
@@ -560,9 +498,14 @@ sdpa_status_t run(const Args& a, float scale, const float* descales, int causal,
         return cuda_fail(cudaErrorInvalidValue);
 
     const int qt = fwd_q_tiles(fp8, s, sm_count);
-    const sdpa::Params p = make_params(a, score_scale, out_scale, causal, qt * sdpa::kBlockM);
+    sdpa::Params p = make_params(a, score_scale, out_scale, causal, qt * sdpa::kBlockM);
+    p.window = win.window < s.Sq ? win.window : s.Sq;          // (a wider one sees no more)
+    p.sinks = win.sinks < s.Skv ? win.sinks : s.Skv;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = fp8 ? launch_kind<sdpa::kE4M3>(s.D, qt, tq, tk, tv, to, p, sm_count, cs)
+    const cudaError_t e = win.window ? (dtype == SDPA_DTYPE_BF16
+                                            ? launch_window<sdpa::kBF16>(s.D, qt, tq, tk, tv, to, p, sm_count, cs)
+                                            : launch_window<sdpa::kFP16>(s.D, qt, tq, tk, tv, to, p, sm_count, cs))
+                        : fp8 ? launch_kind<sdpa::kE4M3>(s.D, qt, tq, tk, tv, to, p, sm_count, cs)
                         : dtype == SDPA_DTYPE_BF16 ? launch_kind<sdpa::kBF16>(s.D, qt, tq, tk, tv, to, p, sm_count, cs)
                                                    : launch_kind<sdpa::kFP16>(s.D, qt, tq, tk, tv, to, p, sm_count, cs);
     if (e != cudaSuccess)
@@ -691,20 +634,24 @@ size_t bwd_workspace(int B, int Hq, int Sq, int D)
 // launch latency and prologue are a visible share.  Measured against plain
 // launches: causal MHA B=4 H=16 S=1024 D=64 (15 per SM) +10 %; causal GQA
 // S=4096 D=128 (222 per SM) -3.5 %, so long calls launch plainly.
-bool bwd_short_call(const Shape& s, bool causal, int sm_count)
+bool bwd_short_call(const Shape& s, bool causal, int sm_count, Window win = {0, 0})
 {
     const long long n_qt = (s.Sq + sdpa::kBlockM - 1) / sdpa::kBlockM;
     const long long n_kt = (s.Skv + sdpa::kBlockN - 1) / sdpa::kBlockN;
     long long per_head = n_qt * n_kt;
     if (causal) {                    // query tile qt meets key tiles 0..qt
         per_head = 0;
-        for (long long kt = 0; kt < n_kt; ++kt)
-            per_head += n_qt > kt ? n_qt - kt : 0;
+        for (long long kt = 0; kt < n_kt; ++kt) {
+            long long end = n_qt;
+            if (win.window && kt * sdpa::kBlockN >= win.sinks)
+                end = std::min(n_qt, (kt * sdpa::kBlockN + sdpa::kBlockN + win.window - 2) / sdpa::kBlockM + 1);
+            per_head += end > kt ? end - kt : 0;
+        }
     }
     return static_cast<long long>(s.B) * s.Hq * per_head <= 64LL * sm_count;
 }
 
-template <int D, int KIND>
+template <int D, int KIND, bool kWin>
 cudaError_t launch_bwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
                        const CUtensorMap& tdq, const sdpa::bwd::Params& p, const void* O, const void* dO, void* dQ,
                        bool pdl, cudaStream_t stream)
@@ -719,7 +666,7 @@ cudaError_t launch_bwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
     if (e != cudaSuccess)
         return e;
     const unsigned grid = static_cast<unsigned>(static_cast<long long>(p.B) * p.Hkv * p.n_kt);
-    if ((e = launch_pdl(pdl, sdpa::bwd::sdpa_bwd_kernel<D, KIND>, dim3(grid), dim3(sdpa::bwd::kThreads),
+    if ((e = launch_pdl(pdl, sdpa::bwd::sdpa_bwd_kernel<D, KIND, kWin>, dim3(grid), dim3(sdpa::bwd::kThreads),
                         sdpa::bwd::BwdLayout<D>::kSmemBytes, stream, tq, tk, tv, tdo, tdq, p)) != cudaSuccess)
         return e;
     const long long n = rows * D;
@@ -729,7 +676,7 @@ cudaError_t launch_bwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
 
 sdpa_status_t run_bwd(const void* Q, const void* K, const void* V, const void* O, const void* dO, const float* LSE,
                       void* dQ, void* dK, void* dV, const Shape& s, float scale, int causal, sdpa_dtype_t dtype,
-                      void* ws, size_t ws_bytes, void* stream)
+                      void* ws, size_t ws_bytes, void* stream, Window win = {0, 0})
 {
     if (dtype != SDPA_DTYPE_BF16 && dtype != SDPA_DTYPE_FP16)
         return SDPA_ERR_DTYPE;
@@ -796,14 +743,20 @@ sdpa_status_t run_bwd(const void* Q, const void* K, const void* V, const void* O
     if (static_cast<long long>(s.B) * s.Hkv * p.n_kt > INT32_MAX)
         return SDPA_ERR_BAD_SHAPE;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const bool pdl = bwd_short_call(s, causal != 0, sm_count);
-    cudaError_t e;
-    if (dtype == SDPA_DTYPE_BF16)
-        e = s.D == 64 ? launch_bwd<64, sdpa::kBF16>(tq, tk, tv, tdo, tdq, p, O, dO, dQ, pdl, cs)
-                      : launch_bwd<128, sdpa::kBF16>(tq, tk, tv, tdo, tdq, p, O, dO, dQ, pdl, cs);
-    else
-        e = s.D == 64 ? launch_bwd<64, sdpa::kFP16>(tq, tk, tv, tdo, tdq, p, O, dO, dQ, pdl, cs)
-                      : launch_bwd<128, sdpa::kFP16>(tq, tk, tv, tdo, tdq, p, O, dO, dQ, pdl, cs);
+    p.window = win.window < s.Sq ? win.window : s.Sq;
+    p.sinks = win.sinks < s.Skv ? win.sinks : s.Skv;
+    const bool pdl = bwd_short_call(s, causal != 0, sm_count, win);
+    auto go = [&](auto kind, auto windowed) {
+        constexpr int KIND = decltype(kind)::value;
+        constexpr bool kWin = decltype(windowed)::value;
+        return s.D == 64 ? launch_bwd<64, KIND, kWin>(tq, tk, tv, tdo, tdq, p, O, dO, dQ, pdl, cs)
+                         : launch_bwd<128, KIND, kWin>(tq, tk, tv, tdo, tdq, p, O, dO, dQ, pdl, cs);
+    };
+    using Bf = std::integral_constant<int, sdpa::kBF16>;
+    using Hf = std::integral_constant<int, sdpa::kFP16>;
+    const bool bf16 = dtype == SDPA_DTYPE_BF16;
+    const cudaError_t e = win.window ? (bf16 ? go(Bf{}, std::true_type{}) : go(Hf{}, std::true_type{}))
+                                     : (bf16 ? go(Bf{}, std::false_type{}) : go(Hf{}, std::false_type{}));
     if (e != cudaSuccess)
         return cuda_fail(e);
     return SDPA_OK;
@@ -940,8 +893,6 @@ Args make_args(const void* Q, const void* K, const void* V, void* O, float* lse,
 
 }  // namespace
 
-#include "cache_api.cuh"
-
 extern "C" {
 
 sdpa_status_t sdpa_fwd(const void* Q, const void* K, const void* V, void* O, int B, int Hq, int Hkv, int Sq,
@@ -1026,6 +977,30 @@ sdpa_status_t sdpa_bwd(const void* Q, const void* K, const void* V, const void* 
                    workspace_bytes, stream);
 }
 
+sdpa_status_t sdpa_fwd_window(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int Hq, int Hkv,
+                              int Sq, int Skv, int D, const sdpa_layout_t* q_layout, const sdpa_layout_t* k_layout,
+                              const sdpa_layout_t* v_layout, const sdpa_layout_t* o_layout, float scale, int window,
+                              int sinks, sdpa_dtype_t dtype, void* stream)
+{
+    if (dtype != SDPA_DTYPE_BF16 && dtype != SDPA_DTYPE_FP16)
+        return SDPA_ERR_DTYPE;
+    if (window < 1 || sinks < 0)
+        return SDPA_ERR_BAD_SHAPE;
+    const Args a = make_args(Q, K, V, O, LSE, B, Hq, Hkv, Sq, Skv, D, q_layout, k_layout, v_layout, o_layout);
+    return run(a, scale, nullptr, 1, dtype, stream, Window{window, sinks});
+}
+
+sdpa_status_t sdpa_bwd_window(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+                              const float* LSE, void* dQ, void* dK, void* dV, int B, int Hq, int Hkv, int Sq, int Skv,
+                              int D, float scale, int window, int sinks, sdpa_dtype_t dtype, void* workspace,
+                              size_t workspace_bytes, void* stream)
+{
+    if (window < 1 || sinks < 0)
+        return SDPA_ERR_BAD_SHAPE;
+    return run_bwd(Q, K, V, O, dO, LSE, dQ, dK, dV, Shape{B, Hq, Hkv, Sq, Skv, D}, scale, 1, dtype, workspace,
+                   workspace_bytes, stream, Window{window, sinks});
+}
+
 sdpa_status_t sdpa_bwd_fp8(const void* Q8, const void* K8, const void* V8, const void* O, const void* dO8,
                            const float* LSE, void* dQ, void* dK, void* dV, int B, int Hq, int Hkv, int Sq, int Skv,
                            int D, float scale, int causal, float descale_q, float descale_k, float descale_v,
@@ -1082,7 +1057,7 @@ const char* sdpa_status_string(sdpa_status_t status)
 
 int sdpa_last_cuda_error(void)
 {
-    return t_last_cuda_error;
+    return sdpa_host::t_last_cuda_error;
 }
 
 sdpa_status_t sdpa_device_error(unsigned int* code)
@@ -1092,21 +1067,20 @@ sdpa_status_t sdpa_device_error(unsigned int* code)
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess)
         return cuda_fail(e);
-    unsigned int v = 0;
-    e = cudaMemcpyFromSymbol(&v, sdpa::g_sdpa_error, sizeof v);
+    // (each object file of the library has a word of its own)
+    unsigned int v = 0, w = 0;
+    e = take_error_word(&v);
+    if (e == cudaSuccess)
+        e = sdpa_host::take_cache_error(&w);
     if (e != cudaSuccess)
         return cuda_fail(e);
-    const unsigned int zero = 0;
-    e = cudaMemcpyToSymbol(sdpa::g_sdpa_error, &zero, sizeof zero);
-    if (e != cudaSuccess)
-        return cuda_fail(e);
-    *code = v;
+    *code = v ? v : w;
     return SDPA_OK;
 }
 
 int sdpa_abi_version(void)
 {
-    return 6;
+    return 7;
 }
 
 #ifdef SDPA_WAIT_TEST

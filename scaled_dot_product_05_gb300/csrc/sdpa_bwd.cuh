@@ -86,6 +86,7 @@ struct Params {
     int B, Hq, Hkv, Sq, Skv, group;
     int n_qt, n_kt;                  // query / key tiles of 128
     int causal;
+    int window, sinks;               // windowed pass: key j is seen by rows j .. j + window - 1, by all from j on if j < sinks
     float scale;
     float scale_log2;                // scale * log2(e)
 };
@@ -156,7 +157,17 @@ __device__ __forceinline__ int bwd_qt0(const Params& p, int kt)
     return p.causal ? kt : 0;
 }
 
-template <int D, int KIND>
+// One behind the last query tile with a row that sees one of its keys.
+template <bool kWin>
+__device__ __forceinline__ int bwd_qt_end(const Params& p, int kt)
+{
+    if (!kWin || kt * kBlockN < p.sinks)
+        return p.n_qt;
+    const long long last = (long long)kt * kBlockN + kBlockN - 1 + p.window - 1;       // the last row that its last key is seen by
+    return (int)min((long long)p.n_qt, last / kBlockM + 1);
+}
+
+template <int D, int KIND, bool kWin = false>
 __global__ void __launch_bounds__(kThreads, 1)
 sdpa_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -187,7 +198,8 @@ sdpa_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     const int hkv = bg % p.Hkv;
     const int b = bg / p.Hkv;
     const int qt0 = bwd_qt0(p, kt);
-    const int n_q = p.n_qt > qt0 ? p.n_qt - qt0 : 0;
+    const int qt_end = bwd_qt_end<kWin>(p, kt);
+    const int n_q = qt_end > qt0 ? qt_end - qt0 : 0;
     const int n_iter = n_q * p.group;            // (head, query tile) pairs, head-major
 
     const uint32_t sK = smem_u32(smem + L::kOffK);
@@ -243,7 +255,7 @@ sdpa_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     // against 1030 and GQA with 4 heads -2 %, which keep the first order)
     const bool heads_inner = p.causal && p.group >= 8;
     auto head_of = [&](int it) { return hkv * p.group + (heads_inner ? it % p.group : it / n_q); };
-    auto qtile_of = [&](int it) { return heads_inner ? p.n_qt - 1 - it / p.group : qt0 + it % n_q; };
+    auto qtile_of = [&](int it) { return heads_inner ? qt_end - 1 - it / p.group : qt0 + it % n_q; };
 
     if (warp < kSoftmaxWarp0) {
       regs_release<kRegsLow>();
@@ -499,6 +511,8 @@ sdpa_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             // top-left causal: this key is visible to query q iff key <= q;
             // keys past Skv are visible to none
             const int first_q = !key_ok ? (1 << 30) : (p.causal ? key - qtile_of(it) * kBlockM : -1);
+            // windowed: and iff q <= key + window - 1, where the key is not one of the first
+            const int end_q = !kWin || !key_ok ? 0 : key < p.sinks ? 1 << 30 : first_q + p.window;
             // phase 1, from S^T alone: P^T, packed over this warpgroup's own
             // S^T columns (already read; the other warpgroup may not have read
             // its own yet): queries 64 sw + 32 chh .. +31 in cols 64 sw + 16 chh ..
@@ -508,6 +522,7 @@ sdpa_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 const int ch = 2 * sw + chh;
                 uint32_t sv[32];
                 tmem_ld32_wait(s_t + 32 * ch, sv);
+                const uint32_t seen_q = kWin ? bits_below(end_q - 32 * ch) & ~bits_below(first_q - 32 * ch) : 0u;
                 uint32_t pk[16];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -516,8 +531,9 @@ sdpa_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int q = 32 * ch + 4 * i + e;
+                        const bool seen = kWin ? seen_q >> (4 * i + e) & 1 : q >= first_q;
                         pf[chh][4 * i + e] =
-                            q >= first_q ? ex2_approx(__uint_as_float(sv[4 * i + e]) * c - lq[e]) : 0.f;
+                            seen ? ex2_approx(__uint_as_float(sv[4 * i + e]) * c - lq[e]) : 0.f;
                     }
                     pk[2 * i] = pack2<kOutBF16>(pf[chh][4 * i], pf[chh][4 * i + 1]);
                     pk[2 * i + 1] = pack2<kOutBF16>(pf[chh][4 * i + 2], pf[chh][4 * i + 3]);

@@ -41,6 +41,7 @@
 // skipped.
 #pragma once
 
+#include <cfloat>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -124,6 +125,7 @@ struct Params {
     int n_pairs;                     // ceil(Sq / 256)
     int n_ktiles;                    // ceil(Skv / 128)
     int causal;
+    int window, sinks;               // windowed pass: row i sees keys i - window + 1 .. i and 0 .. sinks - 1 (up to i)
     float scale_log2;                // scale * log2(e) (* descale_q * descale_k for E4M3)
     float out_scale;                 // descale_v for E4M3, else 1
     // packed (decode) mode only: key tiles per split, splits, and the split
@@ -261,6 +263,12 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity)
     }
 }
 
+// Bits 0 .. n - 1 of a word (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t bits_below(int n)
+{
+    return n >= 32 ? ~0u : (1u << max(n, 0)) - 1u;
+}
+
 // Two floats -> two 16-bit values (round to nearest even), lo in the low half.
 template <bool kToBF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
@@ -282,10 +290,33 @@ struct Unit {
     int kv0;
     int split;                       // packed mode: which key range
     int n_kv[2];                     // key tiles visited by Q tile 0 / 1 (the first n_kv[t]; 0 = tile unused)
+    // windowed pass: the unit's list of key tiles is 0 .. n_first - 1 and then
+    // near, near + 1 ..; Q tile 1 leaves out the `skip` entries after the first
+    int n_first, near, skip;
     // n_kv[t] for a t known only at run time, as a select: an indexed read
     // would put the struct in local memory (measured: FP8 forward +1.6 %,
     // causal MQA S=512 +3.6 %)
     __device__ __forceinline__ int kv(int t) const { return t ? n_kv[1] : n_kv[0]; }
+    // key tile of entry j
+    template <bool kWin>
+    __device__ __forceinline__ int tile(int j) const
+    {
+        if constexpr (kWin)
+            return j < n_first ? j : near + (j - n_first);
+        return kv0 + j;
+    }
+    // Q tile t visits entry j (of its first kv(t))
+    template <bool kWin>
+    __device__ __forceinline__ bool visits(int t, int j) const
+    {
+        return !kWin || t == 0 || j < n_first || j >= n_first + skip;
+    }
+    // the first entry that it visits
+    template <bool kWin>
+    __device__ __forceinline__ int first(int t) const
+    {
+        return kWin && t && n_first == 0 ? skip : 0;
+    }
 };
 
 // Packed (decode) mode: the Hq / Hkv = G query heads that read one KV head are
@@ -293,7 +324,12 @@ struct Unit {
 // head h of the group), so a K/V tile serves every head of the group at once;
 // the key range may be split over several units.  Non-causal only.
 // Unit u -> (KV head, batch, packed-row pair, split), KV head fastest.
-template <bool kPacked, int QT = 2>
+//
+// Windowed pass (kWin): a Q tile with rows a .. a + 127 sees the key tiles from
+// that of key a - window + 1 to the diagonal, and before those the tiles of the
+// first `sinks` keys.  Every tile in use visits one key tile at least (wholly
+// masked, where its rows see none), so that its result is written.
+template <bool kPacked, int QT = 2, bool kWin = false>
 __device__ __forceinline__ Unit decode_unit(const Params& p, int u)
 {
     Unit w;
@@ -322,6 +358,19 @@ __device__ __forceinline__ Unit decode_unit(const Params& p, int u)
     w.b = bh / p.Hq;
     w.hq = bh % p.Hq;
     w.hkv = w.hq / p.group;
+    if constexpr (kWin) {
+        const int qt = w.pair * QT;
+        const int hi0 = min(qt, p.n_ktiles - 1), hi1 = min(qt + QT - 1, p.n_ktiles - 1);
+        const int lo0 = min(max(0, qt * kBlockM - p.window + 1) / kBlockN, hi0);
+        const int lo1 = min(max(0, (qt + QT - 1) * kBlockM - p.window + 1) / kBlockN, hi1);
+        w.n_first = min(p.sinks / kBlockN + (p.sinks % kBlockN != 0), hi1 + 1);
+        w.near = max(lo0, w.n_first);
+        w.skip = max(0, lo1 - w.near);
+        w.n_kv[0] = hi0 < w.n_first ? hi0 + 1 : w.n_first + hi0 - w.near + 1;
+        w.n_kv[1] = QT == 1 ? 0 : hi1 < w.n_first ? hi1 + 1 : w.n_first + hi1 - w.near + 1;
+        w.n = max(w.n_kv[0], w.n_kv[1]);
+        return w;
+    }
     if constexpr (QT == 1) {
         // one Q tile (w.pair is its index): causal rows of tile i see keys
         // below 128 (i + 1)
@@ -385,7 +434,7 @@ __device__ __forceinline__ uint64_t desc_join(uint32_t hi, uint32_t lo)
 // kKeysPerStep keys is kKeysPerStep rows of kSwz bytes, the next chunk of D
 // columns kChunkBytes further (LBO).  The E4M3 P tile and the ones tile have
 // 128-byte rows: one 128-byte swizzle span, 8-row groups 1024 bytes apart.
-template <int D, int KIND, bool kPacked, int NK, int NV, int QT>
+template <int D, int KIND, bool kPacked, int NK, int NV, int QT, bool kWin>
 __device__ __forceinline__ void mma_issue_s(const Params& p, Barriers<NK, NV>* bars, volatile int* abort,
                                             uint32_t tmem, uint32_t sQ, uint32_t sK)
 {
@@ -406,14 +455,14 @@ __device__ __forceinline__ void mma_issue_s(const Params& p, Barriers<NK, NV>* b
             break;
         if (u < 0)
             continue;
-        const Unit w = decode_unit<kPacked, QT>(p, u);
+        const Unit w = decode_unit<kPacked, QT, kWin>(p, u);
         const int n = w.n;
         for (int j = 0; ok && j < n; ++j) {
             ok = wait_bar(smem_u32(&bars->k_full[ck % NK]), (ck / NK) & 1, abort, kErrWaitMma + 3);
             for (int t = 0; ok && t < 2; ++t) {
-                if (j >= w.n_kv[t])
+                if (j >= w.n_kv[t] || !w.visits<kWin>(t, j))
                     continue;
-                if (j == 0)
+                if (j == w.first<kWin>(t))
                     ok = wait_bar(smem_u32(&bars->q_full[t]), ua[t] & 1, abort, kErrWaitMma + 1 + t);
                 // the previous S in this region has been read out of it: the
                 // last S of either tile (shared region) or of this tile
@@ -461,7 +510,7 @@ __device__ __forceinline__ void mma_issue_s(const Params& p, Barriers<NK, NV>* b
 // (K-major, keys contiguous) comes from shared memory, and l_t (+)= P_t x
 // ones.  Every P V thread (QT of them) releases every V slot of the unit
 // (barrier count QT), tile 0 also the causal key tile it does not visit.
-template <int D, int KIND, bool kPacked, int NK, int NV, int QT>
+template <int D, int KIND, bool kPacked, int NK, int NV, int QT, bool kWin>
 __device__ __forceinline__ void mma_issue_pv(const Params& p, Barriers<NK, NV>* bars, volatile int* abort,
                                              uint32_t tmem, uint32_t sV, uint32_t sP, uint32_t sOnes, int t)
 {
@@ -489,19 +538,19 @@ __device__ __forceinline__ void mma_issue_pv(const Params& p, Barriers<NK, NV>* 
             break;
         if (u < 0)
             continue;
-        const Unit w = decode_unit<kPacked, QT>(p, u);
+        const Unit w = decode_unit<kPacked, QT, kWin>(p, u);
         const int n = w.n;
-        const int nt = w.kv(t);
+        const int nt = w.kv(t), first = w.first<kWin>(t);
         for (int j = 0; ok && j < n; ++j, ++cv) {
             ok = wait_bar(smem_u32(&bars->v_full[cv % NV]), (cv / NV) & 1, abort, kErrWaitMma + 5);
             if (!ok)
                 break;
-            if (j >= nt) {               // past this tile's last key tile (or tile unused): release V_j
+            if (j >= nt || !w.visits<kWin>(t, j)) {    // a key tile that this Q tile has no part in: release V_j
                 mbar_arrive(smem_u32(&bars->v_empty[cv % NV]));
                 continue;
             }
             ok = wait_bar(smem_u32(&bars->p_full[t]), npv & 1, abort, kErrWaitMma + 6 + t);
-            if (ok && j == 0 && units > 0)
+            if (ok && j == first && units > 0)
                 ok = wait_bar(smem_u32(&bars->o_empty[t]), (units - 1) & 1, abort, kErrWaitMma + 8 + t);
             if (!ok)
                 break;
@@ -522,7 +571,7 @@ __device__ __forceinline__ void mma_issue_pv(const Params& p, Barriers<NK, NV>* 
 #pragma unroll
             for (int kk = 0; kk < L::kPVSteps; ++kk) {
                 const uint32_t off_v = (uint32_t)((kk * L::kKeysPerStep * L::kSwz) >> 4);
-                const uint32_t acc = (j > 0 || kk > 0) ? 1u : 0u;
+                const uint32_t acc = (j > first || kk > 0) ? 1u : 0u;
                 if constexpr (kFP8)
                     mma_f8_ss(o_tmem, desc_join(p_hi, p_lo + (uint32_t)(kk * 2)), desc_join(desc_hi, v_lo + off_v),
                               idesc_o, acc);
@@ -549,7 +598,7 @@ __device__ __forceinline__ void mma_issue_pv(const Params& p, Barriers<NK, NV>* 
 
 // tm_o: O as [B][Sq][Hq][D] with the caller's strides, box {kOSwz bytes of a
 // row, 1 head, 32 rows, 1 batch}; unused in packed mode.
-template <int D, int KIND, bool kPacked, int QT = 2>
+template <int D, int KIND, bool kPacked, int QT = 2, bool kWin = false>
 __global__ void __launch_bounds__(Roles<QT>::kThreads, Roles<QT>::kCtasPerSm)
 sdpa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const Params p)
@@ -665,7 +714,7 @@ sdpa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 mbar_arrive_expect_tx(smem_u32(&bars->k_full[s]), L::kTileBytes);
                 for (int c = 0; c < L::kChunks; ++c)
                     tma_load_4d(sK + s * L::kTileBytes + c * L::kChunkBytes, &tm_k, smem_u32(&bars->k_full[s]),
-                                c * (L::kSwz / L::kEsize), w.hkv, (w.kv0 + j) * kBlockN, w.b);
+                                c * (L::kSwz / L::kEsize), w.hkv, w.tile<kWin>(j) * kBlockN, w.b);
                 ++nk;
                 return true;
             };
@@ -676,7 +725,7 @@ sdpa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 mbar_arrive_expect_tx(smem_u32(&bars->v_full[s]), L::kTileBytes);
                 for (int c = 0; c < L::kChunks; ++c)
                     tma_load_4d(sV + s * L::kTileBytes + c * L::kChunkBytes, &tm_v, smem_u32(&bars->v_full[s]),
-                                c * (L::kSwz / L::kEsize), w.hkv, (w.kv0 + j) * kBlockN, w.b);
+                                c * (L::kSwz / L::kEsize), w.hkv, w.tile<kWin>(j) * kBlockN, w.b);
                 ++nv;
                 return true;
             };
@@ -686,7 +735,7 @@ sdpa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     break;
                 if (u < 0)
                     continue;
-                const Unit w = decode_unit<kPacked, QT>(p, u);
+                const Unit w = decode_unit<kPacked, QT, kWin>(p, u);
                 const int n = w.n;
                 ok = load_q(w, 0) && load_k(w, 0) && (w.n_kv[1] == 0 || load_q(w, 1)) && load_v(w, 0);
                 for (int j = 1; ok && j < n; ++j)
@@ -709,11 +758,11 @@ sdpa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       } else if (warp == R::kSMmaWarp) {
         // ============================= S issuer =============================
         if (lane == 0)
-            mma_issue_s<D, KIND, kPacked, NK, NV, QT>(p, bars, abort, tmem, sQ, sK);
+            mma_issue_s<D, KIND, kPacked, NK, NV, QT, kWin>(p, bars, abort, tmem, sQ, sK);
       } else if (warp >= R::kMmaWarp && warp < R::kMmaWarp + QT) {
         // =========================== P V issuers ============================
         if (lane == 0) {
-            mma_issue_pv<D, KIND, kPacked, NK, NV, QT>(p, bars, abort, tmem, sV, sP, smem_u32(smem + L::kOffOnes),
+            mma_issue_pv<D, KIND, kPacked, NK, NV, QT, kWin>(p, bars, abort, tmem, sV, sP, smem_u32(smem + L::kOffOnes),
                                                   warp - R::kMmaWarp);
         }
       }
@@ -752,7 +801,7 @@ sdpa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 break;
             if (u < 0)
                 continue;
-            const Unit w = decode_unit<kPacked, QT>(p, u);
+            const Unit w = decode_unit<kPacked, QT, kWin>(p, u);
             const int n = w.kv(t);
             if (n == 0)
                 continue;                                  // this Q tile has no rows in the unit
@@ -766,7 +815,10 @@ sdpa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 limit = q_idx;
             float m = -INFINITY;                           // running max of S*c
             float l = 0.f;                                 // running sum of exp2(S*c - m) (16-bit kinds)
+            const int first = w.first<kWin>(t);
             for (int j = 0; j < n; ++j) {
+                if (!w.visits<kWin>(t, j))
+                    continue;
                 ok = __all_sync(0xffffffffu,
                                 wait_bar(smem_u32(&bars->s_full[t]), cs & 1, abort, kErrWaitSoftmax + 1 + t));
                 if (!ok)
@@ -778,8 +830,20 @@ sdpa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 // the S region is free for the next S as soon as it is read
                 tc_fence_before_sync();
                 mbar_arrive(smem_u32(&bars->s_free[t]));
-                const int k0 = (w.kv0 + j) * kBlockN;
-                if (k0 + kBlockN - 1 > limit) {
+                const int k0 = w.tile<kWin>(j) * kBlockN;
+                if constexpr (kWin) {
+                    // keys of the tile below `up`, and of those the ones from `low` on or below `stay`
+                    const int up = limit + 1 - k0, low = q_idx - p.window + 1 - k0, stay = p.sinks - k0;
+                    if (up < kBlockN || (low > 0 && stay < kBlockN)) {
+#pragma unroll
+                        for (int i = 0; i < 128; i += 32) {
+                            const uint32_t seen = bits_below(up - i) & (~bits_below(low - i) | bits_below(stay - i));
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                r[i + e] = seen >> e & 1 ? r[i + e] : 0xff800000u;
+                        }
+                    }
+                } else if (k0 + kBlockN - 1 > limit) {
 #pragma unroll
                     for (int i = 0; i < 128; ++i)
                         if (k0 + i > limit)
@@ -797,10 +861,12 @@ sdpa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 }
                 mx0 = fmax3(mx0, __uint_as_float(r[124]), __uint_as_float(r[125]));
                 mx1 = fmax3(mx1, __uint_as_float(r[126]), __uint_as_float(r[127]));
-                const float m_tile = fmax3(fmaxf(mx0, mx1), mx2, mx3) * c;
+                // (a row that has seen no key yet has a finite maximum below any other)
+                const float m_tile = kWin ? fmaxf(fmax3(fmaxf(mx0, mx1), mx2, mx3) * c, -FLT_MAX)
+                                          : fmax3(fmaxf(mx0, mx1), mx2, mx3) * c;
                 float alpha = 1.f;
                 bool rescale = false;
-                if (j == 0) {
+                if (j == first) {
                     m = m_tile;
                 } else if (m_tile > m + (kFP8 ? kRescaleThresholdFP8 : kRescaleThreshold)) {
                     alpha = ex2_approx(m - m_tile);
@@ -905,7 +971,7 @@ sdpa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 l = __uint_as_float(tmem_ld1_wait(l_tmem));   // sum of the E4M3 P values (tensor core, fp32)
             tc_fence_before_sync();
             mbar_arrive(smem_u32(&bars->o_empty[t]));
-            const float inv_l = p.out_scale / l;
+            const float inv_l = kWin && l == 0.f ? 0.f : p.out_scale / l;    // a row that sees no key is 0
             const int64_t row_id = ((int64_t)w.b * p.Hq + hq) * p.Sq + q_idx;
             if (q_idx < p.Sq && (p.lse || (kPacked && p.part_o))) {
                 // log sum_j exp(s_j) = ln 2 * (m + log2 l): m is the max of
