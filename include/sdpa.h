@@ -481,7 +481,44 @@ sdpa_status_t sdpa_fwd_paged(const void *Q, const sdpa_cache_t *cache,
                              float scale, int causal, sdpa_dtype_t dtype,
                              void *workspace, size_t workspace_bytes, void *stream);
 
-/* Workspace bytes sdpa_fwd_paged needs (0 for invalid sizes). */
+/*
+ * sdpa_fwd_paged (causal) with a sliding window: query i sees the positions up
+ * to its own, start[b] + i, that are less than `window` (>= 1) behind it or below
+ * `sinks` (>= 0).  Pages without such a position are not looked up or read: the
+ * block table may hold anything there (they may have been given back), a page
+ * that holds some of both is read.  Masked values that are NaN or infinite reach
+ * no row.  Workspace bytes are sdpa_paged_workspace_bytes; other arguments,
+ * numbers and statuses as for sdpa_fwd_paged.
+ */
+sdpa_status_t sdpa_fwd_paged_window(const void *Q, const sdpa_cache_t *cache,
+                                    const int *block_table, const int *start, const int *count,
+                                    void *O, float *LSE, int B, int Hq, int Hkv, int Sq, int D, int max_pages,
+                                    const sdpa_layout_t *q_layout, const sdpa_layout_t *o_layout,
+                                    float scale, int window, int sinks, sdpa_dtype_t dtype,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * sdpa_fwd_paged for a tree of drafted tokens: the count[b] new tokens of
+ * sequence b lie at positions start[b] + i, and query i sees positions
+ * 0 .. start[b] - 1 and start[b] + j for every new token j with bit j % 32 of
+ * tree_mask[b][i][j / 32] set (itself only with its own bit; bits at count[b]
+ * and above are not looked at).
+ *   tree_mask device, 32-bit words [B][Sq][(Sq + 31) / 32], contiguous.
+ * Keys carry the rotation of their place in the text (start[b] + depth), not of
+ * their slot: rotate them with sdpa_qk_norm_rope and append them without a table.
+ * When a path has been accepted, its keys and values are appended once more
+ * from start[b] on, in order (sdpa_cache_append overwrites the slots).
+ * Other arguments, numbers and statuses as for sdpa_fwd_paged.
+ */
+sdpa_status_t sdpa_fwd_paged_tree(const void *Q, const sdpa_cache_t *cache,
+                                  const int *block_table, const int *start, const int *count,
+                                  const unsigned *tree_mask,
+                                  void *O, float *LSE, int B, int Hq, int Hkv, int Sq, int D, int max_pages,
+                                  const sdpa_layout_t *q_layout, const sdpa_layout_t *o_layout,
+                                  float scale, sdpa_dtype_t dtype,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes sdpa_fwd_paged, sdpa_fwd_paged_window and sdpa_fwd_paged_tree need (0 for invalid sizes). */
 size_t sdpa_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D);
 
 /* Static, human-readable name of a status code. */

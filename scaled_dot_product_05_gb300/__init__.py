@@ -20,7 +20,7 @@ __all__ = ["sdpa_fwd", "sdpa_fwd_fp8", "sdpa_fwd_ex", "sdpa_fwd_fp8_ex", "sdpa_f
            "decode_workspace_bytes", "sdpa_status_string", "sdpa_device_error", "SdpaError", "lib",
            "rope_table", "sdpa_qk_norm_rope", "sdpa_qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_bytes",
            "PagedCache", "sdpa_cache_append", "sdpa_fwd_paged", "paged_workspace_bytes",
-           "sdpa_fwd_window", "sdpa_bwd_window"]
+           "sdpa_fwd_window", "sdpa_bwd_window", "sdpa_fwd_paged_window", "sdpa_fwd_paged_tree", "tree_mask"]
 
 _DTYPE = {torch.bfloat16: _abi.SDPA_DTYPE_BF16, torch.float16: _abi.SDPA_DTYPE_FP16}
 
@@ -327,4 +327,5 @@ def sdpa_device_error() -> int:
 
 from .cache import (PagedCache, paged_workspace_bytes, qk_norm_rope_bwd_workspace_bytes, rope_table,  # noqa: E402
                     sdpa_cache_append, sdpa_fwd_paged, sdpa_qk_norm_rope, sdpa_qk_norm_rope_bwd)
-from .masked import sdpa_bwd_window, sdpa_fwd_window  # noqa: E402
+from .masked import (sdpa_bwd_window, sdpa_fwd_paged_tree, sdpa_fwd_paged_window, sdpa_fwd_window,  # noqa: E402
+                     tree_mask)

@@ -17,7 +17,8 @@ EXPORTS = ("sdpa_fwd", "sdpa_fwd_fp8", "sdpa_fwd_ex", "sdpa_fwd_fp8_ex", "sdpa_f
            "sdpa_fwd_decode_noalloc", "sdpa_decode_workspace_bytes", "sdpa_bwd", "sdpa_bwd_workspace_bytes", "sdpa_bwd_fp8", "sdpa_bwd_fp8_workspace_bytes", "sdpa_status_string", "sdpa_last_cuda_error", "sdpa_device_error",
            "sdpa_abi_version",
            "sdpa_qk_norm_rope", "sdpa_qk_norm_rope_bwd", "sdpa_qk_norm_rope_bwd_workspace_bytes", "sdpa_cache_append",
-           "sdpa_fwd_paged", "sdpa_paged_workspace_bytes", "sdpa_fwd_window", "sdpa_bwd_window")
+           "sdpa_fwd_paged", "sdpa_paged_workspace_bytes", "sdpa_fwd_window", "sdpa_bwd_window",
+           "sdpa_fwd_paged_window", "sdpa_fwd_paged_tree")
 
 
 class Layout(ctypes.Structure):
@@ -90,6 +91,10 @@ def _bind(lib):
     lib.sdpa_cache_append.argtypes = [vp, vp, cp, vp, vp, vp, i, i, i, i, i, lp, lp, rp, i, vp]
     lib.sdpa_fwd_paged.restype = i
     lib.sdpa_fwd_paged.argtypes = [vp, cp, vp, vp, vp, vp, vp] + [i] * 6 + [lp, lp, f, i, i, vp, sz, vp]
+    lib.sdpa_fwd_paged_window.restype = i
+    lib.sdpa_fwd_paged_window.argtypes = [vp, cp, vp, vp, vp, vp, vp] + [i] * 6 + [lp, lp, f, i, i, i, vp, sz, vp]
+    lib.sdpa_fwd_paged_tree.restype = i
+    lib.sdpa_fwd_paged_tree.argtypes = [vp, cp, vp, vp, vp, vp, vp, vp] + [i] * 6 + [lp, lp, f, i, vp, sz, vp]
     lib.sdpa_paged_workspace_bytes.restype = sz
     lib.sdpa_paged_workspace_bytes.argtypes = [i] * 5
     lib.sdpa_status_string.restype = ctypes.c_char_p

@@ -371,7 +371,7 @@ size_t paged_workspace(int Hq, int Hkv, int Sq, int D)
     return static_cast<size_t>(paged_ctas(nr)) * (2 * nr * (D + 1) * sizeof(float) + sizeof(int4));
 }
 
-template <int D, bool kBF16, int NR>
+template <int D, bool kBF16, int NR, int MASK>
 cudaError_t launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const sdpa::paged::Params& p, int dev,
                          cudaStream_t stream)
 {
@@ -381,11 +381,11 @@ cudaError_t launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const sdp
     constexpr bool kWide = NR == kWideRows;
     auto* kernel = [] {
         if constexpr (kWide)
-            return paged_wide_kernel<D, kBF16>;
+            return paged_wide_kernel<D, kBF16, MASK>;
         else
-            return paged_attn_kernel<D, kBF16, NR>;
+            return paged_attn_kernel<D, kBF16, NR, MASK>;
     }();
-    using L = std::conditional_t<kWide, WideLayout<D, kBF16>, PagedLayout<D, kBF16, kWide ? 16 : NR>>;
+    using L = std::conditional_t<kWide, WideLayout<D, kBF16, MASK>, PagedLayout<D, kBF16, kWide ? 16 : NR>>;
     std::call_once(once[dev], [&] {
         attr[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
     });
@@ -399,14 +399,32 @@ cudaError_t launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const sdp
     return e;
 }
 
-template <int D, bool kBF16>
+template <int D, bool kBF16, int MASK>
 cudaError_t launch_paged_rows(int nr, const CUtensorMap& tk, const CUtensorMap& tv, const sdpa::paged::Params& p, int dev,
                               cudaStream_t s)
 {
-    return nr == 8    ? launch_paged<D, kBF16, 8>(tk, tv, p, dev, s)
-           : nr == 16 ? launch_paged<D, kBF16, 16>(tk, tv, p, dev, s)
-                      : launch_paged<D, kBF16, sdpa::paged::kWideRows>(tk, tv, p, dev, s);
+    return nr == 8    ? launch_paged<D, kBF16, 8, MASK>(tk, tv, p, dev, s)
+           : nr == 16 ? launch_paged<D, kBF16, 16, MASK>(tk, tv, p, dev, s)
+                      : launch_paged<D, kBF16, sdpa::paged::kWideRows, MASK>(tk, tv, p, dev, s);
 }
+
+template <int MASK>
+cudaError_t launch_paged_mask(int D, bool bf16, int nr, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const sdpa::paged::Params& p, int dev, cudaStream_t s)
+{
+    if (D == 64)
+        return bf16 ? launch_paged_rows<64, true, MASK>(nr, tk, tv, p, dev, s)
+                    : launch_paged_rows<64, false, MASK>(nr, tk, tv, p, dev, s);
+    return bf16 ? launch_paged_rows<128, true, MASK>(nr, tk, tv, p, dev, s)
+                : launch_paged_rows<128, false, MASK>(nr, tk, tv, p, dev, s);
+}
+
+// What the rows of a call over the cache see.
+struct PagedMask {
+    int kind;                        // sdpa::paged::MaskKind
+    int causal, window, sinks;
+    const unsigned* tree;
+};
 
 }  // namespace
 
@@ -524,10 +542,14 @@ sdpa_status_t sdpa_cache_append(const void* K, const void* V, const sdpa_cache_t
     return e == cudaSuccess ? SDPA_OK : cuda_fail(e);
 }
 
-sdpa_status_t sdpa_fwd_paged(const void* Q, const sdpa_cache_t* cache, const int* block_table, const int* start,
-                             const int* count, void* O, float* LSE, int B, int Hq, int Hkv, int Sq, int D, int max_pages,
-                             const sdpa_layout_t* q_layout, const sdpa_layout_t* o_layout, float scale, int causal,
-                             sdpa_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream)
+}  // extern "C"
+
+namespace {
+
+sdpa_status_t run_paged(const void* Q, const sdpa_cache_t* cache, const int* block_table, const int* start,
+                        const int* count, void* O, float* LSE, int B, int Hq, int Hkv, int Sq, int D, int max_pages,
+                        const sdpa_layout_t* q_layout, const sdpa_layout_t* o_layout, float scale, const PagedMask& mask,
+                        sdpa_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream)
 {
     if (dtype != SDPA_DTYPE_BF16 && dtype != SDPA_DTYPE_FP16)
         return SDPA_ERR_DTYPE;
@@ -560,10 +582,12 @@ sdpa_status_t sdpa_fwd_paged(const void* Q, const sdpa_cache_t* cache, const int
     // O, LSE and the workspace lie apart from one another and from every input
     const long long sc = static_cast<long long>(cache->n_pages) * Hkv * 4;
     const long long lse_bytes = LSE ? static_cast<long long>(B) * Hq * Sq * 4 : 0;
+    const int words = Sq / 32 + (Sq % 32 != 0);
     const Flat flat[] = {{cache->k, ck.span()}, {cache->v, cv.span()}, {cache->k_scale, sc}, {cache->v_scale, sc},
-                         {block_table, 4ll * B * max_pages}, {start, 4ll * B}, {count, 4ll * B}, {Q, q.span()},
-                         {O, o.span()}, {LSE, lse_bytes}, {workspace, static_cast<long long>(need)}};
-    constexpr int kQ = 7, kO = 8, kAll = 11;         // flat[8..10] are written
+                         {block_table, 4ll * B * max_pages}, {start, 4ll * B}, {count, 4ll * B},
+                         {mask.tree, 4ll * B * Sq * words}, {Q, q.span()}, {O, o.span()}, {LSE, lse_bytes},
+                         {workspace, static_cast<long long>(need)}};
+    constexpr int kQ = 8, kO = 9, kAll = 12;         // flat[9..11] are written
     for (int w = kO; w < kAll; ++w)
         for (int i = 0; i < w; ++i)
             if (flat[w].p && flat[i].p && overlaps(flat[w].p, flat[w].n, flat[i].p, flat[i].n) &&
@@ -593,7 +617,11 @@ sdpa_status_t sdpa_fwd_paged(const void* Q, const sdpa_cache_t* cache, const int
     p.page = cache->page_size;
     p.n_pages = cache->n_pages;
     p.max_pages = max_pages;
-    p.causal = causal ? 1 : 0;
+    p.causal = mask.causal;
+    p.window = mask.window;
+    p.sinks = mask.sinks;
+    p.tree = mask.tree;
+    p.tree_words = words;
     p.scale_log2 = scale_log2;
     p.page_shift = p.page == 16 ? 4 : p.page == 32 ? 5 : p.page == 64 ? 6 : 7;
     const int nr = paged_tile_rows(Sq, p.group);
@@ -622,11 +650,50 @@ sdpa_status_t sdpa_fwd_paged(const void* Q, const sdpa_cache_t* cache, const int
         return cuda_fail(cudaErrorInvalidValue);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == SDPA_DTYPE_BF16;
-    const cudaError_t e = D == 64 ? (bf16 ? launch_paged_rows<64, true>(nr, tk, tv, p, dev, cs)
-                                          : launch_paged_rows<64, false>(nr, tk, tv, p, dev, cs))
-                                  : (bf16 ? launch_paged_rows<128, true>(nr, tk, tv, p, dev, cs)
-                                          : launch_paged_rows<128, false>(nr, tk, tv, p, dev, cs));
+    using namespace sdpa::paged;
+    const cudaError_t e = mask.kind == kWindow ? launch_paged_mask<kWindow>(D, bf16, nr, tk, tv, p, dev, cs)
+                          : mask.kind == kTree ? launch_paged_mask<kTree>(D, bf16, nr, tk, tv, p, dev, cs)
+                                               : launch_paged_mask<kPlain>(D, bf16, nr, tk, tv, p, dev, cs);
     return e == cudaSuccess ? SDPA_OK : cuda_fail(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+sdpa_status_t sdpa_fwd_paged(const void* Q, const sdpa_cache_t* cache, const int* block_table, const int* start,
+                             const int* count, void* O, float* LSE, int B, int Hq, int Hkv, int Sq, int D, int max_pages,
+                             const sdpa_layout_t* q_layout, const sdpa_layout_t* o_layout, float scale, int causal,
+                             sdpa_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream)
+{
+    return run_paged(Q, cache, block_table, start, count, O, LSE, B, Hq, Hkv, Sq, D, max_pages, q_layout, o_layout, scale,
+                     PagedMask{sdpa::paged::kPlain, causal ? 1 : 0, 0, 0, nullptr}, dtype, workspace, workspace_bytes, stream);
+}
+
+sdpa_status_t sdpa_fwd_paged_window(const void* Q, const sdpa_cache_t* cache, const int* block_table, const int* start,
+                                    const int* count, void* O, float* LSE, int B, int Hq, int Hkv, int Sq, int D,
+                                    int max_pages, const sdpa_layout_t* q_layout, const sdpa_layout_t* o_layout,
+                                    float scale, int window, int sinks, sdpa_dtype_t dtype, void* workspace,
+                                    size_t workspace_bytes, void* stream)
+{
+    if (window < 1 || sinks < 0)
+        return SDPA_ERR_BAD_SHAPE;
+    return run_paged(Q, cache, block_table, start, count, O, LSE, B, Hq, Hkv, Sq, D, max_pages, q_layout, o_layout, scale,
+                     PagedMask{sdpa::paged::kWindow, 1, window, sinks, nullptr}, dtype, workspace, workspace_bytes, stream);
+}
+
+sdpa_status_t sdpa_fwd_paged_tree(const void* Q, const sdpa_cache_t* cache, const int* block_table, const int* start,
+                                  const int* count, const unsigned* tree_mask, void* O, float* LSE, int B, int Hq, int Hkv,
+                                  int Sq, int D, int max_pages, const sdpa_layout_t* q_layout,
+                                  const sdpa_layout_t* o_layout, float scale, sdpa_dtype_t dtype, void* workspace,
+                                  size_t workspace_bytes, void* stream)
+{
+    if (!tree_mask)
+        return SDPA_ERR_NULL_PTR;
+    if (!aligned(tree_mask, 4))
+        return SDPA_ERR_MISALIGNED;
+    return run_paged(Q, cache, block_table, start, count, O, LSE, B, Hq, Hkv, Sq, D, max_pages, q_layout, o_layout, scale,
+                     PagedMask{sdpa::paged::kTree, 0, 0, 0, tree_mask}, dtype, workspace, workspace_bytes, stream);
 }
 
 size_t sdpa_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D)

@@ -70,6 +70,9 @@ struct Params {
     int B, Sq, Hq, Hkv, group;
     int page, n_pages, max_pages;
     int causal;
+    int window, sinks;               // kWindow: a row sees the last `window` positions up to its own, and the first `sinks`
+    const uint32_t* tree;            // kTree: [B][Sq][tree_words], bit j of row i: it sees new token j
+    int tree_words;
     float scale_log2;                // scale * log2(e)
     int page_shift;                  // log2(page)
     int row_tiles;                   // tiles of NR rows that Sq * group rows need
@@ -83,6 +86,10 @@ struct Params {
 enum : unsigned int { kErrPagedLoad = 0x801, kErrPagedMma = 0x811, kErrPagedSoftmax = 0x821 };
 
 constexpr int kTileKeys = 128;
+
+// What a row sees besides its position's bound: all of it, a window and the
+// first positions, or all that was there before and some of the new tokens.
+enum MaskKind : int { kPlain = 0, kWindow = 1, kTree = 2 };
 
 // The power of two that a row of q is divided by: all of bf16's range, but that
 // it stops at 2^-118, for its inverse to be finite (a row whose largest is
@@ -169,11 +176,49 @@ struct PagedBarriers {
     long long warp_sums[12];
 };
 
+// The key tiles that rows with a window visit: 0 .. first - 1 for the first
+// positions, then near .. up to that of position len - 1 (len >= 1).  `row0`
+// is the position of the first row, `low` the lowest one inside its window.
+struct WindowTiles {
+    int first, near, n;
+    long long low;
+};
+
+__device__ __forceinline__ WindowTiles window_tiles(const Params& p, long long row0, long long len)
+{
+    WindowTiles t;
+    t.low = row0 - p.window + 1;
+    t.low = t.low < 0 ? 0 : t.low;
+    const int tiles = (int)((len + kTileKeys - 1) / kTileKeys);
+    const int sinks = (int)(p.sinks < len ? p.sinks : len);
+    t.first = sinks / kTileKeys + (sinks % kTileKeys != 0);
+    const long long near = t.low / kTileKeys;
+    t.near = near < t.first ? t.first : near < tiles ? (int)near : tiles;
+    t.n = t.first + (tiles - t.near);
+    t.n = t.n < 1 ? 1 : t.n;                           // (a tile that no row sees, so that the result is written)
+    if (t.near == tiles && t.first == 0)
+        t.near = tiles - 1;
+    return t;
+}
+
 // Number of key tiles of entry x = (sequence, row tile): 0 without rows, else
 // at least 1.  (In 32 bits the kernel of many rows comes out 12% slower.)
-template <int NR>
+template <int NR, int MASK>
 __device__ __forceinline__ int entry_tiles(const Params& p, long long x)
 {
+    if constexpr (MASK == kWindow) {
+        const int b = (int)(x / p.row_tiles);
+        const long long r0 = (x - (long long)b * p.row_tiles) * NR;
+        const int count = p.count ? max(0, min(p.Sq, p.count[b])) : p.Sq;
+        const long long rows = (long long)count * p.group;
+        if (r0 >= rows)
+            return 0;
+        const long long last = (rows < r0 + NR ? rows : r0 + NR) - 1, start = p.start[b];
+        const long long cap = (long long)p.max_pages << p.page_shift;
+        long long len = start + last / p.group + 1;
+        len = len < cap ? len : cap;
+        return len < 1 ? 1 : window_tiles(p, start + r0 / p.group, len).n;
+    }
     if constexpr (NR <= 16) {                          // one row tile holds a sequence's rows
         const int b = (int)x;
         const int count = p.count ? max(0, min(p.Sq, p.count[b])) : p.Sq;
@@ -207,7 +252,7 @@ __device__ __forceinline__ long long share_begin(const Params& p, long long tota
 // Whole-block: counts the tiles of all entries (times Hkv each) and finds the
 // entry that holds tile share_begin(c).  Entries are taken in order: the
 // tiles of entry x are those of KV head 0, then 1, ...
-template <int NR, int kThreads, typename Bars>
+template <int NR, int MASK, int kThreads, typename Bars>
 __device__ __forceinline__ void find_share(const Params& p, int c, Bars* bars)
 {
     const long long entries = (long long)p.B * p.row_tiles;
@@ -216,7 +261,7 @@ __device__ __forceinline__ void find_share(const Params& p, int c, Bars* bars)
     const long long x1 = x0 + per < entries ? x0 + per : entries;
     long long sum = 0;
     for (long long x = x0; x < x1; ++x)
-        sum += (long long)entry_tiles<NR>(p, x) * p.Hkv;
+        sum += (long long)entry_tiles<NR, MASK>(p, x) * p.Hkv;
     long long incl = sum;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -240,7 +285,7 @@ __device__ __forceinline__ void find_share(const Params& p, int c, Bars* bars)
     if (target >= first && target < first + sum) {
         long long x = x0;
         for (;; ++x) {
-            const long long n = (long long)entry_tiles<NR>(p, x) * p.Hkv;
+            const long long n = (long long)entry_tiles<NR, MASK>(p, x) * p.Hkv;
             if (target < first + n)
                 break;
             first += n;
@@ -260,7 +305,7 @@ struct Piece {
     long long left;                 // tiles of the share, this piece included
 };
 
-template <int NR, typename Bars>
+template <int NR, int MASK, typename Bars>
 __device__ __forceinline__ bool first_piece(const Params& p, const Bars* bars, Piece& w)
 {
     const int c = blockIdx.x;
@@ -269,7 +314,7 @@ __device__ __forceinline__ bool first_piece(const Params& p, const Bars* bars, P
     if (w.left <= 0)
         return false;
     w.x = bars->x;
-    w.n = entry_tiles<NR>(p, w.x);
+    w.n = entry_tiles<NR, MASK>(p, w.x);
     const long long off = t0 - bars->x_first;
     w.h = off >> 32 ? (int)(off / w.n) : (int)((uint32_t)off / (uint32_t)w.n);
     w.begin = (int)(off - (long long)w.h * w.n);
@@ -277,7 +322,7 @@ __device__ __forceinline__ bool first_piece(const Params& p, const Bars* bars, P
     return true;
 }
 
-template <int NR>
+template <int NR, int MASK>
 __device__ __forceinline__ bool next_piece(const Params& p, Piece& w)
 {
     w.left -= w.end - w.begin;
@@ -287,7 +332,7 @@ __device__ __forceinline__ bool next_piece(const Params& p, Piece& w)
         w.h = 0;
         do {
             ++w.x;
-            w.n = entry_tiles<NR>(p, w.x);
+            w.n = entry_tiles<NR, MASK>(p, w.x);
         } while (w.n == 0);
     }
     w.begin = 0;
@@ -301,9 +346,36 @@ struct Item {
     int r0, rows;                   // first row of the tile, valid rows in it
     long long start;
     int keys;                       // keys that some row of the item sees (within the table)
+    int low;                        // kWindow: the lowest position in a row's window
+    int first, near;                // kWindow: as in WindowTiles
+    // key tile of the item's j-th; what a list of tiles is worth is that of the others
+    template <int MASK>
+    __device__ __forceinline__ int tile(int j) const
+    {
+        return MASK != kWindow || j < first ? j : near + (j - first);
+    }
+    // some row sees some position of the page that begins at pos
+    template <int MASK>
+    __device__ __forceinline__ bool has_page(const Params& p, int pos) const
+    {
+        return pos < keys && (MASK != kWindow || pos < p.sinks || pos + p.page > low);
+    }
 };
 
-template <int NR>
+// Whether new token i of the item's sequence sees position pos (< it.keys).
+template <int MASK>
+__device__ __forceinline__ bool token_sees(const Params& p, const Item& it, int i, int pos)
+{
+    if constexpr (MASK == kWindow) {
+        const long long at = it.start + i;
+        return pos <= at && (pos > at - p.window || pos < p.sinks);
+    } else {
+        const long long j = pos - it.start;            // (new tokens behind the count are not among the keys)
+        return j < 0 || p.tree[((long long)it.b * p.Sq + i) * p.tree_words + (j >> 5)] >> (j & 31) & 1;
+    }
+}
+
+template <int NR, int MASK>
 __device__ __forceinline__ Item item_of(const Params& p, const Piece& w)
 {
     Item t;
@@ -316,6 +388,15 @@ __device__ __forceinline__ Item item_of(const Params& p, const Piece& w)
     long long len = t.start + (NR > 16 && p.causal ? (t.r0 + t.rows - 1) / p.group + 1 : t.count);
     len = len < 0 ? 0 : len;
     t.keys = (int)(len < cap ? len : cap);
+    if constexpr (MASK == kWindow) {
+        t.low = t.first = t.near = 0;
+        if (t.keys > 0) {
+            const WindowTiles list = window_tiles(p, t.start + t.r0 / p.group, t.keys);
+            t.low = (int)(list.low < t.keys ? list.low : t.keys);
+            t.first = list.first;
+            t.near = list.near;
+        }
+    }
     return t;
 }
 
@@ -344,7 +425,7 @@ __device__ __forceinline__ float warp_sums(float (&s)[N], int lane)
 
 // An item whose pieces several CTAs have is joined by the block of the second
 // of them, c: joins[c].w is the number of pieces (0: nothing to join there).
-template <int NR>
+template <int NR, int MASK>
 __device__ __forceinline__ int4 join_of(const Params& p, long long total, const Piece& w)
 {
     const int c = blockIdx.x;
@@ -359,10 +440,10 @@ __device__ __forceinline__ int4 join_of(const Params& p, long long total, const 
         else
             hi = mid - 1;
     }
-    return make_int4((int)w.x, w.h, item_of<NR>(p, w).rows, last - c + 2);
+    return make_int4((int)w.x, w.h, item_of<NR, MASK>(p, w).rows, last - c + 2);
 }
 
-template <int D, bool kBF16, int NR>
+template <int D, bool kBF16, int NR, int MASK>
 __global__ void __launch_bounds__(PagedLayout<D, kBF16, NR>::kThreads, 2)
 paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p)
 {
@@ -416,10 +497,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const uint32_t tmem = bars->tmem_base;
     grid_dependency_wait();
     grid_launch_dependents();
-    find_share<NR, L::kThreads>(p, blockIdx.x, bars);
+    find_share<NR, MASK, L::kThreads>(p, blockIdx.x, bars);
 
     Piece w;
-    bool more = first_piece<NR>(p, bars, w);
+    bool more = first_piece<NR, MASK>(p, bars, w);
     if (warp == kProducer) {
         // =========================== TMA producer ===========================
         // lane i brings page i of a tile; pages that no row sees, or whose
@@ -427,13 +508,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const int ppt = kTileKeys >> p.page_shift;
         uint32_t n = 0;                                    // tiles issued (ring position)
         bool ok = true;
-        for (; ok && more; more = next_piece<NR>(p, w)) {
-            const Item it = item_of<NR>(p, w);
+        for (; ok && more; more = next_piece<NR, MASK>(p, w)) {
+            const Item it = item_of<NR, MASK>(p, w);
             // table entries are read three tiles ahead and looked at when their
             // tile comes, so that no tile waits for one
             auto entry_of = [&](int tile) -> int {
-                const int ord = tile * ppt + lane;
-                return lane < ppt && tile < w.end && ord << p.page_shift < it.keys
+                const int ord = it.tile<MASK>(tile) * ppt + lane;
+                return lane < ppt && tile < w.end && it.has_page<MASK>(p, ord << p.page_shift)
                            ? p.table[(long long)it.b * p.max_pages + ord]
                            : -1;
             };
@@ -469,7 +550,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         if (lane == 0 && blockIdx.x > 0) {                 // (after the loads, which nothing should keep waiting)
             Piece first;
-            p.joins[blockIdx.x] = first_piece<NR>(p, bars, first) ? join_of<NR>(p, bars->total, first) : make_int4(0, 0, 0, 0);
+            p.joins[blockIdx.x] = first_piece<NR, MASK>(p, bars, first) ? join_of<NR, MASK>(p, bars->total, first) : make_int4(0, 0, 0, 0);
         }
         // never leave with copies in flight (after an abort the last K tile
         // may or may not have been issued: at worst its wait runs out)
@@ -499,7 +580,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             uint32_t ks_n = 0, vs_n = 0, pieces = 0;       // S^T and O^T products issued, pieces begun
             uint32_t ns0 = 0, ns1 = 0, nv0 = 0, nv1 = 0;   // the same, of each warpgroup
             bool ok = true;
-            for (; ok && more; more = next_piece<NR>(p, w), ++pieces) {
+            for (; ok && more; more = next_piece<NR, MASK>(p, w), ++pieces) {
                 const int n = w.end - w.begin;
                 auto issue_s = [&](int g) -> bool {
                     const uint32_t ks = ks_n % NK, done = g ? ns1 : ns0;
@@ -567,14 +648,16 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         float* row_shift = row_nmax + NR;                                   // by how much the maximum grows
         float* row_factor = row_nmax + 2 * NR;                              // rescale; in the end the weight of O^T
         float* exch = row_nmax + 3 * NR;                                    // [4][NR]
-        int* nan_at = reinterpret_cast<int*>(group_rows + 7 * NR * G);      // [D]: first masked key with a NaN there
+        // [D]: first masked key with a NaN there; with a mask of its own: the rows that see such a key, a bit each
+        int* nan_at = reinterpret_cast<int*>(group_rows + 7 * NR * G);
+        constexpr bool kMasked = MASK != kPlain;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lanes + g * L::kGroupCols, t_o = t_s + L::kQRows;
         uint32_t ns = 0;                                                    // tiles of this warpgroup so far
         uint32_t nv = 0;                                                    // tiles of the CTA before this piece
         bool ok = true;
-        for (; more; nv += w.end - w.begin, more = next_piece<NR>(p, w)) {
-            const Item it = item_of<NR>(p, w);
+        for (; more; nv += w.end - w.begin, more = next_piece<NR, MASK>(p, w)) {
+            const Item it = item_of<NR, MASK>(p, w);
             // ---- q into 8-bit parts, and each row's numbers
             {
                 constexpr int kPer = L::kSoftmax / L::kQRows;               // threads of a row
@@ -628,7 +711,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         group_rows[7 * NR * k + r] = live ? kLog2W : -INFINITY;
                 }
                 if (threadIdx.x < D)
-                    nan_at[threadIdx.x] = INT_MAX;
+                    nan_at[threadIdx.x] = kMasked ? 0 : INT_MAX;
                 if (threadIdx.x == 0 && it.start + it.count > (long long)p.max_pages * p.page)
                     atomicCAS(&g_sdpa_error, 0u, (unsigned)cache::kErrTable);
                 fence_proxy_async_smem();
@@ -636,7 +719,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 mbar_arrive(smem_u32(&bars->q_full));
             }
             // every row of the item sees keys 0 .. full - 1
-            const int full = row_last[0] + 1;
+            const int full = MASK == kTree ? (int)max(0ll, min(it.start, (long long)it.keys)) : row_last[0] + 1;
+            // with a window: of the keys below `full` those from `full_low` on, or below p.sinks
+            const int full_low = MASK == kWindow ? (int)max(0ll, it.start + (it.r0 + it.rows - 1) / p.group - p.window + 1) : 0;
             uint64_t l[NR / 2];                                             // pairs of rows
 #pragma unroll
             for (int r = 0; r < NR / 2; ++r)
@@ -647,8 +732,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             // scales one ahead: each is looked at when the next is on its way
             const int* table = p.table + (long long)it.b * p.max_pages;
             auto entry_of = [&](int tile) -> int {
-                const int pos = tile * kTileKeys + tid;
-                return tile < w.end && pos < it.keys ? table[pos >> p.page_shift] : INT_MIN;
+                const int pos = it.tile<MASK>(tile) * kTileKeys + tid;
+                const bool in = kMasked ? pos < it.keys && it.has_page<MASK>(p, pos & -p.page) : pos < it.keys;
+                return tile < w.end && in ? table[pos >> p.page_shift] : INT_MIN;
             };
             auto scales_of = [&](int entry, float& a, float& b) -> bool {
                 a = b = 1.f;
@@ -675,9 +761,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 entry_next = entry_of(j + 2 * G);
                 valid_next = scales_of(entry, k_scale, v_scale);
                 const uint32_t vn = nv + (uint32_t)(j - w.begin);           // V ring position
-                const int pos = j * kTileKeys + tid;
+                const int tile0 = it.tile<MASK>(j) * kTileKeys, pos = tile0 + tid;
                 // tiles in which some row does not see some key, by the item's rows or by a page that is none
-                const bool edge = (j + 1) * kTileKeys > full || __any_sync(0xffffffffu, !valid);
+                const bool edge = tile0 + kTileKeys > full || __any_sync(0xffffffffu, !valid) ||
+                                  (MASK == kWindow && tile0 < full_low && tile0 + kTileKeys > p.sinks);
+                uint32_t seen_rows = 0;                                     // of an edge tile: rows that see this key
                 ok = ok && wait_bar(smem_u32(&bars->s_full[g]), ns & 1, abort, kErrPagedSoftmax);
                 tc_fence_after_sync();
                 // s + log2(v_scale): the logarithm of a weight but for the maximum, which comes off with kLog2W on top
@@ -702,12 +790,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                                                  mul_f32x2(sc.y, ks2), add_f32x2(nm.y, lvs2));
                     }
                     if (edge) {
+                        if constexpr (kMasked) {
+                            if (valid) {
+#pragma unroll
+                                for (int r = 0; r < NR; ++r)
+                                    seen_rows |= r < it.rows && token_sees<MASK>(p, it, (it.r0 + r) / p.group, pos) ? 1u << r : 0u;
+                            }
+                        }
 #pragma unroll
                         for (int r = 0; r < NR; r += 2) {
                             float a, b;
                             f32x2_split(x[r / 2], a, b);
-                            x[r / 2] = f32x2(valid && pos <= row_last[r] ? a : -INFINITY,
-                                             valid && pos <= row_last[r + 1] ? b : -INFINITY);
+                            const bool sa = kMasked ? seen_rows >> r & 1 : valid && pos <= row_last[r];
+                            const bool sb = kMasked ? seen_rows >> (r + 1) & 1 : valid && pos <= row_last[r + 1];
+                            x[r / 2] = f32x2(sa ? a : -INFINITY, sb ? b : -INFINITY);
                         }
                     }
                     float m0 = -INFINITY, m1 = -INFINITY;
@@ -746,7 +842,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         row_factor[tid] = seen ? ex2_approx(-up) : 1.f;     // nothing to rescale before the first key
                         row_nmax[tid] -= up;
                         seen = seen || m > -INFINITY;
-                        waits = !seen && row_last[tid] >= (j + G) * kTileKeys;
+                        waits = !seen && (kMasked ? tid < it.rows : row_last[tid] >= (j + G) * kTileKeys);
                     }
                     force = named_bar_any(bar_group, 128, waits);
                     tc_fence_after_sync();
@@ -788,7 +884,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
                         for (int c = 0; c < D / 16; ++c)
                             st_shared_v4(row + c * 16, 0u, 0u, 0u, 0u);
-                    } else if (ok && pos >= full) {
+                    } else if (ok && (kMasked ? seen_rows != (1u << it.rows) - 1u : pos >= full)) {
                         for (int c = 0; c < D / 4; ++c) {
                             // 16-byte chunk c / 4 of the row lies at its swizzled place
                             const int chunk = D == 128 ? (c / 4) ^ (tid & 7) : (c / 4) ^ ((tid >> 1) & 3);
@@ -799,7 +895,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                             if (hit) {
                                 for (int e = 0; e < 4; ++e)
                                     if (hit >> (8 * e + 7) & 1) {
-                                        atomicMin(&nan_at[4 * c + e], pos);
+                                        if constexpr (kMasked)
+                                            atomicOr(&nan_at[4 * c + e], (int)seen_rows);
+                                        else
+                                            atomicMin(&nan_at[4 * c + e], pos);
                                         u &= ~(0xffu << (8 * e));
                                     }
                                 *at = u;
@@ -898,7 +997,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             // channel tid of every row, from both warpgroups' accumulators
             if (g == 0) {
                 const int groups = w.end - w.begin < G ? w.end - w.begin : G;
-                const int nan_from = tid < D ? nan_at[tid] : INT_MAX;
+                const int nan_from = tid < D ? nan_at[tid] : kMasked ? 0 : INT_MAX;
                 float o[NR];
 #pragma unroll
                 for (int r = 0; r < NR; ++r)
@@ -924,7 +1023,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     for (int r = 0; r < NR; ++r) {
                         if (r >= it.rows)
                             break;
-                        const float v = row_last[r] >= nan_from ? NAN : o[r];
+                        const float v = (kMasked ? nan_from >> r & 1 : row_last[r] >= nan_from) ? NAN : o[r];
                         if (!whole) {
                             p.part_o[(slot * NR + r) * D + tid] = v;
                         } else {

@@ -31,7 +31,7 @@ constexpr int kWideRows = 128;
 constexpr float kWideLag = 8.0f;           // a weight may reach 2^8 before the maximum moves
 constexpr float kWideLog2W = 7.0f;         // weight 1 is held as 2^7: 2^15 at most
 
-template <int D, bool kBF16>
+template <int D, bool kBF16, int MASK = kPlain>
 struct WideLayout {
     static constexpr int kParts = kBF16 ? 2 : 3;
     static constexpr int kThreads = 384;   // 8 softmax warps; TMA producer, S issuer, 2 converters
@@ -46,12 +46,42 @@ struct WideLayout {
     static constexpr int kOffV16 = kOffV8 + kStagesV * kTileBytes;
     static constexpr int kOffPages = kOffV16 + 2 * kV16Bytes;   // [kPageBufs][8] float4: scales of 16 keys each
     static constexpr int kOffRows = kOffPages + kPageBufs * 8 * 16;     // [2][128] maxima and [2][128] sums; [D] NaN; any NaN
-    static constexpr int kOffBar = kOffRows + 4 * (4 * kWideRows + D + 4);
+    // (with a mask of its own, a bit for each of the 128 rows in place of the key: [D][4])
+    static constexpr int kOffBar = kOffRows + 4 * (4 * kWideRows + (MASK == kPlain ? D : 4 * D) + 4);
     static constexpr int kBarBytes = 640;
     static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory budget");
     static constexpr uint32_t kTmemCols = 512;                  // S at 0; of warpgroup g: W at 128 + 64 g, O at 256 + 128 g
 };
+
+// Every row of the item sees keys full_from .. full_keys - 1 (and, with a
+// window, the first p.sinks of those below full_keys).
+template <int MASK>
+__device__ __forceinline__ int full_keys(const Params& p, const Item& it)
+{
+    const long long row0 = MASK == kTree ? it.start - 1 : p.causal ? it.start + it.r0 / p.group : it.start + it.count - 1;
+    return row0 < 0 ? 0 : (int)(row0 + 1 < it.keys ? row0 + 1 : it.keys);
+}
+
+template <int MASK>
+__device__ __forceinline__ int full_from(const Params& p, const Item& it)
+{
+    if constexpr (MASK != kWindow)
+        return 0;
+    return (int)max(0ll, min(it.start + (it.r0 + it.rows - 1) / p.group - p.window + 1, (long long)it.keys));
+}
+
+// Bits j .. j + 31 of a row's tree mask; what lies before bit 0 (the tokens
+// that were there before) is seen.
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int words, long long j)
+{
+    if (j <= -32)
+        return ~0u;
+    const int w = (int)(j >> 5);                       // (-1 for what begins before bit 0)
+    const uint32_t lo = row && w >= 0 && w < words ? row[w] : 0u;
+    const uint32_t hi = row && w + 1 < words ? row[w + 1] : 0u;
+    return __funnelshift_r(lo, hi, (uint32_t)(j & 31)) | bits_below(j < 0 ? (int)-j : 0);
+}
 
 template <int NK, int NV>
 struct WideBarriers {
@@ -70,13 +100,15 @@ struct WideBarriers {
     Item item;
 };
 
-template <int D, bool kBF16>
+template <int D, bool kBF16, int MASK>
 __global__ void __launch_bounds__(384, 1)
 paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p)
 {
-    using L = WideLayout<D, kBF16>;
+    using L = WideLayout<D, kBF16, MASK>;
     constexpr int NK = L::kStagesK, NV = L::kStagesV, QP = L::kParts, NR = kWideRows;
     constexpr uint32_t kBarSoftmax = 1;
+    constexpr bool kMasked = MASK != kPlain;
+    constexpr int kNanWords = kMasked ? 4 * D : D;
     using Bars = WideBarriers<NK, NV>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -91,7 +123,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     float* row_max = reinterpret_cast<float*>(smem + L::kOffRows);          // [2][128]
     float* row_sum = row_max + 2 * NR;                                      // [2][128]
     int* nan_at = reinterpret_cast<int*>(row_sum + 2 * NR);                 // [D]: first masked key with a NaN there
-    int* any_nan = nan_at + D;
+    int* any_nan = nan_at + kNanWords;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NK; ++i) {
@@ -134,10 +166,10 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const uint32_t tmem = bars->tmem_base;
     grid_dependency_wait();
     grid_launch_dependents();
-    find_share<NR, L::kThreads>(p, blockIdx.x, bars);
+    find_share<NR, MASK, L::kThreads>(p, blockIdx.x, bars);
 
     Piece w;
-    bool more = first_piece<NR>(p, bars, w);
+    bool more = first_piece<NR, MASK>(p, bars, w);
     if (warp >= 8) {
         regs_release<104>();
         if (warp == 8) {
@@ -145,23 +177,24 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             // as in paged_attn_kernel: lane i brings page i of a tile; and lane
             // i < 8 lays out the scales of the tile's keys 16 i .. 16 i + 15
             if (lane == 0 && blockIdx.x > 0)
-                p.joins[blockIdx.x] = more ? join_of<NR>(p, bars->total, w) : make_int4(0, 0, 0, 0);
+                p.joins[blockIdx.x] = more ? join_of<NR, MASK>(p, bars->total, w) : make_int4(0, 0, 0, 0);
             const int ppt = kTileKeys >> p.page_shift;
             uint32_t n = 0;
             bool ok = true;
-            for (; ok && more; more = next_piece<NR>(p, w)) {
-                const Item it = item_of<NR>(p, w);
+            for (; ok && more; more = next_piece<NR, MASK>(p, w)) {
+                const Item it = item_of<NR, MASK>(p, w);
                 auto entry_of = [&](int tile) -> int {
-                    const int ord = tile * ppt + lane;
-                    return lane < ppt && tile < w.end && ord << p.page_shift < it.keys
+                    const int ord = it.tile<MASK>(tile) * ppt + lane;
+                    return lane < ppt && tile < w.end && it.has_page<MASK>(p, ord << p.page_shift)
                                ? p.table[(long long)it.b * p.max_pages + ord]
                                : -1;
                 };
                 int ahead0 = entry_of(w.begin), ahead1 = entry_of(w.begin + 1);
                 // a part's table entry two tiles ahead, its scales one ahead
                 auto part_of = [&](int tile) -> int {
-                    const int pos = tile * kTileKeys + lane * 16;
-                    return lane < 8 && tile < w.end && pos < it.keys ? p.table[(long long)it.b * p.max_pages + (pos >> p.page_shift)]
+                    const int pos = it.tile<MASK>(tile) * kTileKeys + lane * 16;
+                    const bool in = kMasked ? pos < it.keys && it.has_page<MASK>(p, pos & -p.page) : pos < it.keys;
+                    return lane < 8 && tile < w.end && in ? p.table[(long long)it.b * p.max_pages + (pos >> p.page_shift)]
                                                                      : INT_MIN;
                 };
                 auto scales_of = [&](int entry, float& a, float& b) -> bool {
@@ -240,7 +273,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 uint32_t ns = 0, pieces = 0, f0 = 0, f1 = 0;       // S issued: all, for each warpgroup
                 int prev = -1;                                     // warpgroup of the last S
                 bool ok = true;
-                for (; ok && more; more = next_piece<NR>(p, w), ++pieces) {
+                for (; ok && more; more = next_piece<NR, MASK>(p, w), ++pieces) {
                     ok = wait_bar(smem_u32(&bars->q_full), pieces & 1, abort, kErrPagedMma + 2);
                     for (int j = 0; ok && j < w.end - w.begin; ++j, ++ns) {
                         const int g = j & 1;
@@ -281,13 +314,13 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             const int tid = threadIdx.x - 320;                              // 0 .. 63
             uint32_t n = 0, pieces = 0;
             bool ok = true;
-            for (; ok && more; more = next_piece<NR>(p, w), ++pieces) {
-                const Item it = item_of<NR>(p, w);
+            for (; ok && more; more = next_piece<NR, MASK>(p, w), ++pieces) {
+                const Item it = item_of<NR, MASK>(p, w);
                 // the piece before has been read out and its NaN forgotten
                 ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->q_full), pieces & 1, abort, kErrPagedSoftmax + 8));
-                const long long row0 = p.causal ? it.start + it.r0 / p.group : it.start + it.count - 1;
-                const int full = row0 < 0 ? 0 : (int)(row0 + 1 < it.keys ? row0 + 1 : it.keys);
+                const int full = full_keys<MASK>(p, it), full_low = full_from<MASK>(p, it);
                 for (int j = w.begin; ok && j < w.end; ++j, ++n) {
+                    const int tile0 = it.tile<MASK>(j) * kTileKeys;
                     const uint32_t b = n & 1, ring = n % NV, pb = n % L::kPageBufs;
                     ok = wait_bar(smem_u32(&bars->pages_full[pb]), (n / L::kPageBufs) & 1, abort, kErrPagedSoftmax + 6);
                     uint32_t valid_parts = 0xffu;
@@ -310,14 +343,15 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     uint8_t* src = smem + L::kOffV8 + ring * L::kTileBytes + key0 * D + at * 16;
                     const uint32_t row = sV16 + b * L::kV16Bytes + (c / 4) * (kTileKeys * 128) + key0 * 128;
                     const uint32_t dst0 = row + (((c % 4) * 2) ^ (key0 & 7)) * 16, dst1 = row + (((c % 4) * 2 + 1) ^ (key0 & 7)) * 16;
-                    if ((j + 1) * kTileKeys > full || valid_parts != 0xffu) {
+                    if (tile0 + kTileKeys > full || valid_parts != 0xffu ||
+                        (MASK == kWindow && tile0 < full_low && tile0 + kTileKeys > p.sinks)) {
 #pragma unroll 4
                         for (int i = 0; i < kTurns; ++i) {
-                            const int key = key0 + i * kStep, pos = j * kTileKeys + key;
+                            const int key = key0 + i * kStep, pos = tile0 + key;
                             uint4* u = reinterpret_cast<uint4*>(src + i * kStep * D);
                             if (pos >= it.keys || !(valid_parts >> (key / 16) & 1)) {
                                 *u = make_uint4(0, 0, 0, 0);
-                            } else if (pos >= full) {
+                            } else if (pos >= full || (MASK == kWindow && pos < full_low && pos >= p.sinks)) {
                                 const uint4 q = *u;
                                 auto nans = [](uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };    // 0x7F, 0xFF
                                 if (nans(q.x) | nans(q.y) | nans(q.z) | nans(q.w)) {
@@ -325,7 +359,13 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                                     for (int e = 0; e < 16; ++e) {
                                         uint8_t* byte = src + i * kStep * D + e;
                                         if ((*byte & 0x7f) == 0x7f) {
-                                            atomicMin(&nan_at[16 * c + e], pos);
+                                            if constexpr (kMasked) {
+                                                for (int r = 0; r < it.rows; ++r)
+                                                    if (token_sees<MASK>(p, it, (it.r0 + r) / p.group, pos))
+                                                        atomicOr(&nan_at[4 * (16 * c + e) + (r >> 5)], 1 << (r & 31));
+                                            } else {
+                                                atomicMin(&nan_at[16 * c + e], pos);
+                                            }
                                             *byte = 0;
                                         }
                                     }
@@ -368,8 +408,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         uint32_t ns = 0;                                                    // tiles of this warpgroup so far
         uint32_t nv = 0;                                                    // tiles of the CTA before this piece
         bool ok = true;
-        for (; more; nv += w.end - w.begin, more = next_piece<NR>(p, w)) {
-            Item it = item_of<NR>(p, w);
+        for (; more; nv += w.end - w.begin, more = next_piece<NR, MASK>(p, w)) {
+            Item it = item_of<NR, MASK>(p, w);
             // ---- q into 8-bit parts: two threads a row, half of its channels each
             float scale;                                                    // of this thread's row in the loop below
             {
@@ -417,8 +457,12 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 }
                 if (half == 0)
                     row_max[r] = top < 0x7f800000u ? qs : NAN;              // handed to the row's own threads
-                if (threadIdx.x < D)
+                if constexpr (kMasked) {
+                    for (int e = threadIdx.x; e < kNanWords; e += 256)
+                        nan_at[e] = 0;
+                } else if (threadIdx.x < D) {
                     nan_at[threadIdx.x] = INT_MAX;
+                }
                 if (threadIdx.x == 0) {
                     bars->piece = w;
                     bars->item = it;
@@ -434,12 +478,13 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             const int q_row = (it.r0 + row) / p.group;
             const long long last_pos = p.causal ? it.start + q_row : it.start + it.count - 1;
             const int last = row >= it.rows || last_pos < 0 ? -1 : (int)(last_pos < it.keys ? last_pos : it.keys - 1);
-            const long long row0 = p.causal ? it.start + it.r0 / p.group : it.start + it.count - 1;
-            const int full = row0 < 0 ? 0 : (int)(row0 + 1 < it.keys ? row0 + 1 : it.keys);
+            const int full = full_keys<MASK>(p, it), full_low = full_from<MASK>(p, it);
+            const uint32_t* tree = MASK == kTree && row < it.rows ? p.tree + ((long long)it.b * p.Sq + q_row) * p.tree_words : nullptr;
             float nmax = kWideLog2W;                                        // 7 - maximum
             float l = 0.f;                                                  // sum of exp2(s - maximum + 7)
             bool seen = false;
-            // j counts the piece's tiles
+            // j counts the piece's tiles (with a window, those lie at tile0 of their number)
+            const int begin = w.begin;
             const int tiles = w.end - w.begin, ahead = full - w.begin * kTileKeys, seen_end = last - w.begin * kTileKeys;
             for (int j = g; j < tiles; j += 2, ++ns) {
                 const uint32_t vn = nv + (uint32_t)j, buf = vn % L::kPageBufs;
@@ -453,7 +498,9 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 tmem_ld128_wait(t_s, t_s + 32, t_s + 64, t_s + 96, r);
                 tc_fence_before_sync();
                 mbar_arrive(smem_u32(&bars->s_free[g]));
-                const bool edge = (j + 1) * kTileKeys > ahead;
+                const int tile0 = kMasked ? it.tile<MASK>(begin + j) * kTileKeys : 0;
+                const bool edge = kMasked ? tile0 + kTileKeys > full || (MASK == kWindow && tile0 < full_low && tile0 + kTileKeys > p.sinks)
+                                          : (j + 1) * kTileKeys > ahead;
                 float mx = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
@@ -471,13 +518,33 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 // keys that the row does not see, or whose page is none (.w: the
                 // tile has such a page), whatever was there
                 if (__builtin_expect(edge || pages[buf * 8].w != 0.f, 0)) {
-                    const int seen_keys = seen_end - j * kTileKeys;             // of the tile, less one
+                    if constexpr (kMasked) {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const int end = pages[buf * 8 + c].y == -INFINITY ? -1 : seen_keys;
+                        for (int c = 0; c < 4; ++c) {
+                            const int k0 = tile0 + 32 * c;                      // bit e: the row sees key k0 + e
+                            uint32_t seen_keys = bits_below(last + 1 - k0);
+                            if constexpr (MASK == kWindow) {
+                                // (the row's position is last or, where the table ends before it, behind that)
+                                const int low = (int)max(0ll, min(last_pos - p.window + 1, 1ll << 30));
+                                seen_keys &= ~bits_below(low - k0) | bits_below(p.sinks - k0);
+                            } else {
+                                seen_keys &= tree_bits(tree, p.tree_words, k0 - it.start);
+                            }
+                            seen_keys &= (pages[buf * 8 + 2 * c].y == -INFINITY ? 0u : 0xffffu) |
+                                         (pages[buf * 8 + 2 * c + 1].y == -INFINITY ? 0u : 0xffff0000u);
 #pragma unroll
-                        for (int e = 16 * c; e < 16 * c + 16; ++e)
-                            r[e] = e > end ? 0xff800000u : r[e];
+                            for (int e = 0; e < 32; ++e)
+                                r[32 * c + e] = seen_keys >> e & 1 ? r[32 * c + e] : 0xff800000u;
+                        }
+                    } else {
+                        const int seen_keys = seen_end - j * kTileKeys;         // of the tile, less one
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const int end = pages[buf * 8 + c].y == -INFINITY ? -1 : seen_keys;
+#pragma unroll
+                            for (int e = 16 * c; e < 16 * c + 16; ++e)
+                                r[e] = e > end ? 0xff800000u : r[e];
+                        }
                     }
                 }
                 float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
@@ -619,7 +686,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (nans) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        if (last_key >= nan_at[c + e])
+                        if (kMasked ? nan_at[4 * (c + e) + (row >> 5)] >> (row & 31) & 1 : last_key >= nan_at[c + e])
                             o[e] = NAN;
                 }
                 if (live && !whole) {

@@ -1,6 +1,8 @@
 """Attention whose rows see part of the keys: a sliding window with a few first
-keys that stay visible (the Python side of sdpa_fwd_window and sdpa_bwd_window;
-argument marshalling only)."""
+keys that stay visible, over tensors and over the paged cache, and a tree of
+drafted tokens over that cache (the Python side of sdpa_fwd_window,
+sdpa_bwd_window, sdpa_fwd_paged_window and sdpa_fwd_paged_tree; argument
+marshalling only)."""
 from __future__ import annotations
 
 import math
@@ -8,8 +10,9 @@ import math
 import torch
 
 from . import _DTYPE, _lse_ptr, _shapes, _stream_ptr, bwd_workspace_bytes
-from .cache import _alloc, _call, _empty_like, _like, _strides, _workspace
-from ._abi import lib
+from . import cache as _cache
+from .cache import (PagedCache, _alloc, _cache_args, _call, _empty_like, _like, _strides, _workspace,
+                    paged_workspace_bytes)
 
 
 def _dense(q, k, v):
@@ -45,7 +48,7 @@ def sdpa_fwd_window(q, k, v, o=None, lse=None, *, window: int, sinks: int = 0, s
         raise ValueError("lse must be on the tensors' device")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    _call(dev, lib().sdpa_fwd_window, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _lse_ptr(lse, B, Hq, Sq), B,
+    _call(dev, (_cache._lib or _cache._bound()).sdpa_fwd_window, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _lse_ptr(lse, B, Hq, Sq), B,
           Hq, Hkv, Sq, Skv, D, _strides(q), _strides(k), _strides(v), lo, scale, window, sinks, _DTYPE.get(q.dtype, 99),
           _stream_ptr(stream, dev))
     return o
@@ -75,7 +78,86 @@ def sdpa_bwd_window(q, k, v, o, do, lse, dq=None, dk=None, dv=None, *, window: i
     ws, ws_bytes = _workspace(workspace, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    _call(dev, lib().sdpa_bwd_window, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
+    _call(dev, (_cache._lib or _cache._bound()).sdpa_bwd_window, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
           _lse_ptr(lse, B, Hq, Sq), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, Sq, Skv, D, scale, window,
           sinks, _DTYPE.get(q.dtype, 99), ws, ws_bytes, _stream_ptr(stream, dev))
     return dq, dk, dv
+
+
+def _paged_args(q, cache, block_table, start, count, o, lse, scale, workspace, stream):
+    """What the calls over a cache share: (device, o, arguments before o, o and lse, the arguments up to the scale,
+    workspace)."""
+    dev = cache._device
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != cache.head_dim:
+        raise ValueError("q must be [B, Sq, Hq, D] with the cache's head dimension")
+    if q.get_device() != dev:
+        raise ValueError("q must be on the cache's device")
+    B, Sq, Hq, D = shape
+    Hkv = cache.n_heads
+    lo = None
+    if o is None:
+        o = _empty_like(q, stream, dev)
+    else:
+        lo = _like(o, q, dev, "o")
+    if lse is not None and lse.get_device() != dev:
+        raise ValueError("lse must be on the cache's device")
+    if workspace is None:
+        workspace = _alloc(stream, dev, q.new_empty, (paged_workspace_bytes(B, Hq, Hkv, Sq, D),), dtype=torch.uint8)
+    ws = _workspace(workspace, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    table_p, start_p, count_p, width = _cache_args(cache, block_table, start, count, B)
+    return (dev, o, (q.data_ptr(), cache._ref, table_p, start_p, count_p), (o.data_ptr(), _lse_ptr(lse, B, Hq, Sq)),
+            (B, Hq, Hkv, Sq, D, width, _strides(q), lo, scale), ws)
+
+
+def sdpa_fwd_paged_window(q, cache: PagedCache, block_table, start, count=None, o=None, lse=None, *, window: int,
+                          sinks: int = 0, scale: float | None = None, workspace=None, stream=None) -> torch.Tensor:
+    """:func:`sdpa_fwd_paged` with a sliding window: query i < count[b] of
+    sequence b stands at position start[b] + i and sees positions up to its own
+    that are less than ``window`` behind it or below ``sinks``.  Pages without
+    such a position are not looked up: their entries in the block table may
+    hold anything."""
+    dev, o, args, out, sizes, ws = _paged_args(q, cache, block_table, start, count, o, lse, scale, workspace, stream)
+    _call(dev, (_cache._lib or _cache._bound()).sdpa_fwd_paged_window, *args, *out, *sizes, window, sinks, _DTYPE.get(q.dtype, 99), *ws,
+          _stream_ptr(stream, dev))
+    return o
+
+
+def tree_mask(parents: torch.Tensor) -> torch.Tensor:
+    """The mask of :func:`sdpa_fwd_paged_tree` (int32 [B, T, ceil(T / 32)]) for
+    drafts given by their parents (integers [B, T]; parents[b, i] < i, negative
+    for a token right behind the text): each token sees itself and those on its
+    way to the text."""
+    B, T = parents.shape
+    parents = parents.long()
+    sees = torch.zeros((B, T, T), dtype=torch.bool, device=parents.device)
+    for i in range(T):
+        up = parents[:, i:i + 1]
+        sees[:, i, i] = True
+        if i:
+            above = sees.gather(1, up.clamp(0, i - 1)[:, :, None].expand(B, 1, T))[:, 0]
+            sees[:, i] |= above & (up >= 0)
+    words = (T + 31) // 32
+    bits = torch.zeros((B, T, 32 * words), dtype=torch.int64, device=parents.device)
+    bits[:, :, :T] = sees
+    packed = (bits.unflatten(2, (words, 32)) << torch.arange(32, device=parents.device)).sum(-1)
+    return torch.where(packed >= 1 << 31, packed - (1 << 32), packed).to(torch.int32)
+
+
+def sdpa_fwd_paged_tree(q, cache: PagedCache, block_table, start, mask, count=None, o=None, lse=None, *,
+                        scale: float | None = None, workspace=None, stream=None) -> torch.Tensor:
+    """Attention of drafted tokens over the cache: q [B, T, Hq, D] holds the
+    count[b] drafted tokens of sequence b (None: T each), whose keys and values
+    lie at positions start[b] + i.  Each sees positions 0 .. start[b] - 1 and
+    the drafted tokens j whose bit (bit j % 32 of word j / 32) is set in
+    mask[b, i] (int32 [B, T, ceil(T / 32)], see :func:`tree_mask`), itself only
+    with its own bit.  Other arguments as for :func:`sdpa_fwd_paged`."""
+    dev, o, args, out, sizes, ws = _paged_args(q, cache, block_table, start, count, o, lse, scale, workspace, stream)
+    shape = (q.shape[0], q.shape[1], (q.shape[1] + 31) // 32)
+    if mask.get_device() != dev or mask.dtype != torch.int32 or mask.shape != shape or not mask.is_contiguous():
+        raise ValueError(f"mask must be a contiguous int32 tensor {list(shape)} on the cache's device")
+    _call(dev, (_cache._lib or _cache._bound()).sdpa_fwd_paged_tree, *args, mask.data_ptr(), *out, *sizes, _DTYPE.get(q.dtype, 99), *ws,
+          _stream_ptr(stream, dev))
+    return o
