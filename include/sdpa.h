@@ -521,6 +521,61 @@ sdpa_status_t sdpa_fwd_paged_tree(const void *Q, const sdpa_cache_t *cache,
 /* Workspace bytes sdpa_fwd_paged, sdpa_fwd_paged_window and sdpa_fwd_paged_tree need (0 for invalid sizes). */
 size_t sdpa_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D);
 
+/*
+ * How much attention the keys of a paged cache draw: for each key j of sequence
+ * b and KV head h,
+ *     score_out[b][h][j] = (j < start[b] ? score[b][h][j] : 0)
+ *                          + sum exp(s_j - LSE)
+ * over the rows (query i < count[b], query head of h's group) that see it: the
+ * weights of sdpa_fwd_paged(Q, cache, ...), called with the same arguments, whose
+ * LSE this takes.  Keys j >= start[b] are new and have drawn nothing before.
+ *   LSE       device, read only, fp32 [B][Hq][Sq].
+ *   score     device, read only, fp32 [B][Hkv] rows of score_stride numbers, or
+ *             NULL for zeros.
+ *   score_out device, written, like score; may be score.  Numbers at
+ *             start[b] + count[b] and behind are left as they are.
+ * Keys in pages outside the pool are left out (device error word 0x601), so are
+ * positions outside the block table or at score_stride and behind (0x602).
+ * Weights are fp32, their sum is taken in an order that the sizes give.  Other
+ * arguments, numbers of the scores and statuses as for sdpa_fwd_paged (elements of Q
+ * are exact where Sq * Hq / Hkv > 16).
+ */
+sdpa_status_t sdpa_cache_weights(const void *Q, const sdpa_cache_t *cache,
+                                 const int *block_table, const int *start, const int *count,
+                                 const float *LSE, const float *score, float *score_out,
+                                 int B, int Hq, int Hkv, int Sq, int D, int max_pages, long long score_stride,
+                                 const sdpa_layout_t *q_layout, float scale, int causal,
+                                 sdpa_dtype_t dtype, void *stream);
+
+/*
+ * Brings the sequences of a paged cache down to `budget` tokens, for each KV
+ * head by itself: of sequence b's length[b] tokens the first `sinks` stay, the
+ * last `recent`, and of those between the ones with the largest scores, as many
+ * as the budget has room for (of equal ones the earlier; NaN counts as the
+ * largest).  They keep their order and go to positions 0 .. of new pages; a
+ * sequence of at most `budget` tokens stays whole.  Afterwards a sequence has
+ * min(length[b], budget) tokens, and its table is new_table.
+ *   length    device, int32 [B].
+ *   score     device, read only, fp32 [B][Hkv] rows of score_stride numbers.
+ *   new_table device, int32 [B][new_max_pages]: pages that no sequence uses
+ *             and that stand here once; new_max_pages * page_size >= budget.
+ *   kept      device, written, int32 [B][Hkv][budget]: where a token was before.
+ *   kept_score   device, written, fp32 like kept: its score; or NULL.
+ * Entries behind a sequence's tokens are left as they are, in the new pages too.
+ * A new page's scale is the smallest power of two s with max|x| <= 448 s over
+ * its tokens, as if they had been appended; codes are rounded to it (nearest,
+ * ties to even; exact but for those that become subnormal).  The old pages
+ * are only read and may be shared between sequences.
+ *   sinks + recent <= budget.
+ * A token whose old page lies outside the pool becomes zero, a new page outside
+ * it is not written (device error word 0x601); of a sequence longer than its
+ * table or its row of scores the rest is left out (0x602).
+ */
+sdpa_status_t sdpa_cache_evict(const sdpa_cache_t *cache, const int *block_table, const int *length,
+                               const float *score, const int *new_table, int *kept, float *kept_score,
+                               int B, int Hkv, int D, int max_pages, int new_max_pages, long long score_stride,
+                               int sinks, int recent, int budget, void *stream);
+
 /* Static, human-readable name of a status code. */
 const char *sdpa_status_string(sdpa_status_t status);
 

@@ -20,7 +20,8 @@ __all__ = ["sdpa_fwd", "sdpa_fwd_fp8", "sdpa_fwd_ex", "sdpa_fwd_fp8_ex", "sdpa_f
            "decode_workspace_bytes", "sdpa_status_string", "sdpa_device_error", "SdpaError", "lib",
            "rope_table", "sdpa_qk_norm_rope", "sdpa_qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_bytes",
            "PagedCache", "sdpa_cache_append", "sdpa_fwd_paged", "paged_workspace_bytes",
-           "sdpa_fwd_window", "sdpa_bwd_window", "sdpa_fwd_paged_window", "sdpa_fwd_paged_tree", "tree_mask"]
+           "sdpa_fwd_window", "sdpa_bwd_window", "sdpa_fwd_paged_window", "sdpa_fwd_paged_tree", "tree_mask",
+           "sdpa_cache_weights", "sdpa_cache_evict"]
 
 _DTYPE = {torch.bfloat16: _abi.SDPA_DTYPE_BF16, torch.float16: _abi.SDPA_DTYPE_FP16}
 
@@ -329,3 +330,4 @@ from .cache import (PagedCache, paged_workspace_bytes, qk_norm_rope_bwd_workspac
                     sdpa_cache_append, sdpa_fwd_paged, sdpa_qk_norm_rope, sdpa_qk_norm_rope_bwd)
 from .masked import (sdpa_bwd_window, sdpa_fwd_paged_tree, sdpa_fwd_paged_window, sdpa_fwd_window,  # noqa: E402
                      tree_mask)
+from .evict import sdpa_cache_evict, sdpa_cache_weights  # noqa: E402

@@ -18,7 +18,7 @@ EXPORTS = ("sdpa_fwd", "sdpa_fwd_fp8", "sdpa_fwd_ex", "sdpa_fwd_fp8_ex", "sdpa_f
            "sdpa_abi_version",
            "sdpa_qk_norm_rope", "sdpa_qk_norm_rope_bwd", "sdpa_qk_norm_rope_bwd_workspace_bytes", "sdpa_cache_append",
            "sdpa_fwd_paged", "sdpa_paged_workspace_bytes", "sdpa_fwd_window", "sdpa_bwd_window",
-           "sdpa_fwd_paged_window", "sdpa_fwd_paged_tree")
+           "sdpa_fwd_paged_window", "sdpa_fwd_paged_tree", "sdpa_cache_weights", "sdpa_cache_evict")
 
 
 class Layout(ctypes.Structure):
@@ -95,6 +95,11 @@ def _bind(lib):
     lib.sdpa_fwd_paged_window.argtypes = [vp, cp, vp, vp, vp, vp, vp] + [i] * 6 + [lp, lp, f, i, i, i, vp, sz, vp]
     lib.sdpa_fwd_paged_tree.restype = i
     lib.sdpa_fwd_paged_tree.argtypes = [vp, cp, vp, vp, vp, vp, vp, vp] + [i] * 6 + [lp, lp, f, i, vp, sz, vp]
+    ll = ctypes.c_longlong
+    lib.sdpa_cache_weights.restype = i
+    lib.sdpa_cache_weights.argtypes = [vp, cp] + [vp] * 6 + [i] * 6 + [ll, lp, f, i, i, vp]
+    lib.sdpa_cache_evict.restype = i
+    lib.sdpa_cache_evict.argtypes = [cp] + [vp] * 6 + [i] * 5 + [ll, i, i, i, vp]
     lib.sdpa_paged_workspace_bytes.restype = sz
     lib.sdpa_paged_workspace_bytes.argtypes = [i] * 5
     lib.sdpa_status_string.restype = ctypes.c_char_p

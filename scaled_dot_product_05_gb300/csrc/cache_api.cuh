@@ -2,11 +2,14 @@
 // attention calls: argument checks and launches.
 #pragma once
 
+#include <algorithm>
 #include <mutex>
 #include <type_traits>
 
 #include "api_common.cuh"
 #include "cache_append.cuh"
+#include "cache_evict.cuh"
+#include "cache_weights.cuh"
 #include "paged_attn.cuh"
 #include "paged_wide.cuh"
 #include "qk_norm_rope.cuh"
@@ -316,6 +319,17 @@ sdpa::cache::Pool pool_of(void* codes, float* scale, const View& v)
     return {static_cast<uint8_t*>(codes), scale, v.st.b, v.st.s, v.st.h};
 }
 
+// Tensor map of a pool's codes, one head's part of a page a copy.  L2 fetches no
+// more than a slot's bytes where the slots of a head lie apart: 256-byte fetches
+// would bring in the neighbour head's half each time.
+bool map_of_codes(CUtensorMap* m, const View& v)
+{
+    return make_map(m, v.base, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, v.D, v.H, v.S, v.B, v.st, 1, v.S,
+                    v.st.s == v.D  ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                    : v.D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                 : CU_TENSOR_MAP_L2_PROMOTION_L2_64B);
+}
+
 template <int D, bool kBF16, bool kInter>
 cudaError_t launch_append(const sdpa::cache::AppendParams& p, cudaStream_t stream)
 {
@@ -417,6 +431,90 @@ cudaError_t launch_paged_mask(int D, bool bf16, int nr, const CUtensorMap& tk, c
                     : launch_paged_rows<64, false, MASK>(nr, tk, tv, p, dev, s);
     return bf16 ? launch_paged_rows<128, true, MASK>(nr, tk, tv, p, dev, s)
                 : launch_paged_rows<128, false, MASK>(nr, tk, tv, p, dev, s);
+}
+
+// Kernel, its dynamic shared memory allowed once per device.
+template <typename... KArgs>
+cudaError_t allow_smem(void (*kernel)(KArgs...), int bytes, int dev, std::once_flag* once, cudaError_t* err)
+{
+    std::call_once(once[dev], [&] { err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+    return err[dev];
+}
+
+template <int D, bool kBF16, int NR>
+cudaError_t launch_weights(const CUtensorMap& tk, const sdpa::weights::WeightParams& wp, int dev, cudaStream_t stream)
+{
+    using L = sdpa::weights::NarrowLayout<D, kBF16, NR>;
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t err[kMaxDevices];
+    const cudaError_t e = allow_smem(sdpa::weights::weights_kernel<D, kBF16, NR>, L::kSmemBytes, dev, once, err);
+    return e != cudaSuccess ? e
+                            : launch_pdl(true, sdpa::weights::weights_kernel<D, kBF16, NR>, dim3(wp.p.ctas), dim3(L::kThreads),
+                                         L::kSmemBytes, stream, tk, wp);
+}
+
+template <int D, bool kBF16>
+cudaError_t launch_weights_rows(int nr, const CUtensorMap& tk, const CUtensorMap& tq, const sdpa::weights::WeightParams& wp,
+                                int dev, cudaStream_t stream)
+{
+    if (nr == 8)
+        return launch_weights<D, kBF16, 8>(tk, wp, dev, stream);
+    if (nr == 16)
+        return launch_weights<D, kBF16, 16>(tk, wp, dev, stream);
+    using L = sdpa::weights::ManyLayout<D, kBF16>;
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t err[kMaxDevices];
+    const cudaError_t e = allow_smem(sdpa::weights::weights_many_kernel<D, kBF16>, L::kSmemBytes, dev, once, err);
+    return e != cudaSuccess ? e
+                            : launch_pdl(true, sdpa::weights::weights_many_kernel<D, kBF16>, dim3(wp.p.ctas), dim3(L::kThreads),
+                                         L::kSmemBytes, stream, tk, tq, wp);
+}
+
+template <int D>
+cudaError_t launch_evict(const sdpa::evict::EvictParams& p, cudaStream_t stream)
+{
+    using namespace sdpa::evict;
+    // as many CTAs a row as hold the longest sequence's keys in registers
+    const long long longest = std::min(static_cast<long long>(p.max_pages) * p.page, p.stride);
+    int ranks = 1;
+    while (ranks < 8 && static_cast<long long>(ranks) * kSelectThreads * kSelectKeys < longest)
+        ranks *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Hkv * ranks));
+    cfg.blockDim = dim3(kSelectThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(ranks);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, select_kernel, p);
+    if (e == cudaSuccess)
+        e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    const long long units = static_cast<long long>(p.B) * p.n_ord * 2 * p.Hkv;
+    auto move = [&](auto threads, auto passes) {
+        constexpr int kUnit = decltype(threads)::value, kPasses = decltype(passes)::value;
+        constexpr int kUnits = kMoveThreads / kUnit;
+        return launch_pdl(true, move_kernel<D, kUnit, kPasses>, dim3(static_cast<unsigned>((units + kUnits - 1) / kUnits)),
+                          dim3(kMoveThreads), 0, stream, p);
+    };
+    using std::integral_constant;
+    // 64 .. 512 pieces of 16 bytes at D = 64, 128 .. 1024 at 128
+    const int pieces = p.page * (D / 16);
+    if constexpr (D == 64)
+        if (pieces <= 64)
+            return move(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    if constexpr (D == 128)
+        if (pieces > 512)
+            return move(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+    return pieces <= 128   ? move(integral_constant<int, 128>{}, integral_constant<int, 1>{})
+           : pieces <= 256 ? move(integral_constant<int, 256>{}, integral_constant<int, 1>{})
+                           : move(integral_constant<int, 256>{}, integral_constant<int, 2>{});
 }
 
 // What the rows of a call over the cache see.
@@ -636,17 +734,8 @@ sdpa_status_t run_paged(const void* Q, const sdpa_cache_t* cache, const int* blo
     p.ctas_inverse = ~0ull / p.ctas + 1;
     p.part_lse = p.part_o + static_cast<long long>(p.ctas) * 2 * nr * D;
     p.joins = reinterpret_cast<int4*>(p.part_lse + static_cast<long long>(p.ctas) * 2 * nr);
-    // L2 fetches no more than a slot's bytes where the slots of a head lie
-    // apart: 256-byte fetches would bring in the neighbour head's half each
-    // time
-    auto map = [&](CUtensorMap* m, const void* base, const Strides& st) {
-        return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, Hkv, p.page, p.n_pages, st, 1, p.page,
-                        st.s == D    ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
-                        : D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
-                                   : CU_TENSOR_MAP_L2_PROMOTION_L2_64B);
-    };
     CUtensorMap tk, tv;
-    if (!map(&tk, cache->k, ck.st) || !map(&tv, cache->v, cv.st))
+    if (!map_of_codes(&tk, ck) || !map_of_codes(&tv, cv))
         return cuda_fail(cudaErrorInvalidValue);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == SDPA_DTYPE_BF16;
@@ -694,6 +783,161 @@ sdpa_status_t sdpa_fwd_paged_tree(const void* Q, const sdpa_cache_t* cache, cons
         return SDPA_ERR_MISALIGNED;
     return run_paged(Q, cache, block_table, start, count, O, LSE, B, Hq, Hkv, Sq, D, max_pages, q_layout, o_layout, scale,
                      PagedMask{sdpa::paged::kTree, 0, 0, 0, tree_mask}, dtype, workspace, workspace_bytes, stream);
+}
+
+sdpa_status_t sdpa_cache_weights(const void* Q, const sdpa_cache_t* cache, const int* block_table, const int* start,
+                                 const int* count, const float* LSE, const float* score, float* score_out, int B, int Hq,
+                                 int Hkv, int Sq, int D, int max_pages, long long score_stride,
+                                 const sdpa_layout_t* q_layout, float scale, int causal, sdpa_dtype_t dtype, void* stream)
+{
+    if (dtype != SDPA_DTYPE_BF16 && dtype != SDPA_DTYPE_FP16)
+        return SDPA_ERR_DTYPE;
+    if (!Q || !LSE || !score_out)
+        return SDPA_ERR_NULL_PTR;
+    if (!aligned16(Q) || !aligned(LSE, 4) || !aligned(score, 4) || !aligned(score_out, 4))
+        return SDPA_ERR_MISALIGNED;
+    View ck, cv;
+    sdpa_status_t st = check_cache(cache, block_table, start, count, B, Hkv, D, max_pages, &ck, &cv);
+    if (st != SDPA_OK)
+        return st;
+    if (Sq < 1 || Hq < 1 || score_stride < 1 || score_stride > 1ll << 30)
+        return SDPA_ERR_BAD_SHAPE;
+    if (Hq % Hkv != 0)
+        return SDPA_ERR_HEADS;
+    if (static_cast<__int128>(B) * Sq * Hq > INT32_MAX || static_cast<__int128>(B) * Hkv * score_stride > 1ll << 60)
+        return SDPA_ERR_BAD_SHAPE;
+    const float scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+    if (!valid_scale(scale) || !std::isfinite(scale_log2))
+        return SDPA_ERR_SCALE;
+    const View q{Q, resolve(q_layout, Sq, Hq, D), B, Sq, Hq, D, 2};
+    if (!view_ok(q))
+        return SDPA_ERR_LAYOUT;
+    // the sums lie apart from every input, but may take the place of the old ones
+    const long long sum_bytes = 4ll * B * Hkv * score_stride, sc = static_cast<long long>(cache->n_pages) * Hkv * 4;
+    const Flat flat[] = {{cache->k, ck.span()}, {cache->v, cv.span()}, {cache->k_scale, sc}, {cache->v_scale, sc},
+                         {block_table, 4ll * B * max_pages}, {start, 4ll * B}, {count, 4ll * B}, {Q, q.span()},
+                         {LSE, 4ll * B * Hq * Sq}, {score == score_out ? nullptr : score, sum_bytes}};
+    for (const Flat& f : flat)
+        if (f.p && overlaps(score_out, sum_bytes, f.p, f.n))
+            return SDPA_ERR_ALIAS;
+
+    int dev = 0, sm_count = 0;
+    st = device_ready(&dev, &sm_count);
+    if (st != SDPA_OK)
+        return st;
+    sdpa::weights::WeightParams wp{};
+    sdpa::paged::Params& p = wp.p;
+    p.Q = Q;
+    p.q_sb = q.st.b, p.q_ss = q.st.s, p.q_sh = q.st.h;
+    p.k = pool_of(cache->k, cache->k_scale, ck);
+    p.table = block_table;
+    p.start = start;
+    p.count = count;
+    p.B = B;
+    p.Sq = Sq;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.group = Hq / Hkv;
+    p.page = cache->page_size;
+    p.n_pages = cache->n_pages;
+    p.max_pages = max_pages;
+    p.causal = causal ? 1 : 0;
+    p.scale_log2 = scale_log2;
+    p.page_shift = p.page == 16 ? 4 : p.page == 32 ? 5 : p.page == 64 ? 6 : 7;
+    p.row_tiles = 1;
+    const int nr = paged_tile_rows(Sq, p.group);
+    const __int128 most = static_cast<__int128>(B) * Hkv *
+                          ((static_cast<long long>(max_pages) * p.page + sdpa::paged::kTileKeys - 1) / sdpa::paged::kTileKeys);
+    p.ctas = (nr == sdpa::paged::kWideRows ? 1 : 2) * sm_count;
+    p.ctas = most < p.ctas ? static_cast<int>(most) : p.ctas;
+    p.ctas_inverse = ~0ull / p.ctas + 1;
+    wp.lse = LSE;
+    wp.score = score;
+    wp.out = score_out;
+    wp.stride = score_stride;
+    wp.heads_per = p.group < 128 ? p.group : 128;
+    wp.tok_per = 128 / wp.heads_per;
+    wp.head_blocks = (p.group + wp.heads_per - 1) / wp.heads_per;
+    CUtensorMap tk, tq{};
+    if (!map_of_codes(&tk, ck))
+        return cuda_fail(cudaErrorInvalidValue);
+    const bool bf16 = dtype == SDPA_DTYPE_BF16;
+    if (nr == sdpa::paged::kWideRows &&
+        !make_map(&tq, Q, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, D, Hq, Sq, B, q.st,
+                  wp.heads_per, wp.tok_per))
+        return cuda_fail(cudaErrorInvalidValue);
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = D == 64 ? (bf16 ? launch_weights_rows<64, true>(nr, tk, tq, wp, dev, cs)
+                                          : launch_weights_rows<64, false>(nr, tk, tq, wp, dev, cs))
+                                  : (bf16 ? launch_weights_rows<128, true>(nr, tk, tq, wp, dev, cs)
+                                          : launch_weights_rows<128, false>(nr, tk, tq, wp, dev, cs));
+    return e == cudaSuccess ? SDPA_OK : cuda_fail(e);
+}
+
+sdpa_status_t sdpa_cache_evict(const sdpa_cache_t* cache, const int* block_table, const int* length, const float* score,
+                               const int* new_table, int* kept, float* kept_score, int B, int Hkv, int D, int max_pages,
+                               int new_max_pages, long long score_stride, int sinks, int recent, int budget, void* stream)
+{
+    if (!score || !new_table || !kept)
+        return SDPA_ERR_NULL_PTR;
+    if (!aligned(score, 4) || !aligned(new_table, 4) || !aligned(kept, 4) || !aligned(kept_score, 4))
+        return SDPA_ERR_MISALIGNED;
+    View ck, cv;
+    const sdpa_status_t bad = check_cache(cache, block_table, length, nullptr, B, Hkv, D, max_pages, &ck, &cv);
+    if (bad != SDPA_OK)
+        return bad;
+    const int page = cache->page_size;
+    if (score_stride < 1 || score_stride > 1ll << 30 || sinks < 0 || recent < 0 || budget < 1 || new_max_pages < 1 ||
+        static_cast<long long>(sinks) + recent > budget || static_cast<long long>(new_max_pages) * page < budget)
+        return SDPA_ERR_BAD_SHAPE;
+    const int n_ord = (budget - 1) / page + 1;
+    if (static_cast<__int128>(B) * n_ord * 2 * Hkv > INT32_MAX || static_cast<__int128>(B) * Hkv * 8 > INT32_MAX)
+        return SDPA_ERR_BAD_SHAPE;
+    if (!injective(ck.st, ck.B, ck.S, Hkv, D) || !injective(cv.st, cv.B, cv.S, Hkv, D))
+        return SDPA_ERR_LAYOUT;
+    // what is written lies apart from everything else (in the pool, the new pages from those that are read)
+    const long long sc = static_cast<long long>(cache->n_pages) * Hkv * 4, keep_bytes = 4ll * B * Hkv * budget;
+    const Flat flat[] = {{block_table, 4ll * B * max_pages}, {new_table, 4ll * B * new_max_pages}, {length, 4ll * B},
+                         {score, 4ll * B * Hkv * score_stride}, {kept, keep_bytes}, {kept_score, keep_bytes},
+                         {cache->k_scale, sc}, {cache->v_scale, sc}};
+    if (!disjoint(ck, cv))
+        return SDPA_ERR_ALIAS;
+    for (int i = 0; i < 8; ++i) {
+        if (!disjoint_bytes(ck, flat[i]) || !disjoint_bytes(cv, flat[i]))
+            return SDPA_ERR_ALIAS;
+        for (int j = 0; j < i && i > 3; ++j)
+            if (flat[i].p && flat[j].p && overlaps(flat[i].p, flat[i].n, flat[j].p, flat[j].n))
+                return SDPA_ERR_ALIAS;
+    }
+
+    int dev = 0, sm_count = 0;
+    const sdpa_status_t st = device_ready(&dev, &sm_count);
+    if (st != SDPA_OK)
+        return st;
+    sdpa::evict::EvictParams p{};
+    p.pool[0] = pool_of(cache->k, cache->k_scale, ck);
+    p.pool[1] = pool_of(cache->v, cache->v_scale, cv);
+    p.table = block_table;
+    p.new_table = new_table;
+    p.length = length;
+    p.score = score;
+    p.kept = kept;
+    p.kept_score = kept_score;
+    p.stride = score_stride;
+    p.B = B;
+    p.Hkv = Hkv;
+    p.page = page;
+    p.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
+    p.n_pages = cache->n_pages;
+    p.max_pages = max_pages;
+    p.new_max_pages = new_max_pages;
+    p.sinks = sinks;
+    p.recent = recent;
+    p.budget = budget;
+    p.n_ord = n_ord;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = D == 64 ? launch_evict<64>(p, cs) : launch_evict<128>(p, cs);
+    return e == cudaSuccess ? SDPA_OK : cuda_fail(e);
 }
 
 size_t sdpa_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D)

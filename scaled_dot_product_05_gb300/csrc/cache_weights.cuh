@@ -1,0 +1,744 @@
+// cache_weights.cuh -- how much attention the keys of a paged cache draw.
+//
+// For key j of sequence b and KV head h, over the rows (token i < count[b],
+// query head of the group) that see it,
+//     out_j = (j < start[b] ? score_j : 0) + sum exp(s_j - LSE),
+//     s_j = scale * k_scale(page of j) * (q . k8_j),
+// with the LSE that the attention over the same cache has given: the softmax's
+// weights, summed over the rows.  A key that is new (j >= start[b]) has drawn
+// nothing before.  With the LSE known a key tile needs no other: there is no
+// running maximum and nothing to join, and a thread has one key and adds up its
+// rows, in an order that the sizes give.
+//
+// Two kernels, as for the attention.  Up to 16 rows (a decoding step): the
+// codes go to the FP8 tensor cores as they lie in the cache, the rows in two or
+// three 8-bit parts (see paged_attn.cuh for why these are exact); bound by
+// reading K.  More rows: a tile's codes are turned into the queries' 16-bit
+// type, which holds them exactly, once, and meet the queries as they are, 128
+// rows at a time; bound by the exponentials (128 x 128 of them a tile of rows:
+// 1024 cycles of an SM).
+#pragma once
+
+#include "paged_attn.cuh"
+
+namespace sdpa {
+namespace weights {
+
+using namespace paged;
+
+struct WeightParams {
+    paged::Params p;                 // (its O, lse, v and workspace are not used)
+    const float* lse;                // [B][Hq][Sq]
+    const float* score;              // [B][Hkv][stride], or null
+    float* out;                      // the same, may be score
+    long long stride;
+    int heads_per, tok_per, head_blocks;    // many rows: heads and tokens of a row tile, tiles that a token's heads need
+};
+
+enum : unsigned int { kErrWeightsLoad = 0x831, kErrWeightsMma = 0x841, kErrWeightsSum = 0x851 };
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// A row's LSE in log2 units; +inf (no weight) for a row that sees no key.
+__device__ __forceinline__ float row_lse2(float lse)
+{
+    return lse == -INFINITY ? INFINITY : lse * kLog2e;
+}
+
+// ------------------------------------------------------------ up to 16 rows --
+
+template <int D, bool kBF16, int NR>
+struct NarrowLayout {
+    static constexpr int kParts = kBF16 ? 2 : 3;
+    static constexpr int kGroups = 2;
+    static constexpr int kSoftmax = 128 * kGroups;
+    static constexpr int kThreads = kSoftmax + 64;              // then TMA producer, MMA issuer
+    static constexpr int kTileBytes = kTileKeys * D;
+    static constexpr int kStages = D == 64 ? 10 : 6;
+    static constexpr int kQRows = 16;
+    static constexpr int kQPartBytes = kQRows * D;
+    static constexpr int kOffK = 0;
+    static constexpr int kOffQ = kOffK + kStages * kTileBytes;
+    static constexpr int kOffRows = kOffQ + kParts * kQPartBytes;       // per row: scale, LSE, last key
+    static constexpr int kOffBar = kOffRows + 3 * 4 * kQRows;
+    static constexpr int kBarBytes = 448;
+    static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;
+    static_assert(2 * (kSmemBytes + 1024) <= 233472, "two CTAs per SM");
+    static constexpr uint32_t kTmemCols = 32;
+};
+
+template <int NK>
+struct NarrowBarriers {
+    uint64_t k_full[NK], k_empty[NK];
+    uint64_t s_full[2], s_free[2], q_full, drain;
+    uint32_t tmem_base;
+    int abort;
+    long long total, x, x_first;
+    long long warp_sums[12];
+};
+
+template <int D, bool kBF16, int NR>
+__global__ void __launch_bounds__(NarrowLayout<D, kBF16, NR>::kThreads, 2)
+weights_kernel(const __grid_constant__ CUtensorMap tm_k, const WeightParams wp)
+{
+    using L = NarrowLayout<D, kBF16, NR>;
+    constexpr int NK = L::kStages, QP = L::kParts, MASK = kPlain, G = L::kGroups;
+    constexpr int kProducer = L::kSoftmax / 32, kIssuer = kProducer + 1;
+    constexpr uint32_t kBarAll = 1;
+    using Bars = NarrowBarriers<NK>;
+    const paged::Params& p = wp.p;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    auto* bars = reinterpret_cast<Bars*>(smem + L::kOffBar);
+    static_assert(sizeof(Bars) <= L::kBarBytes, "barrier block");
+    volatile int* abort = &bars->abort;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const int lane = threadIdx.x & 31;
+    const uint32_t sK = smem_u32(smem + L::kOffK), sQ = smem_u32(smem + L::kOffQ);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NK; ++i) {
+            mbar_init(smem_u32(&bars->k_full[i]), 1);
+            mbar_init(smem_u32(&bars->k_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bars->s_full[i]), 1);
+            mbar_init(smem_u32(&bars->s_free[i]), 128);
+        }
+        mbar_init(smem_u32(&bars->q_full), L::kSoftmax);
+        mbar_init(smem_u32(&bars->drain), 1);
+        bars->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kProducer && lane == 0)
+        tma_prefetch_map(&tm_k);
+    if (warp == kIssuer) {
+        tmem_alloc(smem_u32(&bars->tmem_base), L::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = bars->tmem_base;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    find_share<NR, MASK, L::kThreads>(p, blockIdx.x, bars);
+
+    Piece w;
+    bool more = first_piece<NR, MASK>(p, bars, w);
+    if (warp == kProducer) {
+        // =========================== TMA producer ===========================
+        const int ppt = kTileKeys >> p.page_shift;
+        uint32_t n = 0;
+        bool ok = true;
+        for (; ok && more; more = next_piece<NR, MASK>(p, w)) {
+            const Item it = item_of<NR, MASK>(p, w);
+            auto entry_of = [&](int tile) -> int {
+                const int ord = tile * ppt + lane;
+                return lane < ppt && tile < w.end && ord << p.page_shift < it.keys
+                           ? p.table[(long long)it.b * p.max_pages + ord]
+                           : -1;
+            };
+            int ahead[3] = {entry_of(w.begin), entry_of(w.begin + 1), entry_of(w.begin + 2)};
+            for (int j = w.begin; ok && j < w.end; ++j, ++n) {
+                const int id = (unsigned)ahead[0] < (unsigned)p.n_pages ? ahead[0] : -1;
+                ahead[0] = ahead[1];
+                ahead[1] = ahead[2];
+                ahead[2] = entry_of(j + 3);
+                const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * p.page * D;
+                const uint32_t ks = n % NK;
+                if (n >= NK)
+                    ok = wait_bar(smem_u32(&bars->k_empty[ks]), (n / NK - 1) & 1, abort, kErrWeightsLoad);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(smem_u32(&bars->k_full[ks]), bytes);
+                __syncwarp();
+                if (id >= 0)
+                    tma_load_4d(sK + ks * L::kTileBytes + lane * p.page * D, &tm_k, smem_u32(&bars->k_full[ks]), 0, w.h, 0, id);
+            }
+        }
+        if (lane == 0)                                     // never leave with copies in flight
+            for (uint32_t i = n > NK ? n - NK : 0; i < n; ++i)
+                drain_wait(smem_u32(&bars->k_full[i % NK]), (i / NK) & 1);
+        __syncwarp();
+    } else if (warp == kIssuer) {
+        // ============================ MMA issuer ============================
+        if (lane == 0) {
+            constexpr uint32_t kSwzCode = D == 128 ? 2u : 4u;
+            constexpr uint32_t idesc_s = idesc_make(0u, kTileKeys, L::kQRows, false);
+            const uint32_t hi = (uint32_t)(smem_desc(0, 16, 8 * D, kSwzCode) >> 32);
+            uint32_t n = 0, pieces = 0, n0 = 0, n1 = 0;    // tiles; of each warpgroup
+            bool ok = true;
+            for (; ok && more; more = next_piece<NR, MASK>(p, w), ++pieces) {
+                ok = wait_bar(smem_u32(&bars->q_full), pieces & 1, abort, kErrWeightsMma);
+                for (int j = w.begin; ok && j < w.end; ++j, ++n) {
+                    const int g = (j - w.begin) & 1;
+                    const uint32_t ks = n % NK, done = g ? n1 : n0;
+                    ok = wait_bar(smem_u32(&bars->k_full[ks]), (n / NK) & 1, abort, kErrWeightsMma + 1) &&
+                         (done == 0 || wait_bar(smem_u32(&bars->s_free[g]), (done - 1) & 1, abort, kErrWeightsMma + 2));
+                    if (!ok)
+                        break;
+                    tc_fence_after_sync();
+                    const uint32_t k_lo = ((sK + ks * L::kTileBytes) >> 4) | (1u << 16);
+#pragma unroll
+                    for (int q = 0; q < QP; ++q) {
+                        const uint32_t q_lo = ((sQ + q * L::kQPartBytes) >> 4) | (1u << 16);
+                        const uint32_t idesc = idesc_s | (q + 1 == QP ? 1u << 10 : 0u);             // q (B): E5M2 in the end
+#pragma unroll
+                        for (int kk = 0; kk < D / 32; ++kk)
+                            mma_f8_ss(tmem + g * L::kQRows, desc_join(hi, k_lo + 2 * kk), desc_join(hi, q_lo + 2 * kk), idesc,
+                                      q > 0 || kk > 0);
+                    }
+                    mma_commit(smem_u32(&bars->s_full[g]));
+                    mma_commit(smem_u32(&bars->k_empty[ks]));
+                    n0 += g ? 0 : 1;
+                    n1 += g ? 1 : 0;
+                }
+            }
+            mma_commit(smem_u32(&bars->drain));
+            drain_wait(smem_u32(&bars->drain), 0);
+        }
+        __syncwarp();
+    } else {
+        // ========================= one thread a key =========================
+        const int g = warp >> 2;
+        const int tid = threadIdx.x & 127;
+        float* row_scale = reinterpret_cast<float*>(smem + L::kOffRows);
+        float* row_lse = row_scale + L::kQRows;
+        int* row_last = reinterpret_cast<int*>(row_lse + L::kQRows);
+        const uint32_t t_s = tmem + ((uint32_t)((warp & 3) * 32) << 16) + g * L::kQRows;
+        uint32_t ns = 0;                                                    // tiles of this warpgroup so far
+        bool ok = true;
+        for (; more; more = next_piece<NR, MASK>(p, w)) {
+            const Item it = item_of<NR, MASK>(p, w);
+            // ---- q into 8-bit parts, and each row's numbers (as for the attention)
+            {
+                constexpr int kPer = L::kSoftmax / L::kQRows;
+                const int r = threadIdx.x / kPer, seg = threadIdx.x % kPer;
+                const bool live = r < it.rows;
+                const int i = r / p.group, hh = r % p.group;
+                const uint16_t* q = reinterpret_cast<const uint16_t*>(p.Q) + (long long)it.b * p.q_sb + (long long)i * p.q_ss +
+                                    (long long)(w.h * p.group + hh) * p.q_sh;
+                float v[16];
+                uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                if (live && seg < D / 16) {
+                    u[0] = reinterpret_cast<const uint4*>(q)[2 * seg];
+                    u[1] = reinterpret_cast<const uint4*>(q)[2 * seg + 1];
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    rope::unpack4<kBF16>(make_uint2(u[c].x, u[c].y), &v[8 * c]);
+                    rope::unpack4<kBF16>(make_uint2(u[c].z, u[c].w), &v[8 * c + 4]);
+                }
+                uint32_t top = 0;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+#pragma unroll
+                for (int m = 1; m < kPer; m <<= 1)
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+                const bool finite = top < 0x7f800000u;
+                const float qs = query_scale(top), inv = 1.f / qs;
+                const int chunk = D == 128 ? seg ^ (r & 7) : seg ^ ((r >> 1) & 3);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    v[e] *= inv;
+                if (seg < D / 16) {
+#pragma unroll
+                    for (int part = 0; part < QP; ++part) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            o[e / 4] = query_part(&v[e], part + 1 == QP);
+                        st_shared_v4(sQ + part * L::kQPartBytes + r * D + chunk * 16, o[0], o[1], o[2], o[3]);
+                    }
+                }
+                if (seg == 0 && r < NR) {
+                    const long long last = p.causal ? it.start + i : it.start + it.count - 1;
+                    row_scale[r] = finite ? qs * p.scale_log2 : NAN;
+                    row_lse[r] = live ? row_lse2(wp.lse[((long long)it.b * p.Hq + w.h * p.group + hh) * p.Sq + i]) : INFINITY;
+                    row_last[r] = !live || last < 0 ? -1 : (int)(last < it.keys ? last : it.keys - 1);
+                }
+                if (threadIdx.x == 0 && (it.start + it.count > (long long)p.max_pages * p.page || it.keys > wp.stride))
+                    atomicCAS(&g_sdpa_error, 0u, (unsigned)cache::kErrTable);
+                fence_proxy_async_smem();
+                named_bar_sync(kBarAll, L::kSoftmax);
+                mbar_arrive(smem_u32(&bars->q_full));
+            }
+            const int full = row_last[0] + 1;                               // every row sees keys 0 .. full - 1
+            const int* table = p.table + (long long)it.b * p.max_pages;
+            const long long at = ((long long)it.b * p.Hkv + w.h) * wp.stride;
+            auto entry_of = [&](int tile) -> int {
+                const int pos = tile * kTileKeys + tid;
+                return tile < w.end && pos < it.keys ? table[pos >> p.page_shift] : INT_MIN;
+            };
+            auto scale_of = [&](int entry, int tile, float& ks, float& old) -> bool {
+                ks = 1.f;
+                old = 0.f;
+                const bool in = (unsigned)entry < (unsigned)p.n_pages;
+                const int pos = tile * kTileKeys + tid;
+                if (in) {
+                    ks = p.k.scale[(long long)entry * p.Hkv + w.h];
+                    if (wp.score && pos < it.start && pos < wp.stride)
+                        old = wp.score[at + pos];
+                } else if (entry != INT_MIN) {
+                    atomicCAS(&g_sdpa_error, 0u, (unsigned)cache::kErrPage);
+                }
+                return in;
+            };
+            const int first = w.begin + g;
+            int entry = entry_of(first), entry_next = entry_of(first + G);
+            float ks_next, old_next;
+            bool valid_next = scale_of(entry, first, ks_next, old_next);
+            for (int j = first; j < w.end; j += G, ++ns) {
+                const bool valid = valid_next;
+                const float ks = ks_next;
+                float sum = old_next;
+                entry = entry_next;
+                entry_next = entry_of(j + 2 * G);
+                valid_next = scale_of(entry, j + G, ks_next, old_next);
+                ok = ok && wait_bar(smem_u32(&bars->s_full[g]), ns & 1, abort, kErrWeightsSum);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                tc_fence_after_sync();
+                uint32_t s[NR];
+                if constexpr (NR == 8)
+                    tmem_ld8_wait(t_s, s);
+                else
+                    tmem_ld16_wait(t_s, s);
+                tc_fence_before_sync();
+                mbar_arrive(smem_u32(&bars->s_free[g]));
+                const int pos = j * kTileKeys + tid;
+                const bool edge = (j + 1) * kTileKeys > full;
+                float x[NR];
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+                    x[r] = ex2_approx(fmaf(__uint_as_float(s[r]), row_scale[r] * ks, -row_lse[r]));
+                if (edge) {
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+                        x[r] = pos <= row_last[r] ? x[r] : 0.f;
+                }
+                // the rows in pairs, the old sum last
+#pragma unroll
+                for (int h = 1; h < NR; h <<= 1)
+#pragma unroll
+                    for (int r = 0; r + h < NR; r += 2 * h)
+                        x[r] += x[r + h];
+                sum += x[0];
+                if (valid && pos < wp.stride)
+                    wp.out[at + pos] = sum;
+            }
+            // both warpgroups have their last scores: q may be written anew
+            if (!named_bar_all(kBarAll, L::kSoftmax, ok))
+                break;
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == kIssuer) {
+        __syncwarp();
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, L::kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- many rows --
+
+template <int D, bool kBF16>
+struct ManyLayout {
+    static constexpr int kThreads = 320;   // 8 warps of keys; TMA producer, MMA issuer
+    static constexpr int kK8Bytes = kTileKeys * D;
+    static constexpr int kTileBytes = kTileKeys * D * 2;        // 16-bit K or Q tile
+    static constexpr int kStagesQ = D == 64 ? 4 : 3;
+    static constexpr int kOffK8 = 0;                            // 2 stages
+    static constexpr int kOffK16 = kOffK8 + 2 * kK8Bytes;       // 2
+    static constexpr int kOffQ = kOffK16 + 2 * kTileBytes;
+    static constexpr int kOffLse = kOffQ + kStagesQ * kTileBytes;       // [kStagesQ][128]
+    static constexpr int kOffPart = kOffLse + kStagesQ * 512;           // [2][128]: the second warpgroup's sums
+    static constexpr int kOffBar = kOffPart + 2 * 512;
+    static constexpr int kBarBytes = 512;
+    static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;
+    static_assert(kSmemBytes <= 232448, "shared memory budget");
+    static constexpr uint32_t kTmemCols = 256;                  // S of each warpgroup
+};
+
+template <int NQ>
+struct ManyBarriers {
+    uint64_t k8_full[2], k8_empty[2], k16_full[2], k16_empty[2];
+    uint64_t q_full[NQ], q_empty[NQ];
+    uint64_t s_full[2], s_free[2], drain;
+    uint32_t tmem_base;
+    int abort;
+};
+
+// A key tile of one KV head and the row tiles that see it.
+struct KeyUnit {
+    int b, h, tile;                  // b < 0: none
+    int count, keys;
+    long long start;
+    int rt0, rt1;                    // row tiles
+};
+
+// Unit number u of the call: sequences in order, in each its key tiles, in
+// each of those the KV heads.  A CTA takes every gridDim.x-th one, so that under
+// the causal mask the tiles that many rows see go round.  The sequences are looked
+// at 32 at a time, one a lane; whole warps call.
+struct UnitFinder {
+    int b0 = -32;
+    long long base = 0, incl = 0, total = 0;
+    int n = 0, start = 0, count = 0;
+
+    __device__ __forceinline__ KeyUnit find(const WeightParams& wp, long long u)
+    {
+        const paged::Params& p = wp.p;
+        const int lane = threadIdx.x & 31;
+        while (b0 < p.B && u >= base + total) {
+            base += total;
+            b0 += 32;
+            const int b = b0 + lane;
+            count = b >= p.B ? 0 : p.count ? max(0, min(p.Sq, p.count[b])) : p.Sq;
+            start = b < p.B ? p.start[b] : 0;
+            const long long cap = (long long)p.max_pages << p.page_shift;
+            const long long len = min((long long)start + count, cap);
+            n = count == 0 || len < 1 ? 0 : (int)((len + kTileKeys - 1) / kTileKeys);
+            incl = (long long)n * p.Hkv;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const long long o = __shfl_up_sync(0xffffffffu, incl, m);
+                if (lane >= m)
+                    incl += o;
+            }
+            total = __shfl_sync(0xffffffffu, incl, 31);
+            if (b < p.B && count > 0 && (long long)start + count > min(cap, wp.stride))
+                atomicCAS(&g_sdpa_error, 0u, (unsigned)cache::kErrTable);
+        }
+        KeyUnit k;
+        k.b = -1;
+        k.h = k.tile = k.count = k.keys = k.rt0 = k.rt1 = 0;
+        k.start = 0;
+        if (b0 >= p.B)
+            return k;
+        const int at = __ffs(__ballot_sync(0xffffffffu, u < base + incl)) - 1;
+        const long long before = base + __shfl_sync(0xffffffffu, incl - (long long)n * p.Hkv, at);
+        const long long off = u - before;
+        k.b = b0 + at;
+        k.tile = (int)(off / p.Hkv);
+        k.h = (int)(off - (long long)k.tile * p.Hkv);
+        k.start = __shfl_sync(0xffffffffu, start, at);
+        k.count = __shfl_sync(0xffffffffu, count, at);
+        k.keys = (int)min(k.start + k.count, (long long)p.max_pages << p.page_shift);
+        // the first token that sees the tile's first key
+        const long long i0 = p.causal ? max(0ll, (long long)k.tile * kTileKeys - k.start) : 0;
+        k.rt0 = (int)(i0 / wp.tok_per) * wp.head_blocks;
+        k.rt1 = (k.count + wp.tok_per - 1) / wp.tok_per * wp.head_blocks;
+        return k;
+    }
+};
+
+template <int D, bool kBF16>
+__global__ void __launch_bounds__(320, 1)
+weights_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q, const WeightParams wp)
+{
+    using L = ManyLayout<D, kBF16>;
+    constexpr int NQ = L::kStagesQ;
+    using Bars = ManyBarriers<NQ>;
+    const paged::Params& p = wp.p;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    auto* bars = reinterpret_cast<Bars*>(smem + L::kOffBar);
+    static_assert(sizeof(Bars) <= L::kBarBytes, "barrier block");
+    volatile int* abort = &bars->abort;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const int lane = threadIdx.x & 31;
+    const uint32_t sK8 = smem_u32(smem + L::kOffK8), sK16 = smem_u32(smem + L::kOffK16), sQ = smem_u32(smem + L::kOffQ);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bars->k8_full[i]), 1);
+            mbar_init(smem_u32(&bars->k8_empty[i]), 256);
+            mbar_init(smem_u32(&bars->k16_full[i]), 256);
+            mbar_init(smem_u32(&bars->k16_empty[i]), 1);
+            mbar_init(smem_u32(&bars->s_full[i]), 1);
+            mbar_init(smem_u32(&bars->s_free[i]), 128);
+        }
+        for (int i = 0; i < NQ; ++i) {
+            mbar_init(smem_u32(&bars->q_full[i]), 1);
+            mbar_init(smem_u32(&bars->q_empty[i]), 128 + 1);   // the warpgroup has read the LSE, the product the tile
+        }
+        mbar_init(smem_u32(&bars->drain), 1);
+        bars->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8 && lane == 0) {
+        tma_prefetch_map(&tm_k);
+        tma_prefetch_map(&tm_q);
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_u32(&bars->tmem_base), L::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = bars->tmem_base;
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    UnitFinder finder;
+    uint32_t units = 0, n = 0;                             // units and row tiles so far
+    bool ok = true;
+    if (warp == 8) {
+        // =========================== TMA producer ===========================
+        const int ppt = kTileKeys >> p.page_shift;
+        auto entry_of = [&](const KeyUnit& k) -> int {
+            const int ord = k.tile * ppt + lane;
+            return k.b >= 0 && lane < ppt && ord << p.page_shift < k.keys ? p.table[(long long)k.b * p.max_pages + ord] : -1;
+        };
+        KeyUnit k = finder.find(wp, blockIdx.x);
+        int entry = entry_of(k);
+        for (long long u = blockIdx.x; ok && k.b >= 0; u += gridDim.x, ++units) {
+            const KeyUnit next = finder.find(wp, u + gridDim.x);
+            const int id = (unsigned)entry < (unsigned)p.n_pages ? entry : -1;
+            entry = entry_of(next);
+            const uint32_t st = units & 1;
+            if (units >= 2)
+                ok = wait_bar(smem_u32(&bars->k8_empty[st]), (units / 2 - 1) & 1, abort, kErrWeightsLoad + 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok)
+                break;
+            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * p.page * D;
+            if (lane == 0)
+                mbar_arrive_expect_tx(smem_u32(&bars->k8_full[st]), bytes);
+            __syncwarp();
+            if (id >= 0)
+                tma_load_4d(sK8 + st * L::kK8Bytes + lane * p.page * D, &tm_k, smem_u32(&bars->k8_full[st]), 0, k.h, 0, id);
+            for (int rt = k.rt0; ok && rt < k.rt1; ++rt, ++n) {
+                const uint32_t qs = n % NQ;
+                const int tok0 = rt / wp.head_blocks * wp.tok_per, head0 = rt % wp.head_blocks * wp.heads_per;
+                // four rows' LSE a lane (before the wait, which they take their time in)
+                float z[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = 4 * lane + e, i = tok0 + c / wp.heads_per, hh = head0 + c % wp.heads_per;
+                    z[e] = c < wp.tok_per * wp.heads_per && i < k.count && hh < p.group
+                               ? row_lse2(wp.lse[((long long)k.b * p.Hq + k.h * p.group + hh) * p.Sq + i])
+                               : INFINITY;
+                }
+                if (n >= NQ)
+                    ok = wait_bar(smem_u32(&bars->q_empty[qs]), (n / NQ - 1) & 1, abort, kErrWeightsLoad + 2);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                reinterpret_cast<float4*>(smem + L::kOffLse + qs * 512)[lane] = make_float4(-z[0], -z[1], -z[2], -z[3]);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(smem_u32(&bars->q_full[qs]), wp.tok_per * wp.heads_per * D * 2);
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_4d(sQ + qs * L::kTileBytes + c * (kTileKeys * 128), &tm_q, smem_u32(&bars->q_full[qs]), c * 64,
+                                    k.h * p.group + head0, tok0, k.b);
+                }
+                __syncwarp();
+            }
+            k = next;
+        }
+        if (lane == 0) {
+            // (after an abort the copies at hand may not have been issued: at worst their wait runs out)
+            const uint32_t k_issued = ok ? units : units + 1;
+            for (uint32_t i = k_issued > 2 ? k_issued - 2 : 0; i < k_issued; ++i)
+                drain_wait(smem_u32(&bars->k8_full[i & 1]), (i / 2) & 1);
+            for (uint32_t i = n > NQ ? n - NQ : 0; i < n; ++i)
+                drain_wait(smem_u32(&bars->q_full[i % NQ]), (i / NQ) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ============================ MMA issuer ============================
+        constexpr uint32_t idesc = idesc_make(kBF16 ? 1u : 0u, kTileKeys, 128, false);
+        const uint32_t hi = (uint32_t)(smem_desc(0, 16, 1024, 2u) >> 32);
+        uint32_t n0 = 0, n1 = 0;
+        for (long long u = blockIdx.x; ok; u += gridDim.x, ++units) {
+            const KeyUnit k = finder.find(wp, u);
+            if (k.b < 0)
+                break;
+            const uint32_t ub = units & 1;
+            ok = wait_bar(smem_u32(&bars->k16_full[ub]), (units / 2) & 1, abort, kErrWeightsMma + 3);
+            const uint32_t k_lo = ((sK16 + ub * L::kTileBytes) >> 4) | (1u << 16);
+            for (int rt = k.rt0; ok && rt < k.rt1; ++rt, ++n) {
+                const uint32_t qs = n % NQ, g = n & 1, done = g ? n1 : n0;
+                ok = wait_bar(smem_u32(&bars->q_full[qs]), (n / NQ) & 1, abort, kErrWeightsMma + 4) &&
+                     (done == 0 || wait_bar(smem_u32(&bars->s_free[g]), (done - 1) & 1, abort, kErrWeightsMma + 5));
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                tc_fence_after_sync();
+                if (lane == 0) {
+                    const uint32_t q_lo = ((sQ + qs * L::kTileBytes) >> 4) | (1u << 16);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (uint32_t)((kk / 4 * (kTileKeys * 128) + kk % 4 * 32) >> 4);
+                        mma_f16_ss(tmem + g * 128, desc_join(hi, k_lo + off), desc_join(hi, q_lo + off), idesc, kk > 0);
+                    }
+                    mma_commit(smem_u32(&bars->s_full[g]));
+                    mma_commit(smem_u32(&bars->q_empty[qs]));
+                }
+                __syncwarp();
+                n0 += g ? 0 : 1;
+                n1 += g ? 1 : 0;
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok && lane == 0)
+                mma_commit(smem_u32(&bars->k16_empty[ub]));
+            __syncwarp();
+        }
+        if (lane == 0) {
+            mma_commit(smem_u32(&bars->drain));
+            drain_wait(smem_u32(&bars->drain), 0);
+        }
+        __syncwarp();
+    } else {
+        // ========================= one thread a key =========================
+        const int g = warp >> 2;
+        const int tid = threadIdx.x & 127;
+        float* part = reinterpret_cast<float*>(smem + L::kOffPart);
+        const uint32_t t_s = tmem + ((uint32_t)((warp & 3) * 32) << 16) + g * 128;
+        uint32_t ns = 0;                                                    // row tiles of this warpgroup so far
+        // this key's table entry two units ahead, its scale and old sum one ahead
+        auto entry_of = [&](const KeyUnit& k) -> int {
+            const int pos = k.tile * kTileKeys + tid;
+            return k.b >= 0 && pos < k.keys ? p.table[(long long)k.b * p.max_pages + (pos >> p.page_shift)] : INT_MIN;
+        };
+        auto scale_of = [&](const KeyUnit& k, int entry, float& ks, float& old) -> bool {
+            ks = 1.f;
+            old = 0.f;
+            const bool in = (unsigned)entry < (unsigned)p.n_pages;
+            const int pos = k.tile * kTileKeys + tid;
+            if (in) {
+                ks = p.k.scale[(long long)entry * p.Hkv + k.h];
+                if (g == 0 && wp.score && pos < k.start && pos < wp.stride)
+                    old = wp.score[((long long)k.b * p.Hkv + k.h) * wp.stride + pos];
+            } else if (entry != INT_MIN) {
+                atomicCAS(&g_sdpa_error, 0u, (unsigned)cache::kErrPage);
+            }
+            return in;
+        };
+        KeyUnit k = finder.find(wp, blockIdx.x), k1 = finder.find(wp, (long long)blockIdx.x + gridDim.x);
+        int entry = entry_of(k), entry_next = entry_of(k1);
+        float ks_next, old_next;
+        bool valid_next = scale_of(k, entry, ks_next, old_next);
+        for (long long u = blockIdx.x; k.b >= 0; u += gridDim.x, ++units) {
+            const bool valid = valid_next;
+            const float c = ks_next * p.scale_log2, old = old_next;
+            const KeyUnit k2 = finder.find(wp, u + 2ll * gridDim.x);
+            entry = entry_next;
+            entry_next = entry_of(k2);
+            valid_next = scale_of(k1, entry, ks_next, old_next);
+            const uint32_t ub = units & 1;
+            // ---- the tile's codes to 16 bits: 64-channel chunks of 128-byte rows
+            ok = wait_bar(smem_u32(&bars->k8_full[ub]), (units / 2) & 1, abort, kErrWeightsSum + 1);
+            if (units >= 2)
+                ok = ok && wait_bar(smem_u32(&bars->k16_empty[ub]), (units / 2 - 1) & 1, abort, kErrWeightsSum + 2);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+                constexpr int kPer = D / 16, kStep = 256 / kPer;            // threads of a row, rows of a turn (a multiple of 8)
+                const int key0 = threadIdx.x / kPer, cc = threadIdx.x % kPer;
+                const int at = D == 128 ? cc ^ (key0 & 7) : cc ^ ((key0 >> 1) & 3);
+                const uint8_t* src = smem + L::kOffK8 + ub * L::kK8Bytes + key0 * D + at * 16;
+                const uint32_t row = sK16 + ub * L::kTileBytes + cc / 4 * (kTileKeys * 128) + key0 * 128;
+                const uint32_t dst0 = row + ((cc % 4 * 2) ^ (key0 & 7)) * 16, dst1 = row + ((cc % 4 * 2 + 1) ^ (key0 & 7)) * 16;
+                auto pair = [](uint32_t codes) -> uint32_t {
+                    const uint32_t h = e4m3x2_to_f16x2((uint16_t)codes);
+                    if constexpr (!kBF16)
+                        return h;
+                    const float2 f = f16x2_to_f32x2(h);
+                    return pack2<true>(f.x, f.y);
+                };
+#pragma unroll
+                for (int i = 0; i < kTileKeys / kStep; ++i) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(src + i * kStep * D);
+                    const uint32_t off = (uint32_t)(i * kStep * 128);
+                    st_shared_v4(dst0 + off, pair(v.x), pair(v.x >> 16), pair(v.y), pair(v.y >> 16));
+                    st_shared_v4(dst1 + off, pair(v.z), pair(v.z >> 16), pair(v.w), pair(v.w >> 16));
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(smem_u32(&bars->k16_full[ub]));
+                mbar_arrive(smem_u32(&bars->k8_empty[ub]));
+            }
+            // ---- the weights of this warpgroup's row tiles
+            const int pos = k.tile * kTileKeys + tid;
+            float sum = 0.f;
+            for (int rt = k.rt0; ok && rt < k.rt1; ++rt, ++n) {
+                if ((n & 1) != g)
+                    continue;
+                const uint32_t qs = n % NQ;
+                ok = wait_bar(smem_u32(&bars->q_full[qs]), (n / NQ) & 1, abort, kErrWeightsSum + 3) &&
+                     wait_bar(smem_u32(&bars->s_full[g]), ns & 1, abort, kErrWeightsSum + 4);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                ++ns;
+                tc_fence_after_sync();
+                // columns that are rows, and of those the ones that see this key
+                const int tok0 = rt / wp.head_blocks * wp.tok_per, head0 = rt % wp.head_blocks * wp.heads_per;
+                const int rows = min(wp.tok_per, k.count - tok0) * (wp.head_blocks == 1 ? wp.heads_per : min(wp.heads_per, p.group - head0));
+                const long long late = p.causal ? (pos - k.start - tok0) * wp.heads_per : 0;
+                const int from = (int)max(0ll, min(late, 128ll));
+                const bool edge = rows < 128 || __any_sync(0xffffffffu, from > 0);
+                const float4* lse = reinterpret_cast<const float4*>(smem + L::kOffLse + qs * 512);
+                uint64_t acc0 = 0, acc1 = 0;
+                const uint64_t c2 = f32x2(c, c);
+#pragma unroll 1
+                for (int e0 = 0; e0 < rows; e0 += 32) {
+                    uint32_t s[32];
+                    tmem_ld32_wait(t_s + e0, s);
+                    if (e0 + 32 >= rows) {                                  // the last of the tile's scores
+                        tc_fence_before_sync();
+                        mbar_arrive(smem_u32(&bars->s_free[g]));
+                    }
+                    const uint32_t seen = bits_below(rows - e0) & ~bits_below(from - e0);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 z = lse[(e0 + e) / 4];
+                        float x0, x1, x2, x3;
+                        f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, f32x2(z.x, z.y)), x0, x1);
+                        f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, f32x2(z.z, z.w)), x2, x3);
+                        if (edge) {
+                            x0 = seen >> e & 1 ? x0 : -INFINITY;
+                            x1 = seen >> (e + 1) & 1 ? x1 : -INFINITY;
+                            x2 = seen >> (e + 2) & 1 ? x2 : -INFINITY;
+                            x3 = seen >> (e + 3) & 1 ? x3 : -INFINITY;
+                        }
+                        acc0 = add_f32x2(acc0, f32x2(ex2_approx(x0), ex2_approx(x1)));
+                        acc1 = add_f32x2(acc1, f32x2(ex2_approx(x2), ex2_approx(x3)));
+                    }
+                }
+                mbar_arrive(smem_u32(&bars->q_empty[qs]));
+                float a, b;
+                f32x2_split(add_f32x2(acc0, acc1), a, b);
+                sum += a + b;
+            }
+            // ---- both warpgroups' sums
+            if (g == 1)
+                part[ub * 128 + tid] = sum;
+            if (!named_bar_all(1, 256, ok))
+                break;
+            if (g == 0 && valid && pos < wp.stride)
+                wp.out[((long long)k.b * p.Hkv + k.h) * wp.stride + pos] = old + (sum + part[ub * 128 + tid]);
+            k = k1;
+            k1 = k2;
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 9) {
+        __syncwarp();
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, L::kTmemCols);
+    }
+}
+
+}  // namespace weights
+}  // namespace sdpa

@@ -1,0 +1,88 @@
+"""The attention that cached keys draw, and the eviction of those that draw the
+least: the Python side of sdpa_cache_weights and sdpa_cache_evict (argument
+marshalling only)."""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import _DTYPE, _lse_ptr, _stream_ptr
+from . import cache as _cache
+from .cache import PagedCache, _alloc, _cache_args, _call, _int32, _strides
+
+
+def _rows(t, B, H, device, name):
+    """(address, length of a row) of a float32 tensor [B, Hkv, n]."""
+    if t.get_device() != device or t.dtype != torch.float32 or t.dim() != 3 or t.shape[0] != B or t.shape[1] != H \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor [{B}, {H}, n] on the cache's device")
+    return t.data_ptr(), t.shape[2]
+
+
+def sdpa_cache_weights(q, cache: PagedCache, block_table, start, count, lse, score=None, out=None, *, causal: bool = True,
+                       scale: float | None = None, stream=None) -> torch.Tensor:
+    """The attention that each cached key draws in one call of
+    :func:`sdpa_fwd_paged` (same q, tables, start, count, causal and scale; lse is
+    the one that it gave), added to what it has drawn before: returns ``out``
+    (float32 [B, Hkv, n], n at least the longest sequence),
+    out[b, h, j] = (score[b, h, j] if j < start[b] else 0) + the softmax weights of
+    key j, summed over the tokens and the query heads of its group.  ``score``
+    (None: zeros) and ``out`` may be the same tensor; without either, n is the
+    block table's positions and what lies behind a sequence is zero."""
+    dev = cache._device
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != cache.head_dim:
+        raise ValueError("q must be [B, Sq, Hq, D] with the cache's head dimension")
+    if q.get_device() != dev:
+        raise ValueError("q must be on the cache's device")
+    B, Sq, Hq, D = shape
+    Hkv = cache.n_heads
+    table_p, start_p, count_p, width = _cache_args(cache, block_table, start, count, B)
+    if lse is None or lse.get_device() != dev:
+        raise ValueError("the attention's lse is required, on the cache's device")
+    score_p, n = (None, width * cache.page_size) if score is None else _rows(score, B, Hkv, dev, "score")
+    if out is None:
+        out = _alloc(stream, dev, torch.zeros, (B, Hkv, n), dtype=torch.float32, device=q.device)
+    out_p, m = _rows(out, B, Hkv, dev, "out")
+    if score is not None and m != n:
+        raise ValueError("score and out must have rows of one length")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    _call(dev, (_cache._lib or _cache._bound()).sdpa_cache_weights, q.data_ptr(), cache._ref, table_p, start_p, count_p,
+          _lse_ptr(lse, B, Hq, Sq), score_p, out_p, B, Hq, Hkv, Sq, D, width, m, _strides(q), scale, 1 if causal else 0,
+          _DTYPE.get(q.dtype, 99), _stream_ptr(stream, dev))
+    return out
+
+
+def sdpa_cache_evict(cache: PagedCache, block_table, length, score, new_table, *, budget: int, sinks: int = 0,
+                     recent: int = 0, kept=None, kept_score=None, stream=None):
+    """Brings each sequence and KV head of the cache down to ``budget`` tokens:
+    the first ``sinks``, the last ``recent`` and, of those between, the ones with
+    the largest ``score`` (float32 [B, Hkv, n]; of equal ones the earlier) move, in
+    their order, to positions 0 .. of the pages of ``new_table`` (int32
+    [B, pages]; free pages, each named once).  length: int32 [B].  A sequence of
+    at most ``budget`` tokens moves whole; afterwards each has
+    ``length.clamp(max=budget)`` tokens under new_table.  Returns (kept,
+    kept_score), [B, Hkv, budget]: where each token was (int32) and its score,
+    allocated when not given; entries behind a sequence's tokens are not
+    written."""
+    dev = cache._device
+    if block_table.dim() != 2 or new_table.dim() != 2:
+        raise ValueError("block_table and new_table must be [B, pages]")
+    B, Hkv = block_table.shape[0], cache.n_heads
+    table_p, len_p, _, width = _cache_args(cache, block_table, length, None, B)
+    new_p = _int32(new_table, (B, new_table.shape[1]), dev, "new_table")
+    score_p, n = _rows(score, B, Hkv, dev, "score")
+    shape = (B, Hkv, max(0, budget))
+    if kept is None:
+        kept = _alloc(stream, dev, torch.empty, shape, dtype=torch.int32, device=score.device)
+    if kept_score is None:
+        kept_score = _alloc(stream, dev, torch.empty, shape, dtype=torch.float32, device=score.device)
+    kept_p = _int32(kept, shape, dev, "kept")
+    ks_p, m = _rows(kept_score, B, Hkv, dev, "kept_score")
+    if m != shape[2]:
+        raise ValueError("kept_score must be [B, Hkv, budget]")
+    _call(dev, (_cache._lib or _cache._bound()).sdpa_cache_evict, cache._ref, table_p, len_p, score_p, new_p, kept_p, ks_p, B,
+          Hkv, cache.head_dim, width, new_table.shape[1], n, sinks, recent, budget, _stream_ptr(stream, dev))
+    return kept, kept_score
