@@ -471,17 +471,26 @@ cudaError_t launch_weights_rows(int nr, const CUtensorMap& tk, const CUtensorMap
 }
 
 template <int D>
-cudaError_t launch_evict(const sdpa::evict::EvictParams& p, cudaStream_t stream)
+cudaError_t launch_evict(const sdpa::evict::EvictParams& p, int dev, int sm_count, cudaStream_t stream)
 {
     using namespace sdpa::evict;
-    // as many CTAs a row as hold the longest sequence's keys in registers
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t err[kMaxDevices];
+    cudaError_t e = allow_smem(select_kernel, kSelectSmem, dev, once, err);
+    if (e != cudaSuccess)
+        return e;
+    // as many CTAs a row as hold the longest sequence's keys, and
+    // more of them, of 4096 keys at least, while there are SMs for twice as many
     const long long longest = std::min(static_cast<long long>(p.max_pages) * p.page, p.stride);
+    const long long rows = static_cast<long long>(p.B) * p.Hkv;
     int ranks = 1;
-    while (ranks < 8 && static_cast<long long>(ranks) * kSelectThreads * kSelectKeys < longest)
+    while (ranks < 8 && (ranks * 1ll * kSelectKeys < longest ||
+                         (rows * ranks * 2 <= sm_count && ranks * 4096ll < longest)))
         ranks *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Hkv * ranks));
     cfg.blockDim = dim3(kSelectThreads);
+    cfg.dynamicSmemBytes = kSelectSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -491,30 +500,28 @@ cudaError_t launch_evict(const sdpa::evict::EvictParams& p, cudaStream_t stream)
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, select_kernel, p);
+    e = cudaLaunchKernelEx(&cfg, select_kernel, p);
     if (e == cudaSuccess)
         e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
     const long long units = static_cast<long long>(p.B) * p.n_ord * 2 * p.Hkv;
-    auto move = [&](auto threads, auto passes) {
-        constexpr int kUnit = decltype(threads)::value, kPasses = decltype(passes)::value;
-        constexpr int kUnits = kMoveThreads / kUnit;
-        return launch_pdl(true, move_kernel<D, kUnit, kPasses>, dim3(static_cast<unsigned>((units + kUnits - 1) / kUnits)),
+    auto move = [&](auto warps, auto rows) {
+        constexpr int kWarps = decltype(warps)::value, kRows = decltype(rows)::value;
+        constexpr int kUnits = kMoveThreads / 32 / kWarps;
+        return launch_pdl(true, move_kernel<D, kWarps, kRows>, dim3(static_cast<unsigned>((units + kUnits - 1) / kUnits)),
                           dim3(kMoveThreads), 0, stream, p);
     };
     using std::integral_constant;
-    // 64 .. 512 pieces of 16 bytes at D = 64, 128 .. 1024 at 128
-    const int pieces = p.page * (D / 16);
-    if constexpr (D == 64)
-        if (pieces <= 64)
-            return move(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-    if constexpr (D == 128)
-        if (pieces > 512)
-            return move(integral_constant<int, 256>{}, integral_constant<int, 4>{});
-    return pieces <= 128   ? move(integral_constant<int, 128>{}, integral_constant<int, 1>{})
-           : pieces <= 256 ? move(integral_constant<int, 256>{}, integral_constant<int, 1>{})
-                           : move(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+    // eight pieces of 16 bytes a lane at most
+    constexpr int kRows = 256 * 16 / D;                // tokens of a warp's: 32 at D = 128, 64 at D = 64
+    using One = integral_constant<int, 1>;
+    switch (p.page) {
+    case 16: return move(One{}, integral_constant<int, 16>{});
+    case 32: return move(One{}, integral_constant<int, 32>{});
+    case 64: return move(integral_constant<int, 64 / kRows>{}, integral_constant<int, kRows>{});
+    default: return move(integral_constant<int, 128 / kRows>{}, integral_constant<int, kRows>{});
+    }
 }
 
 // What the rows of a call over the cache see.
@@ -936,7 +943,7 @@ sdpa_status_t sdpa_cache_evict(const sdpa_cache_t* cache, const int* block_table
     p.budget = budget;
     p.n_ord = n_ord;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = D == 64 ? launch_evict<64>(p, cs) : launch_evict<128>(p, cs);
+    const cudaError_t e = D == 64 ? launch_evict<64>(p, dev, sm_count, cs) : launch_evict<128>(p, dev, sm_count, cs);
     return e == cudaSuccess ? SDPA_OK : cuda_fail(e);
 }
 

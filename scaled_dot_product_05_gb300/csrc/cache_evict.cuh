@@ -4,16 +4,24 @@
 // ones the earlier), in their order, in pages of their own.
 //
 // Two kernels.  The first finds the tokens: a CTA (or a cluster, for long
-// sequences) has the scores of one sequence and KV head in registers, as keys
-// that order like integers, and finds the key of the last token that stays bit
-// by bit, counting the keys that reach a candidate: 32 rounds of compares and
-// one barrier each, without atomics.  Then the warps, each with consecutive
-// positions, number their tokens.  The second moves the codes, a page of the
-// new ones a unit: a token's 16-byte pieces wait in registers for the page's
-// largest value, then are written under the smallest power of two that holds
-// it (the append's rule).  A power of two moves a code exactly, but for those
-// that become subnormal.
-// Bound by reading and writing the codes that stay.
+// sequences and where there are few) lays the scores of one sequence and KV head
+// into shared memory as keys that order like integers, and finds the key of the
+// last token that stays by its digits: a histogram of the upper 11 bits, of the
+// next 11 among the keys that share them, of the last 10.  Then the warps, each
+// with consecutive positions, number their tokens.  The second moves the codes, a
+// warp up to 4 KB of a new page: the 16-byte pieces of its tokens wait in
+// registers for the page's largest value, then are written under the smallest
+// power of two that holds it (the append's rule).  A power of two moves a code
+// exactly, but for those that become subnormal.
+//
+// Measured (8 sequences of 32768 tokens brought down to 8192, 8 KV heads of 128,
+// 283 MB): 65.6 us, of which the first kernel takes 19 and the second 46, 5.8 TB/s;
+// one of 4001 to 2000 with 16 heads of 64: 10.7 us, latencies.  The first kernel
+// is bound by its instructions and the barriers between its passes; bit by bit, in
+// 32 rounds of compares over keys in registers, it took 71 us, with the digits but
+// unrolled over registers 27, half of it spent on fetching code that runs once.
+// Eight pieces a lane and 64 registers keep twice as many bytes on their way as
+// 16 pieces and 106: 46 us against 73.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -47,23 +55,59 @@ __device__ __forceinline__ int tokens_of(const EvictParams& p, int b)
 // ------------------------------------------------------------------- select --
 
 constexpr int kSelectThreads = 1024;
-constexpr int kSelectKeys = 32;      // keys a thread holds; what is more is read again in every round
+constexpr int kSelectTurns = 8;      // four keys of a thread a turn in shared memory; what is more is read again each time
+constexpr int kSelectKeys = kSelectThreads * kSelectTurns * 4;         // of a CTA
+constexpr int kBins = 2048;
+constexpr int kDigits = 3;           // of 11, 11 and 10 bits
+constexpr int kSelectSmem = (kSelectKeys + kDigits * kBins) * 4;
 
 // Larger scores have larger keys; both zeros the same one, NaN the largest.  None is 0.
 __device__ __forceinline__ uint32_t key_of(float s)
 {
     const uint32_t u = __float_as_uint(s + 0.f);
-    return s != s ? ~0u : u & 0x80000000u ? ~u : u | 0x80000000u;
+    return s != s ? ~0u : u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+}
+
+// One more in a bin, if `some`; without a branch.
+__device__ __forceinline__ void count_if(uint32_t bin, bool some)
+{
+    asm volatile("{ .reg .pred q; setp.ne.u32 q, %1, 0; @q red.shared.add.u32 [%0], 1; }" ::"r"(bin), "r"((uint32_t)some) : "memory");
+}
+
+// The sum over the lanes before this one, and over all of them in the last.
+__device__ __forceinline__ uint32_t lanes_before(uint32_t c, int lane, uint32_t& incl)
+{
+    incl = c;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, incl, m);
+        incl += lane >= m ? o : 0u;
+    }
+    return incl - c;
 }
 
 __global__ void __launch_bounds__(kSelectThreads, 1) select_kernel(const EvictParams p)
 {
     namespace cg = cooperative_groups;
     constexpr int kWarps = kSelectThreads / 32;
-    __shared__ uint32_t warp_count[2][kWarps], cta_count[3], tie_count[kWarps], above_count[kWarps];
+    static_assert(kBins == 2 * kSelectThreads, "two bins a thread");
+    extern __shared__ __align__(16) uint32_t select_smem[];
+    __shared__ uint32_t warp_sum[kWarps], found[2], tie_count[kWarps], above_count[kWarps];
+    uint32_t* bins = select_smem;                      // [kDigits][kBins]
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // this lane's four keys of turn i at 32 i
+    uint4* keys = reinterpret_cast<uint4*>(select_smem + kDigits * kBins) + warp * (kSelectTurns * 32) + lane;
+    auto sync = [&] {
+        if (ranks > 1)
+            cluster.sync();
+        else
+            __syncthreads();
+    };
+#pragma unroll
+    for (int i = 0; i < kDigits * kBins / kSelectThreads; ++i)
+        bins[i * kSelectThreads + threadIdx.x] = 0;
     grid_dependency_wait();
     grid_launch_dependents();
     const int row = blockIdx.x / ranks;                // sequence and KV head: the cluster's
@@ -84,86 +128,110 @@ __global__ void __launch_bounds__(kSelectThreads, 1) select_kernel(const EvictPa
     }
     const int first = p.sinks, last = n - p.recent;    // candidates: first .. last - 1
     const uint32_t room = p.budget - p.sinks - p.recent;       // of which so many stay (fewer than there are)
-    // a warp has `turns` times 32 consecutive positions
-    const int turns = (n + ranks * kWarps * 32 - 1) / (ranks * kWarps * 32);
-    const int pos0 = (rank * kWarps + warp) * turns * 32 + lane;
-    auto key_at = [&](int i) -> uint32_t {             // of turn i (0: no candidate)
-        const int pos = pos0 + i * 32;
-        return pos >= first && pos < last ? key_of(score[pos]) : 0u;
-    };
-    uint32_t key[kSelectKeys];
-#pragma unroll
-    for (int i = 0; i < kSelectKeys; ++i)
-        key[i] = i < turns ? key_at(i) : 0u;
-    // Counts over the cluster, the same in every thread: warps, then CTAs.
-    int phase = 0;
-    auto total = [&](uint32_t c) -> uint32_t {
-        c = __reduce_add_sync(0xffffffffu, c);
-        if (lane == 0)
-            warp_count[phase & 1][warp] = c;
-        __syncthreads();
-        c = __reduce_add_sync(0xffffffffu, warp_count[phase & 1][lane]);
-        if (ranks > 1) {
-            if (threadIdx.x == 0)
-                cta_count[phase % 3] = c;
-            cluster.sync();
-            c = lane < ranks ? *cluster.map_shared_rank(&cta_count[phase % 3], lane) : 0u;
-            c = __reduce_add_sync(0xffffffffu, c);
+    // a warp has `turns` times 128 consecutive positions, a lane four of each
+    const int turns = (n + ranks * kWarps * 128 - 1) / (ranks * kWarps * 128);
+    const int held = min(turns, kSelectTurns);
+    const int warp0 = (rank * kWarps + warp) * turns * 128;
+    const bool wide = (reinterpret_cast<uintptr_t>(score) & 15) == 0;
+    auto keys_at = [&](int i) -> uint4 {               // of turn i (0: no token)
+        const int pos = warp0 + i * 128 + lane * 4;
+        if (wide && pos + 3 < n) {
+            const float4 s = __ldg(reinterpret_cast<const float4*>(score + pos));
+            return make_uint4(key_of(s.x), key_of(s.y), key_of(s.z), key_of(s.w));
         }
-        ++phase;
-        return c;
+        return make_uint4(pos < n ? key_of(__ldg(score + pos)) : 0u, pos + 1 < n ? key_of(__ldg(score + pos + 1)) : 0u,
+                          pos + 2 < n ? key_of(__ldg(score + pos + 2)) : 0u, pos + 3 < n ? key_of(__ldg(score + pos + 3)) : 0u);
     };
-    auto count_from = [&](uint32_t t) -> uint32_t {    // this thread's keys that reach t
-        uint32_t c = 0;
-#pragma unroll
-        for (int i = 0; i < kSelectKeys; ++i)
-            c += key[i] >= t ? 1u : 0u;
-        for (int i = kSelectKeys; i < turns; ++i)
-            c += key_at(i) >= t ? 1u : 0u;
-        return c;
+#pragma unroll 4
+    for (int i = 0; i < held; ++i)
+        keys[32 * i] = keys_at(i);
+    __syncthreads();                                   // the bins are zero
+    // f(turn, keys, which of them are candidates)
+    auto each = [&](auto f) {
+#pragma unroll 1
+        for (int i = 0; i < turns; ++i) {
+            const uint4 u = i < held ? keys[32 * i] : keys_at(i);
+            const uint32_t k[4] = {u.x, u.y, u.z, u.w};
+            const int turn0 = warp0 + i * 128, pos = turn0 + lane * 4;
+            uint32_t which = 15u;
+            if (turn0 < first || turn0 + 128 > last)
+                which = bits_below(last - pos) & ~bits_below(first - pos) & 15u;
+            f(pos, k, which);
+        }
     };
-    // the largest key that `room` candidates reach
-    uint32_t limit = 0;
+    // ---- the largest key that `room` candidates reach, and how many of the keys that are it stay
+    uint32_t limit = 0, ties = room;
     if (room > 0) {
 #pragma unroll 1
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t t = limit | 1u << bit;
-            if (total(count_from(t)) >= room)
-                limit = t;
-        }
-    }
-    const uint32_t above = room == 0 || limit == ~0u ? 0u : total(count_from(limit + 1));
-    const uint32_t ties = room - above;                // so many of the keys that are the limit, from the first on
-    // ---- tokens before each warp's: those that stay whatever the ties, and ties
-    uint32_t mine_above = 0, mine_ties = 0;
-    auto sort_out = [&](int i, uint32_t k, bool& stays, bool& tie) {
-        const int pos = pos0 + i * 32;
-        stays = pos < n && (pos < first || pos >= last || (room > 0 && k > limit));
-        tie = room > 0 && k == limit;                  // (limit is a candidate's key, so not 0)
-    };
+        for (int digit = 0; digit < kDigits; ++digit) {
+            const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
+            uint32_t* mine = bins + digit * kBins;
+            const uint32_t at = smem_u32(mine), above = digit == 0 ? 0u : digit == 1 ? ~0u << 21 : ~0u << 10;  // the digits found
+            const uint32_t mask = digit == 2 ? 0xffcu : 0x1ffcu;
+            each([&](int, const uint32_t* k, uint32_t which) {
 #pragma unroll
-    for (int i = 0; i < kSelectKeys; ++i) {
-        bool stays, tie;
-        sort_out(i, key[i], stays, tie);
-        mine_above += stays && i < turns;
-        mine_ties += tie;
+                for (int j = 0; j < 4; ++j)
+                    count_if(at + (digit == 2 ? k[j] << 2 & mask : k[j] >> (shift - 2) & mask),
+                             ((k[j] ^ limit) & above) == 0 && (which >> j & 1));
+            });
+            sync();
+            // thread t has bins 2047 - 2 t and the one below it
+            const int top = kBins - 1 - 2 * (int)threadIdx.x;
+            uint32_t c1 = 0, c0 = 0;
+            for (int r = 0; r < ranks; ++r) {
+                const uint2 c = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(mine, r) + top - 1);
+                c0 += c.x;
+                c1 += c.y;
+            }
+            uint32_t incl;
+            lanes_before(c0 + c1, lane, incl);
+            if (lane == 31)
+                warp_sum[warp] = incl;
+            __syncthreads();
+            uint32_t before = lane < warp ? warp_sum[lane] : 0u;
+            before = __reduce_add_sync(0xffffffffu, before) + incl - (c0 + c1);
+            if (before < ties && ties <= before + c0 + c1) {           // one thread
+                const bool upper = ties <= before + c1;
+                found[0] = upper ? top : top - 1;
+                found[1] = ties - before - (upper ? 0u : c1);
+            }
+            __syncthreads();
+            limit |= found[0] << shift;
+            ties = found[1];
+        }
+    } else {
+        limit = ~0u;                                   // (no candidate stays: none is above, and no tie does)
     }
-    for (int i = kSelectKeys; i < turns; ++i) {
-        bool stays, tie;
-        sort_out(i, key_at(i), stays, tie);
-        mine_above += stays;
-        mine_ties += tie;
-    }
+    // ---- tokens before each warp's: those that stay whatever the ties, and ties
+    auto sort_out = [&](const uint32_t* k, uint32_t which, uint32_t& stay, uint32_t& tie) {
+        stay = tie = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            stay |= k[j] > limit ? 1u << j : 0u;
+            tie |= k[j] == limit ? 1u << j : 0u;
+        }
+        if (which != 15u) {                            // tokens that are no candidates stay
+            stay &= which;
+            tie &= which;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                stay |= k[j] != 0 && !(which >> j & 1) ? 1u << j : 0u;
+        }
+    };
+    uint32_t mine_above = 0, mine_ties = 0;
+    each([&](int, const uint32_t* k, uint32_t which) {
+        uint32_t stay, tie;
+        sort_out(k, which, stay, tie);
+        mine_above += __popc(stay);
+        mine_ties += __popc(tie);
+    });
     mine_above = __reduce_add_sync(0xffffffffu, mine_above);
     mine_ties = __reduce_add_sync(0xffffffffu, mine_ties);
     if (lane == 0) {
         above_count[warp] = mine_above;
         tie_count[warp] = mine_ties;
     }
-    if (ranks > 1)
-        cluster.sync();
-    else
-        __syncthreads();
+    sync();
     uint32_t a = 0, t = 0;
     for (int r = 0; r <= rank; ++r) {
         const uint32_t ca = cluster.map_shared_rank(above_count, r)[lane], ct = cluster.map_shared_rank(tie_count, r)[lane];
@@ -171,29 +239,30 @@ __global__ void __launch_bounds__(kSelectThreads, 1) select_kernel(const EvictPa
         a += __reduce_add_sync(0xffffffffu, before ? ca : 0u);
         t += __reduce_add_sync(0xffffffffu, before ? ct : 0u);
     }
-    // ---- the tokens, numbered
-    auto write = [&](int i, uint32_t k) {
-        const int pos = pos0 + i * 32;
-        bool stays, tie;
-        sort_out(i, k, stays, tie);
-        const uint32_t below = (1u << lane) - 1u;
-        const uint32_t m_ties = __ballot_sync(0xffffffffu, tie), m_stays = __ballot_sync(0xffffffffu, stays);
-        const uint32_t tie_rank = t + __popc(m_ties & below);
-        if (stays || (tie && tie_rank < ties)) {
-            const uint32_t at = a + __popc(m_stays & below) + min(tie_rank, ties);
-            kept[at] = pos;
-            if (kept_score)
-                kept_score[at] = score[pos];
-        }
-        a += __popc(m_stays);
-        t += __popc(m_ties);
-    };
+    // ---- the tokens, numbered: `a` of them and `t` ties lie before the warp's turn
+    a += min(t, ties);
+    each([&](int pos, const uint32_t* k, uint32_t which) {
+        uint32_t stay, tie, incl;
+        sort_out(k, which, stay, tie);
+        if (t < ties && __any_sync(0xffffffffu, tie != 0)) {           // the first ties stay, too
+            uint32_t rank_of = t + lanes_before(__popc(tie), lane, incl);
 #pragma unroll
-    for (int i = 0; i < kSelectKeys; ++i)
-        if (i < turns)
-            write(i, key[i]);
-    for (int i = kSelectKeys; i < turns; ++i)
-        write(i, key_at(i));
+            for (int j = 0; j < 4; ++j)
+                if (tie >> j & 1)
+                    stay |= rank_of++ < ties ? 1u << j : 0u;
+            t += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        uint32_t at = a + lanes_before(__popc(stay), lane, incl);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (stay >> j & 1) {
+                kept[at] = pos + j;
+                if (kept_score)                        // (its key says what it was)
+                    kept_score[at] = __uint_as_float(k[j] & 0x80000000u ? k[j] & 0x7fffffffu : ~k[j]);
+                ++at;
+            }
+        a += __shfl_sync(0xffffffffu, incl, 31);
+    });
     if (ranks > 1)
         cluster.sync();                                // (no CTA leaves while another reads its counts)
 }
@@ -202,113 +271,152 @@ __global__ void __launch_bounds__(kSelectThreads, 1) select_kernel(const EvictPa
 
 constexpr int kMoveThreads = 256;
 
-// kUnit threads a unit, kPasses 16-byte pieces a thread.
-template <int D, int kUnit, int kPasses>
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p)
+__device__ __forceinline__ float warp_max_of(float v)
 {
-    constexpr int kPieces = D / 16;                    // of a token
-    constexpr int kUnits = kMoveThreads / kUnit;
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1)
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
+    return v;
+}
+
+// The largest of 16 codes' magnitudes, which order like integers; NaN (0x7F)
+// left out.
+__device__ __forceinline__ uint32_t largest_code(uint4 u)
+{
+    auto lanes = [](uint32_t m) { return max(m & 0xffffu, m >> 16); };
+    const uint32_t even = 0x007f007fu;
+    uint32_t m = __vmaxu2(__vmaxu2(__vmaxu2(u.x & even, u.x >> 8 & even), __vmaxu2(u.y & even, u.y >> 8 & even)),
+                          __vmaxu2(__vmaxu2(u.z & even, u.z >> 8 & even), __vmaxu2(u.w & even, u.w >> 8 & even)));
+    m = lanes(m);
+    if (m == 0x7f) {
+        m = 0;
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t c = w[i / 4] >> (i % 4 * 8) & 0x7f;
+            m = c < 0x7f ? max(m, c) : m;
+        }
+    }
+    return m;
+}
+
+// kWarps warps a unit, kRows tokens of the page a warp.
+template <int D, int kWarps, int kRows>
+__global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const EvictParams p)
+{
+    constexpr int kPieces = D / 16;                    // 16-byte pieces of a token
+    constexpr int kEach = kRows * kPieces / 32;        // pieces a lane
+    constexpr int kStep = 32 / kPieces;                // tokens that a warp reads at a time
+    constexpr int kHold = (kRows + 31) / 32;           // tokens that a lane looks up
+    constexpr int kUnits = kMoveThreads / 32 / kWarps;
     __shared__ float warp_max[kMoveThreads / 32];
     grid_dependency_wait();
     grid_launch_dependents();
     // unit -> (KV head fastest, K or V, new page, sequence)
-    const int tid = threadIdx.x % kUnit;
-    const uint32_t unit = blockIdx.x * kUnits + threadIdx.x / kUnit;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % kWarps;
+    const uint32_t unit = blockIdx.x * kUnits + warp / kWarps;
     uint32_t rest = unit / (uint32_t)p.Hkv;
     const int h = (int)(unit - rest * p.Hkv);
     const int kv = (int)(rest & 1);
     rest >>= 1;
     const int b = (int)(rest / (uint32_t)p.n_ord);
     const int ord = (int)(rest - b * p.n_ord);
-    int rows = 0, to = -1;                             // tokens of the page, and the page
-    if (b < p.B) {
-        rows = max(0, min(p.page, min(tokens_of(p, b), p.budget) - (ord << p.page_shift)));
-        if (rows > 0) {
-            to = p.new_table[(long long)b * p.new_max_pages + ord];
-            if ((unsigned)to >= (unsigned)p.n_pages) {
-                if (tid == 0)
-                    atomicCAS(&g_sdpa_error, 0u, (unsigned)cache::kErrPage);
-                rows = 0;
-            }
-        }
-    }
     const cache::Pool pool = p.pool[kv];
-    uint4 u[kPasses];
-    float scale[kPasses];
-    float amax = 0.f;
-    const int* kept = p.kept + ((long long)b * p.Hkv + h) * p.budget + ((long long)ord << p.page_shift);
-    int from[kPasses];
+    int rows = 0, to = -1;                             // tokens of the page, and the page
+    // ---- where this warp's tokens are, one or more a lane (-1: none there)
+    long long from[kHold];
+    float scale[kHold];
+    if (b < p.B) {
+        const int* kept = p.kept + ((long long)b * p.Hkv + h) * p.budget + ((long long)ord << p.page_shift) + part * kRows;
+        int pos[kHold], entry[kHold];
+        // (read beside the length, and looked at when that says that there is something)
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-        const int r = (tid + i * kUnit) / kPieces;
-        from[i] = r < rows ? kept[r] : -1;
-    }
-    int entry[kPasses];
+        for (int i = 0; i < kHold; ++i)
+            pos[i] = lane + 32 * i < kRows && (ord << p.page_shift) + part * kRows + lane + 32 * i < p.budget ? kept[lane + 32 * i] : -1;
+        to = p.new_table[(long long)b * p.new_max_pages + ord];
+        rows = max(0, min(p.page, min(tokens_of(p, b), p.budget) - (ord << p.page_shift)));
+        if (rows > 0 && (unsigned)to >= (unsigned)p.n_pages) {
+            if (lane == 0)
+                atomicCAS(&g_sdpa_error, 0u, (unsigned)cache::kErrPage);
+            rows = 0;
+        }
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i)
-        entry[i] = from[i] >= 0 ? p.table[(long long)b * p.max_pages + (from[i] >> p.page_shift)] : 0;
+        for (int i = 0; i < kHold; ++i) {
+            pos[i] = part * kRows + lane + 32 * i < rows ? pos[i] : -1;
+            entry[i] = pos[i] >= 0 ? p.table[(long long)b * p.max_pages + (pos[i] >> p.page_shift)] : -1;
+        }
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-        u[i] = make_uint4(0, 0, 0, 0);
-        scale[i] = 1.f;
-        if (from[i] >= 0) {
+        for (int i = 0; i < kHold; ++i) {
+            from[i] = -1;
+            scale[i] = 1.f;
             if ((unsigned)entry[i] < (unsigned)p.n_pages) {
+                from[i] = (long long)entry[i] * pool.sp + (long long)(pos[i] & (p.page - 1)) * pool.ss + (long long)h * pool.sh;
                 scale[i] = pool.scale[(long long)entry[i] * p.Hkv + h];
-                u[i] = *reinterpret_cast<const uint4*>(pool.codes + (long long)entry[i] * pool.sp +
-                                                       (long long)(from[i] & (p.page - 1)) * pool.ss + (long long)h * pool.sh +
-                                                       (tid + i * kUnit) % kPieces * 16);
-            } else {                                   // a token whose page is none is zero
+            } else if (pos[i] >= 0) {                  // a token whose page is none becomes zero
                 atomicCAS(&g_sdpa_error, 0u, (unsigned)cache::kErrPage);
             }
         }
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-        // the largest code: magnitudes order like integers, NaN (0x7F) left out
-        uint32_t m = 0;
-        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t v = w[k] & 0x7f7f7f7fu;
-            m = __vmaxu4(m, v & ~__vcmpeq4(v, 0x7f7f7f7fu));
+        for (int i = 0; i < kHold; ++i) {
+            from[i] = -1;
+            scale[i] = 1.f;
         }
-        m = max(max(m & 0xff, m >> 8 & 0xff), max(m >> 16 & 0xff, m >> 24));
-        amax = fmaxf(amax, f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)m)).x * scale[i]);
     }
+    // ---- their pieces: token i * kStep + lane / kPieces of the warp's, piece lane % kPieces
+    uint4 u[kEach];
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1)
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-    if constexpr (kUnit > 32) {
-        if ((threadIdx.x & 31) == 0)
-            warp_max[threadIdx.x >> 5] = amax;
+    for (int i = 0; i < kEach; ++i) {
+        const long long at = __shfl_sync(0xffffffffu, from[i * kStep / 32], (i * kStep + lane / kPieces) & 31);
+        u[i] = at >= 0 ? *reinterpret_cast<const uint4*>(pool.codes + at + lane % kPieces * 16) : make_uint4(0, 0, 0, 0);
+    }
+    float s[kEach], amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        s[i] = __shfl_sync(0xffffffffu, scale[i * kStep / 32], (i * kStep + lane / kPieces) & 31);
+        amax = fmaxf(amax, f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)largest_code(u[i]))).x * s[i]);
+    }
+    amax = warp_max_of(amax);
+    if constexpr (kWarps > 1) {
+        if (lane == 0)
+            warp_max[warp] = amax;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kUnit / 32; ++i)
-            amax = fmaxf(amax, warp_max[threadIdx.x / kUnit * (kUnit / 32) + i]);
+        for (int i = 0; i < kWarps; ++i)
+            amax = fmaxf(amax, warp_max[warp / kWarps * kWarps + i]);
     }
     if (rows == 0)
         return;
     const float fresh = cache::pow2_scale(amax), inv = 1.f / fresh;
-    if (tid == 0)
+    if (lane == 0 && part == 0)
         pool.scale[(long long)to * p.Hkv + h] = fresh;
     uint8_t* dst = pool.codes + (long long)to * pool.sp + (long long)h * pool.sh;
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-        const int at = tid + i * kUnit;
-        if (from[i] < 0)
-            continue;
-        const float f = scale[i] * inv;                // (exact: inv is a power of two)
+    for (int i = 0; i < kEach; ++i) {
+        const float f = s[i] * inv;                    // (exact: inv is a power of two)
         if (f != 1.f) {
             uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+            // A power of two between f16's 2^-24 and 2^15: the product in f16 is
+            // exact down to 2^-21, and what is below 2^-10 becomes zero anyhow
+            if ((__float_as_uint(f) & 0x7fffffu) == 0 && f >= 5.9604644775390625e-8f && f <= 32768.f) {
+                const uint32_t f2 = f32x2_to_f16x2(f, f);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 x = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)w[k]));
-                const float2 y = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(w[k] >> 16)));
-                w[k] = (uint32_t)f32x2_to_e4m3x2(x.x * f, x.y * f) | ((uint32_t)f32x2_to_e4m3x2(y.x * f, y.y * f) << 16);
+                for (int k = 0; k < 4; ++k)
+                    w[k] = f16x2_to_e4m3x2(mul_f16x2(e4m3x2_to_f16x2((uint16_t)w[k]), f2)) |
+                           (f16x2_to_e4m3x2(mul_f16x2(e4m3x2_to_f16x2((uint16_t)(w[k] >> 16)), f2)) << 16);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 x = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)w[k]));
+                    const float2 y = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(w[k] >> 16)));
+                    w[k] = (uint32_t)f32x2_to_e4m3x2(x.x * f, x.y * f) | ((uint32_t)f32x2_to_e4m3x2(y.x * f, y.y * f) << 16);
+                }
             }
             u[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        *reinterpret_cast<uint4*>(dst + (long long)(at / kPieces) * pool.ss + at % kPieces * 16) = u[i];
+        const int r = part * kRows + i * kStep + lane / kPieces;
+        if (r < rows)
+            *reinterpret_cast<uint4*>(dst + (long long)r * pool.ss + lane % kPieces * 16) = u[i];
     }
 }
 
