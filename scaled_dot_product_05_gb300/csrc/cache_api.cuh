@@ -370,12 +370,12 @@ constexpr int kPagedCtas = 304;
 int paged_tile_rows(int Sq, int group)
 {
     const long long rows = static_cast<long long>(Sq) * group;
-    return rows <= 8 ? 8 : rows <= 16 ? 16 : sdpa::paged::kWideRows;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= sdpa::paged::kWideRows / 2 ? sdpa::paged::kWideRows / 2 : sdpa::paged::kWideRows;
 }
 
 int paged_ctas(int tile_rows)
 {
-    return tile_rows == sdpa::paged::kWideRows ? kPagedCtas / 2 : kPagedCtas;
+    return tile_rows > 16 ? kPagedCtas / 2 : kPagedCtas;
 }
 
 // The pieces' results, their LSE, and what is to join.
@@ -392,14 +392,14 @@ cudaError_t launch_paged(const CUtensorMap& tk, const CUtensorMap& tv, const sdp
     using namespace sdpa::paged;
     static std::once_flag once[kMaxDevices];
     static cudaError_t attr[kMaxDevices];
-    constexpr bool kWide = NR == kWideRows;
+    constexpr bool kWide = NR > 16;
     auto* kernel = [] {
         if constexpr (kWide)
-            return paged_wide_kernel<D, kBF16, MASK>;
+            return paged_wide_kernel<D, kBF16, MASK, kWideRows / NR>;
         else
             return paged_attn_kernel<D, kBF16, NR, MASK>;
     }();
-    using L = std::conditional_t<kWide, WideLayout<D, kBF16, MASK>, PagedLayout<D, kBF16, kWide ? 16 : NR>>;
+    using L = std::conditional_t<kWide, WideLayout<D, kBF16, MASK, kWide ? kWideRows / NR : 1>, PagedLayout<D, kBF16, kWide ? 16 : NR>>;
     std::call_once(once[dev], [&] {
         attr[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
     });
@@ -419,6 +419,7 @@ cudaError_t launch_paged_rows(int nr, const CUtensorMap& tk, const CUtensorMap& 
 {
     return nr == 8    ? launch_paged<D, kBF16, 8, MASK>(tk, tv, p, dev, s)
            : nr == 16 ? launch_paged<D, kBF16, 16, MASK>(tk, tv, p, dev, s)
+           : nr == sdpa::paged::kWideRows / 2 ? launch_paged<D, kBF16, sdpa::paged::kWideRows / 2, MASK>(tk, tv, p, dev, s)
                       : launch_paged<D, kBF16, sdpa::paged::kWideRows, MASK>(tk, tv, p, dev, s);
 }
 
@@ -734,7 +735,7 @@ sdpa_status_t run_paged(const void* Q, const sdpa_cache_t* cache, const int* blo
     // no more CTAs than there can be tiles
     const __int128 most = static_cast<__int128>(B) * Hkv * p.row_tiles *
                           ((static_cast<long long>(max_pages) * p.page + sdpa::paged::kTileKeys - 1) / sdpa::paged::kTileKeys);
-    const int per_sm = nr == sdpa::paged::kWideRows ? 1 : 2;
+    const int per_sm = nr > 16 ? 1 : 2;
     p.ctas = per_sm * sm_count < paged_ctas(nr) ? per_sm * sm_count : paged_ctas(nr);
     p.ctas = most < p.ctas ? static_cast<int>(most) : p.ctas;
     p.part_o = static_cast<float*>(workspace);
@@ -855,7 +856,7 @@ sdpa_status_t sdpa_cache_weights(const void* Q, const sdpa_cache_t* cache, const
     const int nr = paged_tile_rows(Sq, p.group);
     const __int128 most = static_cast<__int128>(B) * Hkv *
                           ((static_cast<long long>(max_pages) * p.page + sdpa::paged::kTileKeys - 1) / sdpa::paged::kTileKeys);
-    p.ctas = (nr == sdpa::paged::kWideRows ? 1 : 2) * sm_count;
+    p.ctas = (nr > 16 ? 1 : 2) * sm_count;
     p.ctas = most < p.ctas ? static_cast<int>(most) : p.ctas;
     p.ctas_inverse = ~0ull / p.ctas + 1;
     wp.lse = LSE;
@@ -869,7 +870,7 @@ sdpa_status_t sdpa_cache_weights(const void* Q, const sdpa_cache_t* cache, const
     if (!map_of_codes(&tk, ck))
         return cuda_fail(cudaErrorInvalidValue);
     const bool bf16 = dtype == SDPA_DTYPE_BF16;
-    if (nr == sdpa::paged::kWideRows &&
+    if (nr > 16 &&
         !make_map(&tq, Q, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, D, Hq, Sq, B, q.st,
                   wp.heads_per, wp.tok_per))
         return cuda_fail(cudaErrorInvalidValue);

@@ -20,6 +20,12 @@
 // 8192 keys (32 query heads on 8 of 128) 104 us and 13.5 us for the join.  What
 // is between is the warpgroups' own chain (scores, maximum, weights, the wait
 // for the product to be taken) and some 15 000 cycles for each change of piece.
+//
+// Up to 64 rows (kSplit = 2: trees of drafts, mostly) stand in the lanes twice:
+// lanes 0 .. 63 take the first 64 keys of a tile, lanes 64 .. 127 the others, and
+// each have weights of zero for the other half, written once.  The products cost
+// what they did, the exponentials half; the two halves of a row are joined like
+// the warpgroups'.  8 trees of 16 tokens behind up to 8192 keys: 39.9 us against 48.
 #pragma once
 
 #include "paged_attn.cuh"
@@ -27,14 +33,19 @@
 namespace sdpa {
 namespace paged {
 
-constexpr int kWideRows = 128;
+constexpr int kWideRows = 128;           // lanes of a product; row tiles have that many rows, or half of them (kSplit = 2)
 constexpr float kWideLag = 8.0f;           // a weight may reach 2^8 before the maximum moves
 constexpr float kWideLog2W = 7.0f;         // weight 1 is held as 2^7: 2^15 at most
 
-template <int D, bool kBF16, int MASK = kPlain>
+template <int D, bool kBF16, int MASK, int kSplit>
 struct WideLayout {
     static constexpr int kParts = kBF16 ? 2 : 3;
-    static constexpr int kThreads = 384;   // 8 softmax warps; TMA producer, S issuer, 2 converters
+    // 8 softmax warps, TMA producer, S issuer, converters: two, or a warpgroup (behind
+    // two idle warps) where the softmax threads need fewer registers for their half of the keys
+    static constexpr int kConverters = kSplit == 1 ? 64 : 128;
+    static constexpr int kThreads = kSplit == 1 ? 384 : 512;
+    static constexpr uint32_t kRegsLow = kSplit == 1 ? 104 : 96, kRegsSoftmax = kSplit == 1 ? 192 : 160;
+    static_assert(kRegsLow * (kThreads - 256) + kRegsSoftmax * 256 <= 65536 / kThreads / 8 * 8 * kThreads, "register split");
     static constexpr int kTileBytes = kTileKeys * D;            // 8-bit K or V tile, a part of Q
     static constexpr int kV16Bytes = kTileKeys * D * 2;
     static constexpr int kStagesK = D == 64 ? 4 : 3;
@@ -93,19 +104,20 @@ struct WideBarriers {
     uint32_t tmem_base;
     int abort;
     long long total, x, x_first;
-    long long warp_sums[12];
+    long long warp_sums[16];
     // the piece at hand, kept here while the softmax threads' registers hold
     // their scores
     Piece piece;
     Item item;
 };
 
-template <int D, bool kBF16, int MASK>
-__global__ void __launch_bounds__(384, 1)
+template <int D, bool kBF16, int MASK, int kSplit>
+__global__ void __launch_bounds__(kSplit == 1 ? 384 : 512, 1)
 paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p)
 {
-    using L = WideLayout<D, kBF16, MASK>;
-    constexpr int NK = L::kStagesK, NV = L::kStagesV, QP = L::kParts, NR = kWideRows;
+    using L = WideLayout<D, kBF16, MASK, kSplit>;
+    constexpr int NK = L::kStagesK, NV = L::kStagesV, QP = L::kParts, NR = kWideRows / kSplit;
+    constexpr int kKeys = kTileKeys / kSplit;          // of a tile, a softmax thread's
     constexpr uint32_t kBarSoftmax = 1;
     constexpr bool kMasked = MASK != kPlain;
     constexpr int kNanWords = kMasked ? 4 * D : D;
@@ -121,8 +133,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const uint32_t sV8 = smem_u32(smem + L::kOffV8), sV16 = smem_u32(smem + L::kOffV16);
     float4* pages = reinterpret_cast<float4*>(smem + L::kOffPages);
     float* row_max = reinterpret_cast<float*>(smem + L::kOffRows);          // [2][128]
-    float* row_sum = row_max + 2 * NR;                                      // [2][128]
-    int* nan_at = reinterpret_cast<int*>(row_sum + 2 * NR);                 // [D]: first masked key with a NaN there
+    float* row_sum = row_max + 2 * kWideRows;                               // [2][128]
+    int* nan_at = reinterpret_cast<int*>(row_sum + 2 * kWideRows);                 // [D]: first masked key with a NaN there
     int* any_nan = nan_at + kNanWords;
 
     if (threadIdx.x == 0) {
@@ -132,10 +144,10 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         for (int i = 0; i < NV; ++i) {
             mbar_init(smem_u32(&bars->v_full[i]), 1);
-            mbar_init(smem_u32(&bars->v_empty[i]), 64);
+            mbar_init(smem_u32(&bars->v_empty[i]), L::kConverters);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&bars->v16_full[i]), 64);
+            mbar_init(smem_u32(&bars->v16_full[i]), L::kConverters);
             mbar_init(smem_u32(&bars->v16_empty[i]), 1);
             mbar_init(smem_u32(&bars->s_full[i]), 1);
             mbar_init(smem_u32(&bars->s_free[i]), 128);
@@ -144,7 +156,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         for (int i = 0; i < L::kPageBufs; ++i) {
             mbar_init(smem_u32(&bars->pages_full[i]), 8);
-            mbar_init(smem_u32(&bars->pages_free[i]), 128 + 64);
+            mbar_init(smem_u32(&bars->pages_free[i]), 128 + L::kConverters);
         }
         mbar_init(smem_u32(&bars->q_full), 256);
         for (int i = 0; i < 3; ++i)
@@ -171,7 +183,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     Piece w;
     bool more = first_piece<NR, MASK>(p, bars, w);
     if (warp >= 8) {
-        regs_release<104>();
+        regs_release<L::kRegsLow>();
         if (warp == 8) {
             // ========================= TMA producer =========================
             // as in paged_attn_kernel: lane i brings page i of a tile; and lane
@@ -268,7 +280,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             // S of tile j + 1 as soon as the scores of tile j have been read
             if (lane == 0) {
                 constexpr uint32_t kSwzCode = D == 128 ? 2u : 4u;
-                constexpr uint32_t idesc_s = idesc_make(0u, NR, kTileKeys, false);
+                constexpr uint32_t idesc_s = idesc_make(0u, kWideRows, kTileKeys, false);
                 const uint32_t hi = (uint32_t)(smem_desc(0, 16, 8 * D, kSwzCode) >> 32);
                 uint32_t ns = 0, pieces = 0, f0 = 0, f1 = 0;       // S issued: all, for each warpgroup
                 int prev = -1;                                     // warpgroup of the last S
@@ -305,13 +317,13 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 drain_wait(smem_u32(&bars->drain[0]), 0);
             }
             __syncwarp();
-        } else {
+        } else if (warp >= (L::kThreads - L::kConverters) / 32) {
             // ========================== converters ==========================
             // V's codes to f16, 16 at a time, into the layout of a 16-bit tile
             // (64 channels a chunk, 128-byte rows); rows that no row of the item
             // sees are zero, a NaN that only some see is taken out and kept in
             // mind
-            const int tid = threadIdx.x - 320;                              // 0 .. 63
+            const int tid = threadIdx.x - (L::kThreads - L::kConverters);
             uint32_t n = 0, pieces = 0;
             bool ok = true;
             for (; ok && more; more = next_piece<NR, MASK>(p, w), ++pieces) {
@@ -337,7 +349,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         break;
                     // this thread's 16 channels c of keys key0, key0 + kStep, ..:
                     // a multiple of 8 apart, so all at one swizzled place
-                    constexpr int kPer = D / 16, kStep = 64 / kPer, kTurns = kTileKeys / kStep;
+                    constexpr int kPer = D / 16, kStep = L::kConverters / kPer, kTurns = kTileKeys / kStep, kBatch = kSplit == 1 ? 8 : 4;
                     const int key0 = tid / kPer, c = tid % kPer;
                     const int at = D == 128 ? c ^ (key0 & 7) : c ^ ((key0 >> 1) & 3);
                     uint8_t* src = smem + L::kOffV8 + ring * L::kTileBytes + key0 * D + at * 16;
@@ -374,13 +386,13 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         }
                     }
 #pragma unroll
-                    for (int i0 = 0; i0 < kTurns; i0 += 8) {
-                        uint4 u[8];
+                    for (int i0 = 0; i0 < kTurns; i0 += kBatch) {
+                        uint4 u[kBatch];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
+                        for (int i = 0; i < kBatch; ++i)
                             u[i] = *reinterpret_cast<const uint4*>(src + (i0 + i) * kStep * D);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
+                        for (int i = 0; i < kBatch; ++i) {
                             const uint32_t off = (uint32_t)((i0 + i) * kStep * 128);
                             st_shared_v4(dst0 + off, e4m3x2_to_f16x2((uint16_t)u[i].x), e4m3x2_to_f16x2((uint16_t)(u[i].x >> 16)),
                                          e4m3x2_to_f16x2((uint16_t)u[i].y), e4m3x2_to_f16x2((uint16_t)(u[i].y >> 16)));
@@ -396,26 +408,34 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             }
         }
     } else {
-        regs_acquire<192>();
+        regs_acquire<L::kRegsSoftmax>();
         // ======================== softmax warpgroups ========================
         const int g = warp >> 2;
-        const int row = threadIdx.x & 127;                                  // of the tile; TMEM lane
+        const int lane_row = threadIdx.x & 127;                             // TMEM lane
+        const int row = lane_row % NR, part = lane_row / NR;                // row of the tile; which of its keys (the warp's)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        constexpr uint32_t idesc_o = idesc_make(0u, NR, D, true);
+        constexpr uint32_t idesc_o = idesc_make(0u, kWideRows, D, true);
         const uint32_t hi_v = (uint32_t)(smem_desc(0, 16, 1024, 2u) >> 32);
         constexpr uint32_t kLboV = (uint32_t)((kTileKeys * 128) >> 4) << 16;            // next 64 channels
         const uint32_t t_s = tmem + lanes, t_w = t_s + 128 + 64 * g, t_o = t_s + 256 + 128 * g;
         uint32_t ns = 0;                                                    // tiles of this warpgroup so far
         uint32_t nv = 0;                                                    // tiles of the CTA before this piece
         bool ok = true;
+        if constexpr (kSplit > 1) {
+            // this row's weights of the other part's keys: zero, once
+            const uint32_t zero[32] = {};
+            tmem_st32(t_w + (1 - part) * 32, zero);
+            tmem_st_wait();
+        }
         for (; more; nv += w.end - w.begin, more = next_piece<NR, MASK>(p, w)) {
             Item it = item_of<NR, MASK>(p, w);
             // ---- q into 8-bit parts: two threads a row, half of its channels each
             float scale;                                                    // of this thread's row in the loop below
             {
                 const int r = threadIdx.x >> 1, half = threadIdx.x & 1;
-                const bool live = r < it.rows;
-                const int i = (it.r0 + r) / p.group, hh = (it.r0 + r) % p.group;
+                const int of = r % NR;                                      // (each part of the keys has all rows)
+                const bool live = of < it.rows;
+                const int i = (it.r0 + of) / p.group, hh = (it.r0 + of) % p.group;
                 const uint4* q = reinterpret_cast<const uint4*>(
                     reinterpret_cast<const uint16_t*>(p.Q) + (long long)it.b * p.q_sb + (long long)i * p.q_ss +
                     (long long)(w.h * p.group + hh) * p.q_sh + half * (D / 2));
@@ -485,7 +505,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             bool seen = false;
             // j counts the piece's tiles (with a window, those lie at tile0 of their number)
             const int begin = w.begin;
-            const int tiles = w.end - w.begin, ahead = full - w.begin * kTileKeys, seen_end = last - w.begin * kTileKeys;
+            const int tiles = w.end - w.begin, ahead = full - w.begin * kTileKeys, seen_end = last - w.begin * kTileKeys - part * kKeys;
             for (int j = g; j < tiles; j += 2, ++ns) {
                 const uint32_t vn = nv + (uint32_t)j, buf = vn % L::kPageBufs;
                 ok = ok && wait_bar(smem_u32(&bars->s_full[g]), ns & 1, abort, kErrPagedSoftmax);
@@ -494,17 +514,23 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (!ok)
                     break;
                 tc_fence_after_sync();
-                uint32_t r[128];
-                tmem_ld128_wait(t_s, t_s + 32, t_s + 64, t_s + 96, r);
+                uint32_t r[kKeys];
+                if constexpr (kSplit == 1) {
+                    tmem_ld128_wait(t_s, t_s + 32, t_s + 64, t_s + 96, r);
+                } else {
+                    tmem_ld32_wait(t_s + part * 64, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+                    tmem_ld32_wait(t_s + part * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+                }
                 tc_fence_before_sync();
                 mbar_arrive(smem_u32(&bars->s_free[g]));
+                const float4* page = pages + buf * 8 + part * (8 / kSplit);     // of this thread's keys
                 const int tile0 = kMasked ? it.tile<MASK>(begin + j) * kTileKeys : 0;
                 const bool edge = kMasked ? tile0 + kTileKeys > full || (MASK == kWindow && tile0 < full_low && tile0 + kTileKeys > p.sinks)
                                           : (j + 1) * kTileKeys > ahead;
                 float mx = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float4 pg = pages[buf * 8 + c];
+                for (int c = 0; c < 8 / kSplit; ++c) {
+                    const float4 pg = page[c];
                     const float a = scale * pg.x, b = pg.y + nmax;
                     const uint64_t a2 = f32x2(a, a), b2 = f32x2(b, b);
 #pragma unroll
@@ -520,8 +546,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (__builtin_expect(edge || pages[buf * 8].w != 0.f, 0)) {
                     if constexpr (kMasked) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const int k0 = tile0 + 32 * c;                      // bit e: the row sees key k0 + e
+                        for (int c = 0; c < 4 / kSplit; ++c) {
+                            const int k0 = tile0 + part * kKeys + 32 * c;                      // bit e: the row sees key k0 + e
                             uint32_t seen_keys = bits_below(last + 1 - k0);
                             if constexpr (MASK == kWindow) {
                                 // (the row's position is last or, where the table ends before it, behind that)
@@ -530,17 +556,17 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                             } else {
                                 seen_keys &= tree_bits(tree, p.tree_words, k0 - it.start);
                             }
-                            seen_keys &= (pages[buf * 8 + 2 * c].y == -INFINITY ? 0u : 0xffffu) |
-                                         (pages[buf * 8 + 2 * c + 1].y == -INFINITY ? 0u : 0xffff0000u);
+                            seen_keys &= (page[2 * c].y == -INFINITY ? 0u : 0xffffu) |
+                                         (page[2 * c + 1].y == -INFINITY ? 0u : 0xffff0000u);
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
                                 r[32 * c + e] = seen_keys >> e & 1 ? r[32 * c + e] : 0xff800000u;
                         }
                     } else {
-                        const int seen_keys = seen_end - j * kTileKeys;         // of the tile, less one
+                        const int seen_keys = seen_end - j * kTileKeys;         // of the thread's, less one
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const int end = pages[buf * 8 + c].y == -INFINITY ? -1 : seen_keys;
+                        for (int c = 0; c < 8 / kSplit; ++c) {
+                            const int end = page[c].y == -INFINITY ? -1 : seen_keys;
 #pragma unroll
                             for (int e = 16 * c; e < 16 * c + 16; ++e)
                                 r[e] = e > end ? 0xff800000u : r[e];
@@ -549,7 +575,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 }
                 float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
-                for (int e = 0; e < 128; e += 8) {
+                for (int e = 0; e < kKeys; e += 8) {
                     m0 = fmax3(m0, __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
                     m1 = fmax3(m1, __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
                     m2 = fmax3(m2, __uint_as_float(r[e + 4]), __uint_as_float(r[e + 5]));
@@ -571,16 +597,16 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     l *= factor;
                     const uint64_t s2 = f32x2(-shift, -shift);
 #pragma unroll
-                    for (int e = 0; e < 128; e += 2) {
+                    for (int e = 0; e < kKeys; e += 2) {
                         float y0, y1;
                         f32x2_split(add_f32x2(f32x2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), s2), y0, y1);
                         r[e] = __float_as_uint(y0);
                         r[e + 1] = __float_as_uint(y1);
                     }
                 }
-                uint32_t pk[64];
+                uint32_t pk[kKeys / 2];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
+                for (int c = 0; c < 8 / kSplit; ++c) {
                     uint64_t acc = 0;
 #pragma unroll
                     for (int e = 16 * c; e < 16 * c + 16; e += 2) {
@@ -590,7 +616,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     }
                     float s0, s1;
                     f32x2_split(acc, s0, s1);
-                    l = fmaf(s0 + s1, pages[buf * 8 + c].z, l);
+                    l = fmaf(s0 + s1, page[c].z, l);
                 }
                 mbar_arrive(smem_u32(&bars->pages_free[buf]));
                 // the product before has updated O
@@ -611,14 +637,15 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         tmem_st32(t_o + c, o);
                     }
                 }
-                tmem_st32(t_w, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
-                tmem_st32(t_w + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
+                tmem_st32(t_w + part * 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
+                if constexpr (kSplit == 1)
+                    tmem_st32(t_w + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
                 tmem_st_wait();
                 tc_fence_before_sync();
                 mbar_arrive(smem_u32(&bars->w_full[g]));
                 // O (+)= W V: the warpgroup's first thread issues it when all
                 // weights and the tile's V are there
-                if (row == 0) {
+                if (lane_row == 0) {
                     const uint32_t vb = vn & 1;
                     ok = wait_bar(smem_u32(&bars->w_full[g]), ns & 1, abort, kErrPagedMma + 4) &&
                          wait_bar(smem_u32(&bars->v16_full[vb]), (vn / 2) & 1, abort, kErrPagedMma + 3);
@@ -640,25 +667,36 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             it = bars->item;
             if (ok && g < w.end - w.begin)
                 ok = wait_bar(smem_u32(&bars->pv_done[g]), (ns - 1) & 1, abort, kErrPagedSoftmax + 3);
-            row_max[g * NR + row] = kWideLog2W - nmax;
-            row_sum[g * NR + row] = l;
+            row_max[g * kWideRows + lane_row] = kWideLog2W - nmax;
+            row_sum[g * kWideRows + lane_row] = l;
             ok = named_bar_all(kBarSoftmax, 256, ok);
             if (!ok)
                 break;
             tc_fence_after_sync();
-            const float l0 = row_sum[row], l1 = row_sum[NR + row];
-            const float m0 = l0 == 0.f ? -INFINITY : row_max[row], m1 = l1 == 0.f ? -INFINITY : row_max[NR + row];
-            const float m = fmaxf(m0, m1);
-            const float f0 = l0 == 0.f ? 0.f : exp2f(m0 - m), f1 = l1 == 0.f ? 0.f : exp2f(m1 - m);
-            const float sum = fmaf(l0, f0, l1 * f1);
-            const float w0 = sum == 0.f ? 0.f : f0 / sum, w1 = sum == 0.f ? 0.f : f1 / sum;
+            // the row's sums: of both warpgroups, and of each part of the keys
+            float m = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 2 * kSplit; ++k) {
+                const int at = k / kSplit * kWideRows + k % kSplit * NR + row;
+                m = row_sum[at] == 0.f ? m : fmaxf(m, row_max[at]);
+            }
+#pragma unroll
+            for (int k = 0; k < 2 * kSplit; ++k) {
+                const int at = k / kSplit * kWideRows + k % kSplit * NR + row;
+                const float lk = row_sum[at];
+                sum = lk == 0.f ? sum : fmaf(lk, exp2f(row_max[at] - m), sum);
+            }
+            // the weights of this lane's two accumulators
+            const float l0 = row_sum[lane_row], l1 = row_sum[kWideRows + lane_row];
+            const float w0 = sum == 0.f || l0 == 0.f ? 0.f : exp2f(row_max[lane_row] - m) / sum;
+            const float w1 = sum == 0.f || l1 == 0.f ? 0.f : exp2f(row_max[kWideRows + lane_row] - m) / sum;
             const bool whole = w.begin == 0 && w.end == w.n;
             const bool both = w.end - w.begin > 1;                          // warpgroup 1 had a tile
             const long long slot = (long long)blockIdx.x * 2 + (w.begin > 0 ? 0 : 1);
             const long long head = (long long)w.h * p.group + (it.r0 + row) % p.group;
             const int i = (it.r0 + row) / p.group;
             const bool live = row < it.rows;
-            if (live && g == 0) {
+            if (live && g == 0 && part == 0) {
                 const float lse2 = sum == 0.f ? -INFINITY : m + (log2f(sum) - kWideLog2W);
                 if (!whole)
                     p.part_lse[slot * NR + row] = lse2;
@@ -669,6 +707,9 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             const long long last_at = p.causal ? it.start + i : it.start + it.count - 1;
             const int last_key = last_at < it.keys ? (int)last_at : it.keys - 1;    // (a negative one is below any)
             uint16_t* out = reinterpret_cast<uint16_t*>(p.O) + (long long)it.b * p.o_sb + (long long)i * p.o_ss + head * p.o_sh;
+            // (the parts add up in the place of q, which no product reads any more)
+            float4* other = reinterpret_cast<float4*>(smem + L::kOffQ) + row * (D / 4);
+            static_assert(kSplit == 1 || NR * D * 4 <= L::kParts * L::kTileBytes, "exchange");
 #pragma unroll 1
             for (int c = g * (D / 2); c < (g + 1) * (D / 2); c += 32) {
                 uint32_t a[32], b[32];
@@ -683,18 +724,36 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     if (both)
                         o[e] = fmaf(__uint_as_float(b[e]), w1, o[e]);
                 }
+                if constexpr (kSplit > 1) {
+                    if (part > 0) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            other[(c / 4 + e) ^ (row & 7)] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                    named_bar_sync(kBarSoftmax + 1 + g, 128);
+                    if (part == 0) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float4 x = other[(c / 4 + e) ^ (row & 7)];
+                            o[4 * e] += x.x;
+                            o[4 * e + 1] += x.y;
+                            o[4 * e + 2] += x.z;
+                            o[4 * e + 3] += x.w;
+                        }
+                    }
+                }
                 if (nans) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         if (kMasked ? nan_at[4 * (c + e) + (row >> 5)] >> (row & 31) & 1 : last_key >= nan_at[c + e])
                             o[e] = NAN;
                 }
-                if (live && !whole) {
+                if (live && !whole && part == 0) {
                     float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * NR + row) * D + c);
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                } else if (live) {
+                } else if (live && part == 0) {
                     uint4* dst = reinterpret_cast<uint4*>(out + c);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -706,7 +765,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             named_bar_sync(kBarSoftmax, 256);                  // the rows' numbers and O are read
             tc_fence_after_sync();
         }
-        if (row == 0) {                                        // every product that this thread issued has completed
+        if (lane_row == 0) {                                   // every product that this thread issued has completed
             mma_commit(smem_u32(&bars->drain[1 + g]));
             drain_wait(smem_u32(&bars->drain[1 + g]), 0);
         }
