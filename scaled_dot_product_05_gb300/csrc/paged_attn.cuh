@@ -176,28 +176,27 @@ struct PagedBarriers {
     long long warp_sums[12];
 };
 
-// The key tiles that rows with a window visit: 0 .. first - 1 for the first
-// positions, then near .. up to that of position len - 1 (len >= 1).  `row0`
-// is the position of the first row, `low` the lowest one inside its window.
-struct WindowTiles {
-    int first, near, n;
+// The keys that rows with a window visit, whole pages of them: positions 0 ..
+// first - 1 for the first tokens, then those from first + skip to len - 1 (len
+// >= 1), n tiles if they stand side by side (a tile may hold some of both).
+// `row0` is the position of the first row, `low` the lowest one inside its window.
+struct WindowKeys {
+    int first, skip, n;
     long long low;
 };
 
-__device__ __forceinline__ WindowTiles window_tiles(const Params& p, long long row0, long long len)
+__device__ __forceinline__ WindowKeys window_keys(const Params& p, long long row0, long long len)
 {
-    WindowTiles t;
+    WindowKeys t;
+    const int mask = p.page - 1, end = (int)(len + mask) & ~mask;      // (positions stay below 2^30)
     t.low = row0 - p.window + 1;
     t.low = t.low < 0 ? 0 : t.low;
-    const int tiles = (int)((len + kTileKeys - 1) / kTileKeys);
     const int sinks = (int)(p.sinks < len ? p.sinks : len);
-    t.first = sinks / kTileKeys + (sinks % kTileKeys != 0);
-    const long long near = t.low / kTileKeys;
-    t.near = near < t.first ? t.first : near < tiles ? (int)near : tiles;
-    t.n = t.first + (tiles - t.near);
-    t.n = t.n < 1 ? 1 : t.n;                           // (a tile that no row sees, so that the result is written)
-    if (t.near == tiles && t.first == 0)
-        t.near = tiles - 1;
+    t.first = (sinks + mask) & ~mask;
+    const int near = t.low < end ? (int)t.low & ~mask : end;
+    t.skip = near > t.first ? near - t.first : 0;
+    const int keys = end - t.skip;
+    t.n = keys < 1 ? 1 : (keys + kTileKeys - 1) / kTileKeys;           // (one that no row sees, so that the result is written)
     return t;
 }
 
@@ -207,17 +206,22 @@ template <int NR, int MASK>
 __device__ __forceinline__ int entry_tiles(const Params& p, long long x)
 {
     if constexpr (MASK == kWindow) {
-        const int b = (int)(x / p.row_tiles);
-        const long long r0 = (x - (long long)b * p.row_tiles) * NR;
+        const int b = NR <= 16 ? (int)x : (int)(x / p.row_tiles);
         const int count = p.count ? max(0, min(p.Sq, p.count[b])) : p.Sq;
-        const long long rows = (long long)count * p.group;
-        if (r0 >= rows)
-            return 0;
-        const long long last = (rows < r0 + NR ? rows : r0 + NR) - 1, start = p.start[b];
-        const long long cap = (long long)p.max_pages << p.page_shift;
-        long long len = start + last / p.group + 1;
+        const long long start = p.start[b], cap = (long long)p.max_pages << p.page_shift;
+        long long row0 = start, len = start + count;
+        if constexpr (NR <= 16) {
+            if (count == 0)
+                return 0;
+        } else {
+            const long long r0 = (x - (long long)b * p.row_tiles) * NR, rows = (long long)count * p.group;
+            if (r0 >= rows)
+                return 0;
+            row0 = start + r0 / p.group;
+            len = start + ((rows < r0 + NR ? rows : r0 + NR) - 1) / p.group + 1;
+        }
         len = len < cap ? len : cap;
-        return len < 1 ? 1 : window_tiles(p, start + r0 / p.group, len).n;
+        return len < 1 ? 1 : window_keys(p, row0, len).n;
     }
     if constexpr (NR <= 16) {                          // one row tile holds a sequence's rows
         const int b = (int)x;
@@ -347,12 +351,21 @@ struct Item {
     long long start;
     int keys;                       // keys that some row of the item sees (within the table)
     int low;                        // kWindow: the lowest position in a row's window
-    int first, near;                // kWindow: as in WindowTiles
-    // key tile of the item's j-th; what a list of tiles is worth is that of the others
+    int first, skip;                // kWindow: as in WindowKeys
+    // position of key c of the item's tiles, 128 to each
     template <int MASK>
-    __device__ __forceinline__ int tile(int j) const
+    __device__ __forceinline__ int pos(int c) const
     {
-        return MASK != kWindow || j < first ? j : near + (j - first);
+        return MASK != kWindow || c < first ? c : c + skip;
+    }
+    // every position of tile j, which begins at `tile0`, lies in from .. end - 1, or below `sinks`
+    template <int MASK>
+    __device__ __forceinline__ bool inside(int j, int tile0, int from, int end, int sinks) const
+    {
+        if constexpr (MASK != kWindow)
+            return tile0 + kTileKeys <= end;
+        const int c = j * kTileKeys;
+        return (c >= first || c + kTileKeys <= first) && tile0 + kTileKeys <= end && (tile0 >= from || tile0 + kTileKeys <= sinks);
     }
     // some row sees some position of the page that begins at pos
     template <int MASK>
@@ -389,12 +402,12 @@ __device__ __forceinline__ Item item_of(const Params& p, const Piece& w)
     len = len < 0 ? 0 : len;
     t.keys = (int)(len < cap ? len : cap);
     if constexpr (MASK == kWindow) {
-        t.low = t.first = t.near = 0;
+        t.low = t.first = t.skip = 0;
         if (t.keys > 0) {
-            const WindowTiles list = window_tiles(p, t.start + t.r0 / p.group, t.keys);
+            const WindowKeys list = window_keys(p, NR <= 16 ? t.start : t.start + t.r0 / p.group, t.keys);
             t.low = (int)(list.low < t.keys ? list.low : t.keys);
             t.first = list.first;
-            t.near = list.near;
+            t.skip = list.skip;
         }
     }
     return t;
@@ -513,7 +526,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             // table entries are read three tiles ahead and looked at when their
             // tile comes, so that no tile waits for one
             auto entry_of = [&](int tile) -> int {
-                const int ord = it.tile<MASK>(tile) * ppt + lane;
+                const int ord = it.pos<MASK>((tile * ppt + lane) << p.page_shift) >> p.page_shift;
                 return lane < ppt && tile < w.end && it.has_page<MASK>(p, ord << p.page_shift)
                            ? p.table[(long long)it.b * p.max_pages + ord]
                            : -1;
@@ -705,7 +718,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (seg == 0 && r < NR) {
                     const long long last = p.causal ? it.start + i : it.start + it.count - 1;
                     row_scale[r] = finite ? qs * p.scale_log2 : NAN;
-                    row_last[r] = !live || last < 0 ? -1 : (int)(last < it.keys ? last : it.keys - 1);
+                    // (with a mask of its own: the row's token)
+                    row_last[r] = kMasked ? (live ? i : -1) : !live || last < 0 ? -1 : (int)(last < it.keys ? last : it.keys - 1);
 #pragma unroll
                     for (int k = 0; k < G; ++k)                             // rows that are none get no weight
                         group_rows[7 * NR * k + r] = live ? kLog2W : -INFINITY;
@@ -719,9 +733,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 mbar_arrive(smem_u32(&bars->q_full));
             }
             // every row of the item sees keys 0 .. full - 1
-            const int full = MASK == kTree ? (int)max(0ll, min(it.start, (long long)it.keys)) : row_last[0] + 1;
+            const int full = MASK == kTree     ? (int)max(0ll, min(it.start, (long long)it.keys))
+                             : MASK == kWindow ? (int)max(0ll, min(it.start + 1, (long long)it.keys))
+                                               : row_last[0] + 1;
             // with a window: of the keys below `full` those from `full_low` on, or below p.sinks
-            const int full_low = MASK == kWindow ? (int)max(0ll, it.start + (it.r0 + it.rows - 1) / p.group - p.window + 1) : 0;
+            const int full_low = MASK == kWindow ? (int)max(0ll, it.start + it.count - p.window) : 0;
             uint64_t l[NR / 2];                                             // pairs of rows
 #pragma unroll
             for (int r = 0; r < NR / 2; ++r)
@@ -732,7 +748,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             // scales one ahead: each is looked at when the next is on its way
             const int* table = p.table + (long long)it.b * p.max_pages;
             auto entry_of = [&](int tile) -> int {
-                const int pos = it.tile<MASK>(tile) * kTileKeys + tid;
+                const int pos = it.pos<MASK>(tile * kTileKeys + tid);
                 const bool in = kMasked ? pos < it.keys && it.has_page<MASK>(p, pos & -p.page) : pos < it.keys;
                 return tile < w.end && in ? table[pos >> p.page_shift] : INT_MIN;
             };
@@ -761,10 +777,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 entry_next = entry_of(j + 2 * G);
                 valid_next = scales_of(entry, k_scale, v_scale);
                 const uint32_t vn = nv + (uint32_t)(j - w.begin);           // V ring position
-                const int tile0 = it.tile<MASK>(j) * kTileKeys, pos = tile0 + tid;
+                const int tile0 = it.pos<MASK>(j * kTileKeys), pos = it.pos<MASK>(j * kTileKeys + tid);
                 // tiles in which some row does not see some key, by the item's rows or by a page that is none
-                const bool edge = tile0 + kTileKeys > full || __any_sync(0xffffffffu, !valid) ||
-                                  (MASK == kWindow && tile0 < full_low && tile0 + kTileKeys > p.sinks);
+                const bool edge = !it.inside<MASK>(j, tile0, full_low, full, p.sinks) || __any_sync(0xffffffffu, !valid);
                 uint32_t seen_rows = 0;                                     // of an edge tile: rows that see this key
                 ok = ok && wait_bar(smem_u32(&bars->s_full[g]), ns & 1, abort, kErrPagedSoftmax);
                 tc_fence_after_sync();
@@ -794,7 +809,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                             if (valid) {
 #pragma unroll
                                 for (int r = 0; r < NR; ++r)
-                                    seen_rows |= r < it.rows && token_sees<MASK>(p, it, (it.r0 + r) / p.group, pos) ? 1u << r : 0u;
+                                    seen_rows |= row_last[r] >= 0 && token_sees<MASK>(p, it, row_last[r], pos) ? 1u << r : 0u;
                             }
                         }
 #pragma unroll

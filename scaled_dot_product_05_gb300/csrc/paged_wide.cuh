@@ -196,7 +196,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             for (; ok && more; more = next_piece<NR, MASK>(p, w)) {
                 const Item it = item_of<NR, MASK>(p, w);
                 auto entry_of = [&](int tile) -> int {
-                    const int ord = it.tile<MASK>(tile) * ppt + lane;
+                    const int ord = it.pos<MASK>((tile * ppt + lane) << p.page_shift) >> p.page_shift;
                     return lane < ppt && tile < w.end && it.has_page<MASK>(p, ord << p.page_shift)
                                ? p.table[(long long)it.b * p.max_pages + ord]
                                : -1;
@@ -204,7 +204,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 int ahead0 = entry_of(w.begin), ahead1 = entry_of(w.begin + 1);
                 // a part's table entry two tiles ahead, its scales one ahead
                 auto part_of = [&](int tile) -> int {
-                    const int pos = it.tile<MASK>(tile) * kTileKeys + lane * 16;
+                    const int pos = it.pos<MASK>(tile * kTileKeys + lane * 16);
                     const bool in = kMasked ? pos < it.keys && it.has_page<MASK>(p, pos & -p.page) : pos < it.keys;
                     return lane < 8 && tile < w.end && in ? p.table[(long long)it.b * p.max_pages + (pos >> p.page_shift)]
                                                                      : INT_MIN;
@@ -332,7 +332,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->q_full), pieces & 1, abort, kErrPagedSoftmax + 8));
                 const int full = full_keys<MASK>(p, it), full_low = full_from<MASK>(p, it);
                 for (int j = w.begin; ok && j < w.end; ++j, ++n) {
-                    const int tile0 = it.tile<MASK>(j) * kTileKeys;
+                    const int tile0 = it.pos<MASK>(j * kTileKeys);
                     const uint32_t b = n & 1, ring = n % NV, pb = n % L::kPageBufs;
                     ok = wait_bar(smem_u32(&bars->pages_full[pb]), (n / L::kPageBufs) & 1, abort, kErrPagedSoftmax + 6);
                     uint32_t valid_parts = 0xffu;
@@ -355,11 +355,10 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     uint8_t* src = smem + L::kOffV8 + ring * L::kTileBytes + key0 * D + at * 16;
                     const uint32_t row = sV16 + b * L::kV16Bytes + (c / 4) * (kTileKeys * 128) + key0 * 128;
                     const uint32_t dst0 = row + (((c % 4) * 2) ^ (key0 & 7)) * 16, dst1 = row + (((c % 4) * 2 + 1) ^ (key0 & 7)) * 16;
-                    if (tile0 + kTileKeys > full || valid_parts != 0xffu ||
-                        (MASK == kWindow && tile0 < full_low && tile0 + kTileKeys > p.sinks)) {
+                    if (!it.inside<MASK>(j, tile0, full_low, full, p.sinks) || valid_parts != 0xffu) {
 #pragma unroll 4
                         for (int i = 0; i < kTurns; ++i) {
-                            const int key = key0 + i * kStep, pos = tile0 + key;
+                            const int key = key0 + i * kStep, pos = it.pos<MASK>(j * kTileKeys + key);
                             uint4* u = reinterpret_cast<uint4*>(src + i * kStep * D);
                             if (pos >= it.keys || !(valid_parts >> (key / 16) & 1)) {
                                 *u = make_uint4(0, 0, 0, 0);
@@ -524,9 +523,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 tc_fence_before_sync();
                 mbar_arrive(smem_u32(&bars->s_free[g]));
                 const float4* page = pages + buf * 8 + part * (8 / kSplit);     // of this thread's keys
-                const int tile0 = kMasked ? it.tile<MASK>(begin + j) * kTileKeys : 0;
-                const bool edge = kMasked ? tile0 + kTileKeys > full || (MASK == kWindow && tile0 < full_low && tile0 + kTileKeys > p.sinks)
-                                          : (j + 1) * kTileKeys > ahead;
+                const int key0 = (begin + j) * kTileKeys, tile0 = kMasked ? it.pos<MASK>(key0) : 0;
+                const bool edge = kMasked ? !it.inside<MASK>(begin + j, tile0, full_low, full, p.sinks) : (j + 1) * kTileKeys > ahead;
                 float mx = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < 8 / kSplit; ++c) {
@@ -546,8 +544,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (__builtin_expect(edge || pages[buf * 8].w != 0.f, 0)) {
                     if constexpr (kMasked) {
 #pragma unroll
-                        for (int c = 0; c < 4 / kSplit; ++c) {
-                            const int k0 = tile0 + part * kKeys + 32 * c;                      // bit e: the row sees key k0 + e
+                        for (int c = 0; c < 8 / kSplit; ++c) {                  // (parts of 16 keys lie in one page)
+                            const int k0 = it.pos<MASK>(key0 + part * kKeys + 16 * c);      // bit e: the row sees key k0 + e
                             uint32_t seen_keys = bits_below(last + 1 - k0);
                             if constexpr (MASK == kWindow) {
                                 // (the row's position is last or, where the table ends before it, behind that)
@@ -556,11 +554,10 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                             } else {
                                 seen_keys &= tree_bits(tree, p.tree_words, k0 - it.start);
                             }
-                            seen_keys &= (page[2 * c].y == -INFINITY ? 0u : 0xffffu) |
-                                         (page[2 * c + 1].y == -INFINITY ? 0u : 0xffff0000u);
+                            seen_keys = page[c].y == -INFINITY ? 0u : seen_keys;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                r[32 * c + e] = seen_keys >> e & 1 ? r[32 * c + e] : 0xff800000u;
+                            for (int e = 0; e < 16; ++e)
+                                r[16 * c + e] = seen_keys >> e & 1 ? r[16 * c + e] : 0xff800000u;
                         }
                     } else {
                         const int seen_keys = seen_end - j * kTileKeys;         // of the thread's, less one
