@@ -13,10 +13,14 @@
 // Two kernels, as for the attention.  Up to 16 rows (a decoding step): the
 // codes go to the FP8 tensor cores as they lie in the cache, the rows in two or
 // three 8-bit parts (see paged_attn.cuh for why these are exact); bound by
-// reading K.  More rows: a tile's codes are turned into the queries' 16-bit
-// type, which holds them exactly, once, and meet the queries as they are, 128
-// rows at a time; bound by the exponentials (128 x 128 of them a tile of rows:
-// 1024 cycles of an SM).
+// reading K: 8 sequences of 32768 keys (285 MB with the sums) 51.5 us, 5.5 TB/s.
+// More rows: a tile's codes are turned into the queries' 16-bit type, which holds
+// them exactly, once, and meet the queries as they are, 128 rows at a time.  The
+// two warpgroups take alternate row tiles; 2 chunks of 512 tokens behind up to 8192
+// keys 51 us.  There a row tile takes a warpgroup 2650 cycles, of which 1500 go into
+// its 128 exponentials a thread, 450 into reading the scores and 280 into waiting for
+// them; the tensor pipe is a quarter busy (with the scores read 32 at a time, and
+// the next tile's product behind the last of them: 60 us).
 #pragma once
 
 #include "paged_attn.cuh"
@@ -350,15 +354,16 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_k, const WeightParams wp)
 
 template <int D, bool kBF16>
 struct ManyLayout {
-    static constexpr int kThreads = 320;   // 8 warps of keys; TMA producer, MMA issuer
+    static constexpr int kThreads = 384;   // 8 warps of keys; TMA producer, MMA issuer, 2 idle
     static constexpr int kK8Bytes = kTileKeys * D;
     static constexpr int kTileBytes = kTileKeys * D * 2;        // 16-bit K or Q tile
-    static constexpr int kStagesQ = D == 64 ? 4 : 3;
+    // a tile of q is free when it has been multiplied, its rows' LSE when it has been summed
+    static constexpr int kStagesQ = D == 64 ? 4 : 3, kStagesLse = 8;
     static constexpr int kOffK8 = 0;                            // 2 stages
     static constexpr int kOffK16 = kOffK8 + 2 * kK8Bytes;       // 2
     static constexpr int kOffQ = kOffK16 + 2 * kTileBytes;
-    static constexpr int kOffLse = kOffQ + kStagesQ * kTileBytes;       // [kStagesQ][128]
-    static constexpr int kOffPart = kOffLse + kStagesQ * 512;           // [2][128]: the second warpgroup's sums
+    static constexpr int kOffLse = kOffQ + kStagesQ * kTileBytes;       // [kStagesLse][128]
+    static constexpr int kOffPart = kOffLse + kStagesLse * 512;         // [2][128]: the second warpgroup's sums
     static constexpr int kOffBar = kOffPart + 2 * 512;
     static constexpr int kBarBytes = 512;
     static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;
@@ -369,11 +374,19 @@ struct ManyLayout {
 template <int NQ>
 struct ManyBarriers {
     uint64_t k8_full[2], k8_empty[2], k16_full[2], k16_empty[2];
-    uint64_t q_full[NQ], q_empty[NQ];
+    uint64_t q_full[NQ], q_empty[NQ], lse_full[8], lse_empty[8];
     uint64_t s_full[2], s_free[2], drain;
     uint32_t tmem_base;
     int abort;
 };
+
+// First token and head of a row tile.
+__device__ __forceinline__ void row_tile_at(const WeightParams& wp, int rt, int& tok0, int& head0)
+{
+    const int block = wp.head_blocks == 1 ? rt : rt / wp.head_blocks;
+    tok0 = block * wp.tok_per;
+    head0 = (rt - block * wp.head_blocks) * wp.heads_per;
+}
 
 // A key tile of one KV head and the row tiles that see it.
 struct KeyUnit {
@@ -440,11 +453,12 @@ struct UnitFinder {
 };
 
 template <int D, bool kBF16>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(384, 1)
 weights_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q, const WeightParams wp)
 {
     using L = ManyLayout<D, kBF16>;
-    constexpr int NQ = L::kStagesQ;
+    constexpr int NQ = L::kStagesQ, NL = L::kStagesLse;
+    static_assert(NL == 8, "barriers");
     using Bars = ManyBarriers<NQ>;
     const paged::Params& p = wp.p;
     extern __shared__ uint8_t smem_raw[];
@@ -467,7 +481,11 @@ weights_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         }
         for (int i = 0; i < NQ; ++i) {
             mbar_init(smem_u32(&bars->q_full[i]), 1);
-            mbar_init(smem_u32(&bars->q_empty[i]), 128 + 1);   // the warpgroup has read the LSE, the product the tile
+            mbar_init(smem_u32(&bars->q_empty[i]), 1);
+        }
+        for (int i = 0; i < NL; ++i) {
+            mbar_init(smem_u32(&bars->lse_full[i]), 32);
+            mbar_init(smem_u32(&bars->lse_empty[i]), 128);
         }
         mbar_init(smem_u32(&bars->drain), 1);
         bars->abort = 0;
@@ -491,15 +509,37 @@ weights_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     UnitFinder finder;
     uint32_t units = 0, n = 0;                             // units and row tiles so far
     bool ok = true;
-    if (warp == 8) {
+    if (warp >= 8) {
+      regs_release<104>();
+      if (warp == 8) {
         // =========================== TMA producer ===========================
         const int ppt = kTileKeys >> p.page_shift;
         auto entry_of = [&](const KeyUnit& k) -> int {
             const int ord = k.tile * ppt + lane;
             return k.b >= 0 && lane < ppt && ord << p.page_shift < k.keys ? p.table[(long long)k.b * p.max_pages + ord] : -1;
         };
+        // this lane's four columns of a row tile: their tokens and heads in it
+        int tok[4], head[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int c = 4 * lane + e;
+            tok[e] = c < wp.tok_per * wp.heads_per ? c / wp.heads_per : 1 << 30;
+            head[e] = c % wp.heads_per;
+        }
+        // and their LSE, negative (read one row tile ahead: a read takes as long as a tile)
+        float z[4];
+        auto load_lse = [&](const KeyUnit& k, int rt) {
+            int tok0, head0;
+            row_tile_at(wp, rt, tok0, head0);
+            const float* at = wp.lse + ((long long)k.b * p.Hq + k.h * p.group + head0) * p.Sq + tok0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                z[e] = tok[e] < k.count - tok0 && head[e] < p.group - head0 ? at[(long long)head[e] * p.Sq + tok[e]] : -INFINITY;
+        };
         KeyUnit k = finder.find(wp, blockIdx.x);
         int entry = entry_of(k);
+        if (k.b >= 0)
+            load_lse(k, k.rt0);
         for (long long u = blockIdx.x; ok && k.b >= 0; u += gridDim.x, ++units) {
             const KeyUnit next = finder.find(wp, u + gridDim.x);
             const int id = (unsigned)entry < (unsigned)p.n_pages ? entry : -1;
@@ -518,23 +558,22 @@ weights_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 tma_load_4d(sK8 + st * L::kK8Bytes + lane * p.page * D, &tm_k, smem_u32(&bars->k8_full[st]), 0, k.h, 0, id);
             for (int rt = k.rt0; ok && rt < k.rt1; ++rt, ++n) {
                 const uint32_t qs = n % NQ;
-                const int tok0 = rt / wp.head_blocks * wp.tok_per, head0 = rt % wp.head_blocks * wp.heads_per;
-                // four rows' LSE a lane (before the wait, which they take their time in)
-                float z[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int c = 4 * lane + e, i = tok0 + c / wp.heads_per, hh = head0 + c % wp.heads_per;
-                    z[e] = c < wp.tok_per * wp.heads_per && i < k.count && hh < p.group
-                               ? row_lse2(wp.lse[((long long)k.b * p.Hq + k.h * p.group + hh) * p.Sq + i])
-                               : INFINITY;
-                }
+                int tok0, head0;
+                row_tile_at(wp, rt, tok0, head0);
+                const float4 lse = make_float4(-row_lse2(z[0]), -row_lse2(z[1]), -row_lse2(z[2]), -row_lse2(z[3]));
+                if (rt + 1 < k.rt1)
+                    load_lse(k, rt + 1);
+                else if (next.b >= 0)
+                    load_lse(next, next.rt0);
                 if (n >= NQ)
                     ok = wait_bar(smem_u32(&bars->q_empty[qs]), (n / NQ - 1) & 1, abort, kErrWeightsLoad + 2);
+                if (n >= NL)
+                    ok = ok && wait_bar(smem_u32(&bars->lse_empty[n % NL]), (n / NL - 1) & 1, abort, kErrWeightsLoad + 3);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok)
                     break;
-                reinterpret_cast<float4*>(smem + L::kOffLse + qs * 512)[lane] = make_float4(-z[0], -z[1], -z[2], -z[3]);
-                __syncwarp();
+                reinterpret_cast<float4*>(smem + L::kOffLse + n % NL * 512)[lane] = lse;
+                mbar_arrive(smem_u32(&bars->lse_full[n % NL]));
                 if (lane == 0) {
                     mbar_arrive_expect_tx(smem_u32(&bars->q_full[qs]), wp.tok_per * wp.heads_per * D * 2);
 #pragma unroll
@@ -555,7 +594,7 @@ weights_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 drain_wait(smem_u32(&bars->q_full[i % NQ]), (i / NQ) & 1);
         }
         __syncwarp();
-    } else if (warp == 9) {
+      } else if (warp == 9) {
         // ============================ MMA issuer ============================
         constexpr uint32_t idesc = idesc_make(kBF16 ? 1u : 0u, kTileKeys, 128, false);
         const uint32_t hi = (uint32_t)(smem_desc(0, 16, 1024, 2u) >> 32);
@@ -599,7 +638,9 @@ weights_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             drain_wait(smem_u32(&bars->drain), 0);
         }
         __syncwarp();
+      }
     } else {
+        regs_acquire<192>();
         // ========================= one thread a key =========================
         const int g = warp >> 2;
         const int tid = threadIdx.x & 127;
@@ -673,8 +714,8 @@ weights_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             for (int rt = k.rt0; ok && rt < k.rt1; ++rt, ++n) {
                 if ((n & 1) != g)
                     continue;
-                const uint32_t qs = n % NQ;
-                ok = wait_bar(smem_u32(&bars->q_full[qs]), (n / NQ) & 1, abort, kErrWeightsSum + 3) &&
+                // (q's own barrier may be two phases ahead of this thread)
+                ok = wait_bar(smem_u32(&bars->lse_full[n % NL]), (n / NL) & 1, abort, kErrWeightsSum + 3) &&
                      wait_bar(smem_u32(&bars->s_full[g]), ns & 1, abort, kErrWeightsSum + 4);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok)
@@ -682,40 +723,56 @@ weights_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 ++ns;
                 tc_fence_after_sync();
                 // columns that are rows, and of those the ones that see this key
-                const int tok0 = rt / wp.head_blocks * wp.tok_per, head0 = rt % wp.head_blocks * wp.heads_per;
+                int tok0, head0;
+                row_tile_at(wp, rt, tok0, head0);
                 const int rows = min(wp.tok_per, k.count - tok0) * (wp.head_blocks == 1 ? wp.heads_per : min(wp.heads_per, p.group - head0));
                 const long long late = p.causal ? (pos - k.start - tok0) * wp.heads_per : 0;
                 const int from = (int)max(0ll, min(late, 128ll));
                 const bool edge = rows < 128 || __any_sync(0xffffffffu, from > 0);
-                const float4* lse = reinterpret_cast<const float4*>(smem + L::kOffLse + qs * 512);
+                const float4* lse = reinterpret_cast<const float4*>(smem + L::kOffLse + n % NL * 512);
                 uint64_t acc0 = 0, acc1 = 0;
                 const uint64_t c2 = f32x2(c, c);
-#pragma unroll 1
-                for (int e0 = 0; e0 < rows; e0 += 32) {
-                    uint32_t s[32];
-                    tmem_ld32_wait(t_s + e0, s);
-                    if (e0 + 32 >= rows) {                                  // the last of the tile's scores
-                        tc_fence_before_sync();
-                        mbar_arrive(smem_u32(&bars->s_free[g]));
-                    }
-                    const uint32_t seen = bits_below(rows - e0) & ~bits_below(from - e0);
+                if (__builtin_expect(!edge, 1)) {
+                    // all scores at once, so that the next tile's may come
+                    uint32_t s[128];
+                    tmem_ld128_wait(t_s, t_s + 32, t_s + 64, t_s + 96, s);
+                    tc_fence_before_sync();
+                    mbar_arrive(smem_u32(&bars->s_free[g]));
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 z = lse[(e0 + e) / 4];
+                    for (int e = 0; e < 128; e += 4) {
+                        const float4 z = lse[e / 4];
                         float x0, x1, x2, x3;
                         f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, f32x2(z.x, z.y)), x0, x1);
                         f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, f32x2(z.z, z.w)), x2, x3);
-                        if (edge) {
+                        acc0 = add_f32x2(acc0, f32x2(ex2_approx(x0), ex2_approx(x1)));
+                        acc1 = add_f32x2(acc1, f32x2(ex2_approx(x2), ex2_approx(x3)));
+                    }
+                } else {
+#pragma unroll 1
+                    for (int e0 = 0; e0 < rows; e0 += 32) {
+                        uint32_t s[32];
+                        tmem_ld32_wait(t_s + e0, s);
+                        if (e0 + 32 >= rows) {                              // the last of the tile's scores
+                            tc_fence_before_sync();
+                            mbar_arrive(smem_u32(&bars->s_free[g]));
+                        }
+                        const uint32_t seen = bits_below(rows - e0) & ~bits_below(from - e0);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 z = lse[(e0 + e) / 4];
+                            float x0, x1, x2, x3;
+                            f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, f32x2(z.x, z.y)), x0, x1);
+                            f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, f32x2(z.z, z.w)), x2, x3);
                             x0 = seen >> e & 1 ? x0 : -INFINITY;
                             x1 = seen >> (e + 1) & 1 ? x1 : -INFINITY;
                             x2 = seen >> (e + 2) & 1 ? x2 : -INFINITY;
                             x3 = seen >> (e + 3) & 1 ? x3 : -INFINITY;
+                            acc0 = add_f32x2(acc0, f32x2(ex2_approx(x0), ex2_approx(x1)));
+                            acc1 = add_f32x2(acc1, f32x2(ex2_approx(x2), ex2_approx(x3)));
                         }
-                        acc0 = add_f32x2(acc0, f32x2(ex2_approx(x0), ex2_approx(x1)));
-                        acc1 = add_f32x2(acc1, f32x2(ex2_approx(x2), ex2_approx(x3)));
                     }
                 }
-                mbar_arrive(smem_u32(&bars->q_empty[qs]));
+                mbar_arrive(smem_u32(&bars->lse_empty[n % NL]));
                 float a, b;
                 f32x2_split(add_f32x2(acc0, acc1), a, b);
                 sum += a + b;
