@@ -588,8 +588,8 @@ int sdpa_last_cuda_error(void);
  * softmax gave up; 0x4xx / 0x5xx = a bounded wait of the 16-bit / FP8
  * backward pass gave up; 0x601 / 0x602 / 0x701 = an index that a call was
  * given in device memory is out of range, see sdpa_cache_append; 0x8xx = a
- * bounded wait of the attention over a paged cache gave up).  Synchronises
- * the device.  Returns SDPA_OK or
+ * bounded wait of the attention over a paged cache, or of sdpa_cache_weights,
+ * gave up).  Synchronises the device.  Returns SDPA_OK or
  * SDPA_ERR_CUDA; `code` (host pointer) receives the word.
  */
 sdpa_status_t sdpa_device_error(unsigned int *code);

@@ -208,7 +208,29 @@ def test_evict(gpu, case):  # noqa: F811
 
 
 @pytest.mark.gpu
-def test_evict_more_than_the_registers_hold(gpu):  # noqa: F811
+@pytest.mark.parametrize("n", [401, 402, 403])
+def test_evict_rows_of_any_length(gpu, n):  # noqa: F811
+    """Rows of scores that begin on any multiple of four bytes."""
+    import scaled_dot_product_05_gb300 as lib
+    length, budget = [n, n - 1, 77], 100
+    cache = make_cache(3 * 26 + 3 * 7, 16, 3, 64, "heads", 2)
+    ids = torch.randperm(cache.n_pages, generator=torch.Generator().manual_seed(3)).to(torch.int32)
+    table, new_table = ids[:78].reshape(3, 26), ids[78:].reshape(3, 7)
+    score = scores("ties", (3, 3, n), 5)
+    before = PlainCache(cache)
+    kept = torch.full((3, 3, budget), -9, dtype=torch.int32, device=DEV)
+    kept_score = torch.full((3, 3, budget), -9.0, device=DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    args = (cache, table.to(DEV), i32(length), score.to(DEV), new_table.to(DEV))
+    torch.cuda.synchronize()
+    lib.sdpa_cache_evict(*args, budget=budget, sinks=1, recent=2, kept=kept, kept_score=kept_score, stream=s)
+    s.synchronize()
+    check_evict(cache, before, table, new_table, length, score, kept, kept_score, budget, 1, 2, -9)
+
+
+@pytest.mark.gpu
+def test_evict_more_than_shared_memory_holds(gpu):  # noqa: F811
     """Scores of 300 000 tokens (eight CTAs hold 262 144)."""
     import scaled_dot_product_05_gb300 as lib
     n, page, budget = 300000, 128, 1000
