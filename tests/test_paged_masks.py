@@ -317,3 +317,48 @@ def test_refusals(gpu):  # noqa: F811
                 torch.zeros((1, 3, 1), dtype=torch.int32)):
         with pytest.raises(ValueError):
             lib.sdpa_fwd_paged_tree(*args, bad)
+
+
+# ------------------------------------------- 17 to 64 rows, and calls with none --
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("case", [
+    (16, 17, 1, 128, 1, "bf16", "heads"), (64, 8, 2, 64, 5, "fp16", "tokens"), (32, 32, 2, 128, 4, "bf16", "pairs"),
+    (128, 4, 4, 64, 33, "bf16", "heads"), (16, 12, 4, 128, 21, "fp16", "heads")], ids=str)
+def test_plain_attention_of_some_rows(gpu, case, causal):  # noqa: F811
+    """The attention without a mask of its own, where its rows stand in the lanes twice."""
+    from tests.test_paged_cache import check as check_plain, launch, read_case
+    page, Hq, Hkv, D, Sq, dt, layout = case
+    start, count = [0, 126, 1000, 3, 64, 2500], [Sq, Sq, max(1, Sq - 1), 1, 0, Sq]
+    full = (page, Hq, Hkv, D, Sq, dt, layout, causal, start, count, None)
+    cache, table, q = read_case(full)
+    o, lse = launch(full, cache, table, q)
+    check_plain(full, cache, table, q, o, lse, fill=7.0)
+    # a NaN value of the last token stays out of the rows that do not see it
+    if causal and Sq > 1:
+        for b in (1, 5):
+            pos = start[b] + Sq - 1
+            cache.v.view(torch.uint8)[table[b, pos // page].long(), pos % page, 0, 5] = 0x7F
+        o2, lse2 = launch(full, cache, table, q)
+        want = torch.zeros_like(o, dtype=torch.bool)
+        for b in (1, 5):
+            want[b, Sq - 1, :Hq // Hkv, 5] = True
+        assert torch.equal(o2.isnan(), want) and torch.equal(o2[~want], o[~want]) and torch.equal(lse2, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Sq", [1, 4, 12, 40])
+def test_no_rows_at_all(gpu, Sq):  # noqa: F811
+    """Counts of zero everywhere: nothing is written."""
+    import scaled_dot_product_05_gb300 as lib
+    cache, table, q = case_data(16, 8, 2, 64, Sq, "bf16", "heads", [30, 0, 500])
+    o, lse = outputs(q)
+    args = (q.to(DEV), cache, table.to(DEV), i32([30, 0, 500]))
+    none = i32([0, 0, 0])
+    lib.sdpa_fwd_paged_window(*args, none, o, lse, window=20, sinks=1)
+    lib.sdpa_fwd_paged_tree(*args, torch.zeros((3, Sq, (Sq + 31) // 32), dtype=torch.int32, device=DEV), none, o, lse)
+    out = torch.full((3, 2, table.shape[1] * 16), FILL, device=DEV)
+    lib.sdpa_cache_weights(*args, none, lse, None, out)
+    assert lib.sdpa_device_error() == 0
+    assert (o == FILL).all() and (lse == FILL).all() and (out == FILL).all()
