@@ -895,7 +895,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (edge) {
                     ok = ok && wait_bar(smem_u32(&bars->v_full[vn % NV]), (vn / NV) & 1, abort, kErrPagedSoftmax + 2);
                     const uint32_t row = sV + (vn % NV) * L::kTileBytes + tid * D;
-                    if (ok && !valid) {
+                    if (ok && (kMasked ? seen_rows == 0 : !valid)) {
 #pragma unroll
                         for (int c = 0; c < D / 16; ++c)
                             st_shared_v4(row + c * 16, 0u, 0u, 0u, 0u);
