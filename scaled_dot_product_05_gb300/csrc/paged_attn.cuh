@@ -11,6 +11,17 @@
 // is outside the page table, are left out and reported in the device error
 // word; no address is formed from such an index.
 //
+// Two masks of their own (MASK): with a window a token sees the last `window`
+// positions up to its own and the first `sinks`; of a tree of drafts it sees
+// what was there before and the new tokens that its bits name.  With a window
+// the tiles hold the pages of the first tokens and those of the window side by
+// side; other pages are neither looked up nor read.  Only tiles on an edge look
+// at what each row sees; there a key that no row sees has its V zeroed, and a
+// NaN in V that some rows see is taken out and noted with those rows, a bit each.
+// Measured (D = 128, 32 query heads on 8, bf16): 64 sequences of up to 16384 keys
+// with a window of 4096 101 - 107 us (552 MB, 5.2 - 5.5 TB/s), one of 1500 keys with
+// a window of 512 9.6 us (12.8 us while masked values were looked at for NaN).
+//
 // The codes go to the FP8 tensor cores as they lie in the cache, and the
 // 16-bit operands are split instead into 8-bit parts that add up to them; the
 // products of 8-bit values are exact in the fp32 accumulator.  q, divided by a

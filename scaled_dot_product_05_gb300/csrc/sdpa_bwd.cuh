@@ -41,6 +41,10 @@
 //                  tile's Q and dO (128 x D fp32 is exactly their size), for
 //                  the reducer (every key tile of a query row contributes to
 //                  its dQ)
+// With a window (kWin) a key tile meets the query tiles from its own to the last
+// one whose window reaches it, that of the first keys all behind it; B = 2, S =
+// 4096, 32 query heads on 8 of 128, bf16, a window of 1024: 378 us (445 with Delta
+// and the conversion), 3.3 us a query tile, as in the causal pass.
 // A preprocessing kernel forms Delta, a final one converts the fp32 dQ
 // (both in sdpa_bwd_prep.cuh).
 #pragma once

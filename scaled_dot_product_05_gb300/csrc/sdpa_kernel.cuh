@@ -38,7 +38,10 @@
 // hq / (Hq / Hkv) (section 9, "Compare MHA, GQA and MQA"); nothing is
 // replicated.  Causal masking keeps the lower triangle (section 7, "Add causal
 // masking"): row i sees keys 0..i; key tiles wholly above the diagonal are
-// skipped.
+// skipped.  With a window (kWin) row i sees keys i - window + 1 .. i and the first
+// `sinks`: the tiles between those are skipped as well.  Measured (B = 2, S = 8192,
+// 32 query heads on 8 of 128, bf16, a window of 1024, 4 first keys): 241 us, 1070
+// TFLOP/s of what the rows see, 1230 of the tiles multiplied.
 #pragma once
 
 #include <cfloat>
